@@ -342,6 +342,105 @@ int moe_decode_run_noalloc(const moe_weights_t* weights, const moe_run_opts_t* o
 int moe_combine(const void* rows_dev, size_t rows_bytes, const float* weights_dev, int32_t B, int32_t topk,
                 int32_t D, void* out_dev, size_t out_bytes, void* stream);
 
+/* -------------------------------------------------------- dense side ---- */
+/* What stands in front of the routed experts (the router: moe_gate, moe_route) and beside
+ * them (a shared expert in 8-bit integers: moe_quant_i8, moe_linear_i8).  Rows are
+ * contiguous within themselves; ld* is the distance between rows in elements.  Offsets are
+ * 64 bits wide.  No workspace, no state: calls on any streams may overlap.  Inputs are not
+ * modified; outputs must not overlap inputs unless said otherwise.  At most 2^22 tokens (B, M)
+ * a call. */
+
+enum moe_dtype { MOE_BF16 = 0, MOE_F16 = 1, MOE_F32 = 2 };
+
+/* Bytes of the router weight [E, D] laid out by moe_gate_pack.  wtype MOE_BF16: one BF16
+ * plane; MOE_F32: three, the weight's upper, middle and lower eight mantissa bits, whose
+ * sum is the FP32 weight.  E is padded to a multiple of 16.  0 on invalid sizes (1 <= E <=
+ * 1024, 512 <= D <= 16384 with D % 512 == 0, as the experts). */
+size_t moe_gate_packed_bytes(int32_t E, int32_t D, int32_t wtype);
+
+/* One-time re-layout of a router weight, row-major [E, D] of wtype, into the order
+ * moe_gate reads: per 16 experts and 32 features, one contiguous 1 KB run of the matrix
+ * instruction's operand, its planes one after another.  Weights below 2^-100 in magnitude lose
+ * mantissa bits under 2^-133.  MOE_ENOSPACE if packed_bytes < moe_gate_packed_bytes. */
+int moe_gate_pack(const void* w_dev, int32_t wtype, int32_t E, int32_t D, void* packed_dev,
+                  size_t packed_bytes, void* stream);
+
+/* A packed router weight. */
+typedef struct {
+  int32_t E, D, wtype;
+  const void* packed; /* from moe_gate_pack */
+} moe_gate_t;
+
+/* Router product: logits[t, e] = sum over d of x[t, d] * w[e, d], FP32 sums of exact
+ * products, in a fixed order.  x_dev BF16 [B, D], ldx >= D and a multiple of 8, x_dev
+ * 16-byte aligned; logits_dev FP32 [B, E], ldl >= E.   The logits of a token
+ * with an infinite or NaN feature are not finite (with an FP32 weight: NaN).
+ * MOE_EINVAL for a null pointer, size, stride or alignment outside these. */
+int moe_gate(const moe_gate_t* gate, const void* x_dev, int64_t ldx, int32_t B, float* logits_dev,
+             int64_t ldl, void* stream);
+
+/* Options of moe_route (zero-initialise for the defaults). */
+typedef struct {
+  int32_t score;       /* 0 = softmax over the E logits, 1 = sigmoid of each */
+  int32_t groups;      /* 0 = none; else E / groups consecutive experts form a group (E %
+                          groups == 0, groups <= 64) */
+  int32_t topk_groups; /* groups kept (1..groups; 0 without groups) */
+  int32_t group_score; /* a group ranks by its 0 = largest choice, 1 = two largest, summed */
+  int32_t renorm;      /* 1: the weights of a token are divided by their sum */
+  float scale;         /* factor of the weights; 0 = 1 */
+  const float* bias_dev; /* optional FP32 [E]: added to the scores for the choice only */
+  int32_t reserved[2];
+} moe_route_opts_t;
+
+/* Routing: logits [B, E] (moe_dtype, ldl >= E) -> ids_dev i32 [B, topk] and weights_dev FP32
+ * [B, topk], what moe_group / moe_decode_run and moe_combine take.
+ *   choice[e] = score[e] + bias[e], or the logit itself without a bias (the score grows
+ *   with it); with groups, only the topk_groups best groups take part (group_score 1
+ *   without a bias sums scores); ids = the topk largest choices, largest first;
+ *   weight = score (renorm: / sum of the selected scores, 0 where that is 0) * scale.
+ * Choices are compared in FP64 and ties go to the lowest index (of groups too), so ids do
+ * not depend on rounding.  ids are always valid and distinct within a token: a logit of
+ * -inf or NaN masks its expert (score 0, choice -inf; it is selected, lowest index first,
+ * only when the others run out, with weight 0), and so does a NaN choice; logits of +inf
+ * share a softmax's weight equally.  Weights are computed in FP64 and rounded once.
+ * 1 <= E <= 1024, 1 <= topk <= 64, topk <= E (with groups: <= topk_groups * E / groups),
+ * MOE_EINVAL otherwise. */
+int moe_route(const void* logits_dev, int32_t type, int64_t ldl, int32_t B, int32_t E, int32_t topk,
+              const moe_route_opts_t* opts, int32_t* ids_dev, float* weights_dev, void* stream);
+
+/* Symmetric int8 quantization with one scale for each token: x [M, K] (moe_dtype, ldx >= K)
+ * -> codes_dev int8 [M, K] (ldc >= K), scales_dev FP32 [M]:
+ *   scale = amax / 127 (FP32), code = x * 127 / amax, rounded half to even from the exact
+ *   quotient, within +-127.  A row of zeros has scale 0 and codes 0; a row with an
+ *   infinity or NaN has scale NaN and codes 0, so that what is computed from it is NaN.
+ * Bytes of codes_dev between K and ldc are left as they were.  1 <= K <= 131072. */
+int moe_quant_i8(const void* x_dev, int32_t type, int64_t ldx, int32_t M, int32_t K, int8_t* codes_dev,
+                 int64_t ldc, float* scales_dev, void* stream);
+
+/* Options of moe_linear_i8 (zero-initialise for the defaults). */
+typedef struct {
+  int32_t act;           /* 0 = none; 1 = SwiGLU: rows 0..N/2-1 of w are the gate, N/2..N-1 up
+                            (N even), and out has N/2 columns */
+  int32_t reserved;
+  const float* bias_dev; /* optional FP32 [N], before the activation */
+  const void* add_dev;   /* optional [M, columns of out], out's type, added last; may be out_dev
+                            itself with ldadd == ldo */
+  int64_t ldadd;
+} moe_linear_opts_t;
+
+/* Int8 product with scales for each token and channel:
+ *   y[m, n] = (sum over k of a[m, k] * w[n, k]) * a_scales[m] * w_scales[n] + bias[n]
+ *   act 1: y[m, n] = silu(y[m, n]) * y[m, N/2 + n];   out = y + add, rounded once
+ * The sum is exact (32-bit integers), the rest is FP32.  a_dev int8 [M, K] (lda >= K), w_dev
+ * int8 [N, K] (ldw >= K), out_dev [M, N or N/2] of out_type (ldo).  All 256 codes are taken
+ * at their value.  Rows whose start is 16-byte aligned with K % 16 == 0 (a_dev, w_dev,
+ * lda, ldw) are read the fast way.  1 <= N <= 2^20, M * N <= 2^34, 1 <= K <=
+ * 131071 (the sum's range), lda and ldw < 2^22; MOE_EINVAL otherwise. */
+int moe_linear_i8(const int8_t* a_dev, int64_t lda, const float* a_scales_dev, const int8_t* w_dev,
+                  int64_t ldw, const float* w_scales_dev, int32_t M, int32_t N, int32_t K,
+                  const moe_linear_opts_t* opts, void* out_dev, int32_t out_type, int64_t ldo,
+                  void* stream);
+
 #ifdef __cplusplus
 }
 #endif

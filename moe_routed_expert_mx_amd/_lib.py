@@ -42,6 +42,21 @@ class moe_run_opts_t(ctypes.Structure):
                 ("ahead", ctypes.c_void_p), ("ahead_rows", ctypes.c_int32)]
 
 
+class moe_gate_t(ctypes.Structure):
+    _fields_ = [("E", ctypes.c_int32), ("D", ctypes.c_int32), ("wtype", ctypes.c_int32), ("packed", ctypes.c_void_p)]
+
+
+class moe_route_opts_t(ctypes.Structure):
+    _fields_ = [("score", ctypes.c_int32), ("groups", ctypes.c_int32), ("topk_groups", ctypes.c_int32),
+                ("group_score", ctypes.c_int32), ("renorm", ctypes.c_int32), ("scale", ctypes.c_float),
+                ("bias_dev", ctypes.c_void_p), ("reserved", ctypes.c_int32 * 2)]
+
+
+class moe_linear_opts_t(ctypes.Structure):
+    _fields_ = [("act", ctypes.c_int32), ("reserved", ctypes.c_int32), ("bias_dev", ctypes.c_void_p),
+                ("add_dev", ctypes.c_void_p), ("ldadd", ctypes.c_int64)]
+
+
 class moe_prefetch_row_t(ctypes.Structure):
     _fields_ = [("addr", ctypes.c_void_p), ("bytes", ctypes.c_uint64)]
 
@@ -85,6 +100,14 @@ def _load():
         "moe_decode_run_noalloc": (c.c_int, [c.POINTER(moe_weights_t), c.POINTER(moe_run_opts_t), P, P, c.c_int32,
                                              c.c_int32, P, c.c_size_t, P]),
         "moe_combine": (c.c_int, [P, c.c_size_t, P, c.c_int32, c.c_int32, c.c_int32, P, c.c_size_t, P]),
+        "moe_gate_packed_bytes": (c.c_size_t, [c.c_int32] * 3),
+        "moe_gate_pack": (c.c_int, [P, c.c_int32, c.c_int32, c.c_int32, P, c.c_size_t, P]),
+        "moe_gate": (c.c_int, [c.POINTER(moe_gate_t), P, c.c_int64, c.c_int32, P, c.c_int64, P]),
+        "moe_route": (c.c_int, [P, c.c_int32, c.c_int64, c.c_int32, c.c_int32, c.c_int32,
+                                c.POINTER(moe_route_opts_t), P, P, P]),
+        "moe_quant_i8": (c.c_int, [P, c.c_int32, c.c_int64, c.c_int32, c.c_int32, P, c.c_int64, P, P]),
+        "moe_linear_i8": (c.c_int, [P, c.c_int64, P, P, c.c_int64, P, c.c_int32, c.c_int32, c.c_int32,
+                                    c.POINTER(moe_linear_opts_t), P, c.c_int32, c.c_int64, P]),
         "moe_work_split": (c.c_int, [c.c_int32] * 6 + [P, P]),
         "moe_grouped_runs": (c.c_int, [c.c_int32, P, c.c_int32, c.c_int32, c.c_int32, P]),
     }
@@ -98,7 +121,8 @@ lib = _load()
 EXPORTED = ("moe_status_string", "moe_plan_bytes", "moe_units_bytes", "moe_workspace_bytes", "moe_packed_weight_bytes",
             "moe_pack_weights", "moe_workspace_init", "moe_plan", "moe_group", "moe_plan_group", "moe_units_export",
             "moe_experts_run", "moe_decode_run", "moe_decode_run_noalloc", "moe_combine", "moe_work_split",
-            "moe_grouped_runs")
+            "moe_grouped_runs", "moe_gate_packed_bytes", "moe_gate_pack", "moe_gate", "moe_route", "moe_quant_i8",
+            "moe_linear_i8")
 
 
 def status_string(status: int) -> str:
@@ -251,3 +275,149 @@ def moe_combine(rows, weights, out, stream=None):
     D = rows.shape[-1]
     _check("moe_combine", lib.moe_combine(_ptr(rows), _nbytes(rows), _ptr(weights), B, K, D, _ptr(out), _nbytes(out),
                                           _stream(stream)))
+
+
+# --------------------------------------------------------------- dense side
+# These entry points check their tensors (the library sees pointers only): types, shapes,
+# unit stride within rows and one GPU for all of them raise ValueError.  They run on that
+# GPU's current stream, whichever GPU is current.
+_MOE_TYPE = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
+
+
+def _need(ok: bool, what: str):
+    if not ok:
+        raise ValueError(what)
+
+
+def _rows(t, name: str, dtype=None):
+    """Row distance of a [rows, columns] tensor whose rows are contiguous."""
+    _need(t.dim() == 2, f"{name}: expected two dimensions, got {t.dim()}")
+    _need(t.dtype == dtype if dtype is not None else t.dtype in _MOE_TYPE, f"{name}: type {t.dtype} not taken")
+    cols = t.shape[1]
+    ld, inner = t.stride()
+    _need(inner == 1 or cols == 1, f"{name}: the elements of a row must be contiguous")
+    if t.shape[0] == 1:
+        return max(cols, 1)
+    _need(ld >= cols, f"{name}: rows overlap (stride {ld}, {cols} columns)")
+    return ld
+
+
+def _vector(t, name: str, n: int, dtype=torch.float32):
+    _need(t.dtype == dtype and t.dim() == 1 and t.shape[0] == n, f"{name}: expected {dtype} [{n}]")
+    _need(n == 1 or t.stride(0) == 1, f"{name}: must be contiguous")
+    return t.data_ptr()
+
+
+def _on(stream, first, *others):
+    """(device guard or None, raw stream) of a call on `first`'s GPU."""
+    dev = first.device
+    _need(dev.type == "cuda", "the tensors must be on a GPU")
+    for t in others:
+        _need(t is None or t.device == dev, "the tensors must be on one GPU")
+    if stream is None:
+        raw = torch.cuda.current_stream(dev).cuda_stream
+    elif hasattr(stream, "cuda_stream"):
+        _need(stream.device == dev, "the stream belongs to another GPU than the tensors")
+        raw = stream.cuda_stream
+    else:
+        raw = int(stream)
+    return (None if torch.cuda.current_device() == dev.index else torch.cuda.device(dev)), raw
+
+
+def _enqueue(name: str, guard, *args):
+    if guard is None:
+        status = getattr(lib, name)(*args)
+    else:
+        with guard:
+            status = getattr(lib, name)(*args)
+    _check(name, status)
+
+
+def moe_gate_packed_bytes(E: int, D: int, wdtype=torch.bfloat16) -> int:
+    """Bytes of a packed router weight [E, D] of wdtype (BF16 or FP32); 0 if not supported."""
+    return lib.moe_gate_packed_bytes(E, D, _MOE_TYPE.get(wdtype, -1))
+
+
+def moe_gate_pack(w, packed, stream=None) -> moe_gate_t:
+    """Lay a router weight (BF16 or FP32 [E, D], contiguous) out into `packed` (uint8, moe_gate_packed_bytes)
+    and return its handle for moe_gate.  The caller keeps `packed` alive."""
+    _need(w.dim() == 2 and w.dtype in (torch.bfloat16, torch.float32) and w.is_contiguous(),
+          "w: expected contiguous BF16 or FP32 [E, D]")
+    _need(packed.dtype == torch.uint8 and packed.is_contiguous(), "packed: expected contiguous uint8")
+    E, D = w.shape
+    guard, st = _on(stream, w, packed)
+    _enqueue("moe_gate_pack", guard, w.data_ptr(), _MOE_TYPE[w.dtype], E, D, packed.data_ptr(), packed.numel(), st)
+    return moe_gate_t(E, D, _MOE_TYPE[w.dtype], packed.data_ptr())
+
+
+def moe_gate(gate: moe_gate_t, x, logits, stream=None):
+    """Router product: x BF16 [B, D] (rows may be strided) -> logits FP32 [B, E]."""
+    ldx, ldl = _rows(x, "x", torch.bfloat16), _rows(logits, "logits", torch.float32)
+    B = x.shape[0]
+    _need(x.shape[1] == gate.D, f"x: expected {gate.D} features")
+    _need(logits.shape == (B, gate.E), f"logits: expected [{B}, {gate.E}]")
+    guard, st = _on(stream, x, logits)
+    _enqueue("moe_gate", guard, ctypes.byref(gate), x.data_ptr(), ldx, B, logits.data_ptr(), ldl, st)
+
+
+_SCORES = {"softmax": 0, "sigmoid": 1}
+_GROUP_SCORES = {"max": 0, "top2": 1}
+
+
+def moe_route(logits, ids, weights, *, score: str = "softmax", bias=None, groups: int = 0, topk_groups: int = 0,
+              group_score: str = "max", renorm: bool = True, scale: float = 1.0, stream=None):
+    """Routing: logits [B, E] (FP32, BF16 or FP16) -> ids int32 [B, topk] and weights FP32 [B, topk], the experts of
+    the largest choice (score + bias) first, as the expert calls and moe_combine take them.  score "softmax" or
+    "sigmoid"; groups experts groups of which topk_groups stay, ranked by group_score "max" or "top2"; renorm
+    divides a token's weights by their sum; scale multiplies them."""
+    ldl = _rows(logits, "logits")
+    B, E = logits.shape
+    _need(score in _SCORES, f"unknown score {score!r}")
+    _need(group_score in _GROUP_SCORES, f"unknown group_score {group_score!r}")
+    _need(ids.dim() == 2 and ids.shape[0] == B and ids.dtype == torch.int32 and ids.is_contiguous(),
+          f"ids: expected contiguous int32 [{B}, topk]")
+    K = ids.shape[1]
+    _need(weights.shape == ids.shape and weights.dtype == torch.float32 and weights.is_contiguous(),
+          f"weights: expected contiguous FP32 [{B}, {K}]")
+    _need(scale != 0.0, "scale must not be 0")
+    opts = moe_route_opts_t(_SCORES[score], groups, topk_groups, _GROUP_SCORES[group_score], bool(renorm), scale,
+                            None if bias is None else _vector(bias, "bias", E))
+    guard, st = _on(stream, logits, ids, weights, bias)
+    _enqueue("moe_route", guard, logits.data_ptr(), _MOE_TYPE[logits.dtype], ldl, B, E, K, ctypes.byref(opts),
+             ids.data_ptr(), weights.data_ptr(), st)
+
+
+def moe_quant_i8(x, codes, scales, stream=None):
+    """Int8 quantization with one scale for each token: x [M, K] (FP32, BF16 or FP16) -> codes int8 [M, K], scales
+    FP32 [M]; code * scale stands for x."""
+    ldx, ldc = _rows(x, "x"), _rows(codes, "codes", torch.int8)
+    M, K = x.shape
+    _need(codes.shape == x.shape, f"codes: expected [{M}, {K}]")
+    ps = _vector(scales, "scales", M)
+    guard, st = _on(stream, x, codes, scales)
+    _enqueue("moe_quant_i8", guard, x.data_ptr(), _MOE_TYPE[x.dtype], ldx, M, K, codes.data_ptr(), ldc, ps, st)
+
+
+_ACTS = {"none": 0, "swiglu": 1}
+
+
+def moe_linear_i8(a, a_scales, w, w_scales, out, *, act: str = "none", bias=None, add=None, stream=None):
+    """Int8 product with scales for each token and channel: a int8 [M, K], w int8 [N, K] -> out [M, N] (FP32, BF16 or
+    FP16), y = (a . w) * a_scales * w_scales + bias (FP32 [N]); act "swiglu": the first N/2 rows of w are the gate,
+    the others up, and out is [M, N/2]; add (as out, may be out itself) is added last."""
+    _need(act in _ACTS, f"unknown act {act!r}")
+    lda, ldw, ldo = _rows(a, "a", torch.int8), _rows(w, "w", torch.int8), _rows(out, "out")
+    (M, K), N = a.shape, w.shape[0]
+    _need(w.shape[1] == K, f"w: expected {K} columns")
+    _need(act != "swiglu" or N % 2 == 0, "w: SwiGLU needs an even number of rows")
+    cols = N // 2 if act == "swiglu" else N
+    _need(out.shape == (M, cols), f"out: expected [{M}, {cols}]")
+    opts = moe_linear_opts_t(_ACTS[act], 0, None if bias is None else _vector(bias, "bias", N))
+    if add is not None:
+        opts.ldadd = _rows(add, "add", out.dtype)
+        _need(add.shape == out.shape, f"add: expected [{M}, {cols}]")
+        opts.add_dev = add.data_ptr()
+    psa, psw = _vector(a_scales, "a_scales", M), _vector(w_scales, "w_scales", N)
+    guard, st = _on(stream, a, a_scales, w, w_scales, out, bias, add)
+    _enqueue("moe_linear_i8", guard, a.data_ptr(), lda, psa, w.data_ptr(), ldw, psw, M, N, K, ctypes.byref(opts),
+             out.data_ptr(), _MOE_TYPE[out.dtype], ldo, st)

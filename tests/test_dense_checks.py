@@ -1,0 +1,137 @@
+"""Refusals of the dense side's entry points: in the library (before any HIP call, with
+pointers that are never dereferenced) and in the binding (on CPU tensors).  No GPU needed."""
+import ctypes
+
+import pytest
+import torch
+
+import moe_routed_expert_mx_amd as m
+
+L, EINVAL, ENOSPACE = m._lib.lib, m._lib.MOE_EINVAL, m._lib.MOE_ENOSPACE
+FAKE = ctypes.c_void_p(0x1000)
+BF, F16, F32 = torch.bfloat16, torch.float16, torch.float32
+
+
+def test_gate_sizes_and_refusals():
+    assert m.moe_gate_packed_bytes(160, 3584, BF) == 160 * 3584 * 2
+    assert m.moe_gate_packed_bytes(161, 512, F32) == 176 * 512 * 6
+    for e, d, t in ((0, 512, BF), (1025, 512, BF), (8, 500, BF), (8, 0, BF), (8, 16896, BF), (8, 512, F16)):
+        assert m.moe_gate_packed_bytes(e, d, t) == 0
+    big = 1 << 30
+    assert L.moe_gate_pack(None, 0, 16, 512, FAKE, big, None) == EINVAL
+    assert L.moe_gate_pack(FAKE, 1, 16, 512, FAKE, big, None) == EINVAL
+    assert L.moe_gate_pack(FAKE, 0, 16, 512, FAKE, 16 * 512 * 2 - 1, None) == ENOSPACE
+
+    def gate(E=16, D=512, wtype=0, packed=0x1000, x=FAKE, ldx=512, B=1, out=FAKE, ldl=16):
+        g = m.moe_gate_t(E, D, wtype, packed)
+        return L.moe_gate(ctypes.byref(g), x, ldx, B, out, ldl, None)
+
+    for bad in (dict(packed=0), dict(x=None), dict(out=None), dict(B=0), dict(B=-1), dict(B=(1 << 22) + 1),
+                dict(ldx=511), dict(ldx=516), dict(ldl=15), dict(E=0), dict(D=100), dict(wtype=1),
+                dict(x=ctypes.c_void_p(0x1008)), dict(packed=0x1002)):
+        assert gate(**bad) == EINVAL, bad
+    assert L.moe_gate(None, FAKE, 512, 1, FAKE, 16, None) == EINVAL
+
+
+def test_route_refusals():
+    def route(logits=FAKE, type=2, ldl=16, B=1, E=16, topk=4, ids=FAKE, w=FAKE, **o):
+        opts = m.moe_route_opts_t(**o)
+        return L.moe_route(logits, type, ldl, B, E, topk, ctypes.byref(opts), ids, w, None)
+
+    for bad in (dict(logits=None), dict(ids=None), dict(w=None), dict(type=3), dict(type=-1), dict(ldl=15), dict(B=0),
+                dict(B=(1 << 22) + 1), dict(E=0), dict(E=1025, ldl=1025), dict(topk=0), dict(topk=17),
+                dict(E=128, ldl=128, topk=65), dict(score=2), dict(score=-1), dict(renorm=2),
+                dict(scale=float("nan")), dict(scale=float("inf")), dict(groups=-1), dict(groups=3, topk_groups=1),
+                dict(groups=4), dict(groups=4, topk_groups=5), dict(topk_groups=1),
+                dict(groups=8, topk_groups=1), dict(groups=4, topk_groups=2, group_score=2), dict(group_score=-1),
+                dict(E=130, ldl=130, groups=65, topk_groups=65)):
+        assert route(**bad) == EINVAL, bad
+
+
+def test_quant_refusals():
+    def quant(x=FAKE, type=0, ldx=8, M=1, K=8, q=FAKE, ldc=8, s=FAKE):
+        return L.moe_quant_i8(x, type, ldx, M, K, q, ldc, s, None)
+
+    for bad in (dict(x=None), dict(q=None), dict(s=None), dict(type=3), dict(ldx=7), dict(ldc=7), dict(M=0),
+                dict(M=(1 << 22) + 1), dict(K=0), dict(K=131073, ldx=131073, ldc=131073)):
+        assert quant(**bad) == EINVAL, bad
+
+
+def test_linear_refusals():
+    def linear(a=FAKE, lda=16, sa=FAKE, w=FAKE, ldw=16, sw=FAKE, M=1, N=8, K=16, out=FAKE, type=0, ldo=8, **o):
+        opts = m.moe_linear_opts_t(**o)
+        return L.moe_linear_i8(a, lda, sa, w, ldw, sw, M, N, K, ctypes.byref(opts), out, type, ldo, None)
+
+    for bad in (dict(a=None), dict(sa=None), dict(w=None), dict(sw=None), dict(out=None), dict(type=3), dict(lda=15),
+                dict(ldw=15), dict(lda=1 << 22), dict(ldw=1 << 22), dict(M=0), dict(N=0), dict(K=0),
+                dict(K=131072, lda=131072, ldw=131072), dict(ldo=7), dict(act=2), dict(act=-1),
+                dict(act=1, N=9, ldo=9), dict(act=1, ldo=3), dict(add_dev=0x1000, ldadd=7),
+                dict(M=(1 << 22) + 1), dict(N=(1 << 20) + 1, ldo=1 << 21), dict(M=1 << 22, N=1 << 20, ldo=1 << 20)):
+        assert linear(**bad) == EINVAL, bad
+
+
+def _z(*shape, dtype=F32):
+    return torch.zeros(*shape, dtype=dtype)
+
+
+def test_binding_checks_tensors():
+    """Shapes, types, strides and devices are refused with ValueError; the last check is
+    the device, so a call that is right but for it names the GPU."""
+    x, lg, ids, w = _z(4, 512, dtype=BF), _z(4, 16), _z(4, 2, dtype=torch.int32), _z(4, 2)
+    g = m.moe_gate_t(16, 512, 0, 0x1000)
+    i8 = torch.int8
+    a, sa, wt, sw, out = _z(4, 32, dtype=i8), _z(4), _z(8, 32, dtype=i8), _z(8), _z(4, 8, dtype=BF)
+    right = [
+        lambda: m.moe_gate_pack(_z(16, 512, dtype=BF), _z(16 * 512 * 2, dtype=torch.uint8)),
+        lambda: m.moe_gate(g, x, lg),
+        lambda: m.moe_route(lg, ids, w),
+        lambda: m.moe_quant_i8(x, _z(4, 512, dtype=i8), _z(4)),
+        lambda: m.moe_linear_i8(a, sa, wt, sw, out),
+        lambda: m.moe_linear_i8(a, sa, wt, sw, out[:, :4], act="swiglu", bias=_z(8), add=_z(4, 4, dtype=BF)),
+    ]
+    for call in right:
+        with pytest.raises(ValueError, match="must be on a GPU"):
+            call()
+    wrong = [
+        lambda: m.moe_gate_pack(_z(512, 16, dtype=BF).t(), _z(16 * 512 * 2, dtype=torch.uint8)),
+        lambda: m.moe_gate_pack(_z(16, 512, dtype=F16), _z(16 * 512 * 2, dtype=torch.uint8)),
+        lambda: m.moe_gate(g, _z(4, 512), lg),
+        lambda: m.moe_gate(g, _z(4, 1024, dtype=BF), lg),
+        lambda: m.moe_gate(g, x, _z(4, 17)),
+        lambda: m.moe_gate(g, x, _z(3, 16)),
+        lambda: m.moe_gate(g, x, _z(4, 16, dtype=BF)),
+        lambda: m.moe_gate(g, _z(512, 4, dtype=BF).t(), lg),
+        lambda: m.moe_gate(g, _z(1, 512, dtype=BF).expand(4, 512), lg),
+        lambda: m.moe_route(_z(4, 16, dtype=torch.float64), ids, w),
+        lambda: m.moe_route(lg, ids.long(), w),
+        lambda: m.moe_route(lg, ids[:3], w),
+        lambda: m.moe_route(lg, ids, _z(4, 3)),
+        lambda: m.moe_route(lg, ids, w.half()),
+        lambda: m.moe_route(lg, _z(2, 4, dtype=torch.int32).t(), w),
+        lambda: m.moe_route(lg, ids, w, bias=_z(15)),
+        lambda: m.moe_route(lg, ids, w, bias=_z(16, dtype=BF)),
+        lambda: m.moe_route(lg, ids, w, score="tanh"),
+        lambda: m.moe_route(lg, ids, w, groups=4, topk_groups=2, group_score="mean"),
+        lambda: m.moe_route(lg, ids, w, scale=0.0),
+        lambda: m.moe_quant_i8(x, _z(4, 512, dtype=torch.uint8), _z(4)),
+        lambda: m.moe_quant_i8(x, _z(4, 511, dtype=i8), _z(4)),
+        lambda: m.moe_quant_i8(x, _z(4, 512, dtype=i8), _z(3)),
+        lambda: m.moe_quant_i8(x, _z(4, 512, dtype=i8), _z(8)[::2]),
+        lambda: m.moe_quant_i8(x[0], _z(4, 512, dtype=i8), _z(4)),
+        lambda: m.moe_linear_i8(a, sa, wt[:, :31], sw, out),
+        lambda: m.moe_linear_i8(a.float(), sa, wt, sw, out),
+        lambda: m.moe_linear_i8(a, sa, wt, sw, out[:3]),
+        lambda: m.moe_linear_i8(a, sa, wt, sw, out, act="swiglu"),
+        lambda: m.moe_linear_i8(a, sa, wt, sw, out, act="gelu"),
+        lambda: m.moe_linear_i8(a, sa, wt[:7], sw[:7], out[:, :3], act="swiglu"),
+        lambda: m.moe_linear_i8(a, sa[:3], wt, sw, out),
+        lambda: m.moe_linear_i8(a, sa, wt, sw.half(), out),
+        lambda: m.moe_linear_i8(a, sa, wt, sw, out, bias=_z(7)),
+        lambda: m.moe_linear_i8(a, sa, wt, sw, out, add=_z(4, 8)),
+        lambda: m.moe_linear_i8(a, sa, wt, sw, out, add=_z(4, 7, dtype=BF)),
+        lambda: m.moe_linear_i8(a, sa, wt, sw, out, add=_z(1, 8, dtype=BF).expand(4, 8)),
+    ]
+    for i, call in enumerate(wrong):
+        with pytest.raises(ValueError) as e:
+            call()
+        assert "must be on a GPU" not in str(e.value), i

@@ -1,0 +1,517 @@
+"""The dense side's operators on the GPU against plain 64-bit forms (dense_ref): the router's
+product, the choice of experts, int8 quantization and the int8 product; then the whole
+layer made of them."""
+import numpy as np
+import pytest
+import torch
+
+import dense_ref as ref
+from helpers import log
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda"
+BF, F16, F32 = torch.bfloat16, torch.float16, torch.float32
+HALF_STEP = {BF: 2.0 ** -8, F16: 2.0 ** -11, F32: 2.0 ** -24}   # largest rounding, relative
+TINY = {BF: 2.0 ** -134, F16: 2.0 ** -25, F32: 2.0 ** -150}     # and among subnormals
+
+
+@pytest.fixture(scope="module")
+def m():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    import moe_routed_expert_mx_amd as pkg
+    return pkg
+
+
+def _gen(seed):
+    return torch.Generator("cpu").manual_seed(seed)
+
+
+# --------------------------------------------------------------------- route
+def _route(m, logits, topk, stream=None, **o):
+    lg = logits.to(DEV) if logits.device.type == "cpu" else logits
+    B = lg.shape[0]
+    ids = torch.full((B + 1, topk), -7, dtype=torch.int32, device=DEV)
+    w = torch.full((B + 1, topk), -7.0, device=DEV)
+    bias = o.pop("bias", None)
+    m.moe_route(lg, ids[:B], w[:B], bias=None if bias is None else bias.to(DEV), stream=stream, **o)
+    torch.cuda.synchronize()
+    assert (ids[B] == -7).all() and (w[B] == -7).all()          # nothing behind the last token
+    return ids[:B].cpu().numpy(), w[:B].cpu().numpy()
+
+
+def _check_route(m, logits, topk, **o):
+    ids, w = _route(m, logits, topk, **dict(o))
+    bias = o.pop("bias", None)
+    rid, rw = ref.route(logits.double().numpy(), topk, bias=None if bias is None else bias.double().numpy(), **o)
+    assert np.array_equal(ids, rid)
+    # FP64 weights, some 2^-50 off, rounded to FP32 once
+    assert np.all(np.abs(w - rw) <= np.abs(rw) * (2.0 ** -24 * 1.001) + TINY[F32])
+
+
+MODES = [dict(), dict(renorm=False), dict(score="sigmoid", scale=2.5), dict(bias=True),
+         dict(score="sigmoid", bias=True), dict(score="sigmoid", bias=True, renorm=False, scale=0.5)]
+
+
+@pytest.mark.parametrize("B,E,K", [(1, 1, 1), (1, 160, 16), (3, 16, 4), (7, 63, 8), (33, 64, 1), (5, 65, 64),
+                                   (257, 160, 16), (9, 257, 5), (6, 1024, 64), (2, 64, 64), (1000, 8, 2)])
+@pytest.mark.parametrize("mode", range(len(MODES)))
+def test_route_sizes(m, B, E, K, mode):
+    log(f"route {B}x{E} top {K} {MODES[mode]}")
+    g = _gen(B * 31 + E + mode)
+    o = dict(MODES[mode])
+    if o.pop("bias", False):
+        o["bias"] = torch.randn(E, generator=g) * 0.1
+    dtype = (F32, BF, F16)[(B + E + mode) % 3]          # the narrow types bring ties
+    _check_route(m, (torch.randn(B, E, generator=g) * 2).to(dtype), K, **o)
+
+
+@pytest.mark.parametrize("E,groups,kept,K", [(160, 10, 5, 16), (256, 8, 4, 8), (64, 64, 7, 7), (12, 2, 1, 6),
+                                             (16, 1, 1, 3), (1024, 64, 3, 48), (35, 7, 7, 35), (96, 3, 2, 64),
+                                             (160, 20, 1, 8), (1020, 4, 2, 10)])
+@pytest.mark.parametrize("score,bias,group_score", [("softmax", False, "max"), ("sigmoid", True, "top2"),
+                                                    ("softmax", False, "top2"), ("softmax", True, "max")])
+def test_route_groups(m, E, groups, kept, K, score, bias, group_score):
+    log(f"route groups E={E} {groups}/{kept} K={K} {score} {bias} {group_score}")
+    g = _gen(E + groups)
+    o = dict(score=score, groups=groups, topk_groups=kept, group_score=group_score)
+    if bias:
+        o["bias"] = torch.randn(E, generator=g) * 0.2
+    dtype = (F32, BF)[(E + groups) % 2]
+    _check_route(m, torch.randn(37, E, generator=g).to(dtype), K, **o)
+
+
+@pytest.mark.parametrize("o", [dict(), dict(renorm=False), dict(score="sigmoid"),
+                               dict(bias=True), dict(score="sigmoid", bias=True),
+                               dict(groups=4, topk_groups=2), dict(groups=4, topk_groups=2, group_score="top2"),
+                               dict(score="sigmoid", bias=True, groups=4, topk_groups=2, group_score="top2")])
+def test_route_masked_infinite_and_tied(m, o):
+    """Rows that are masked in part or whole, by -inf, NaN or the type's lowest value; +inf;
+    equal logits; equal after the score saturates."""
+    log(f"route special values {o}")
+    o, E, inf, nan, low = dict(o), 32, float("inf"), float("nan"), torch.finfo(F32).min
+    x = torch.randn(24, E, generator=_gen(5))
+    x[0] = -inf
+    x[1] = nan
+    x[2] = low
+    x[3], x[3, 5] = -inf, 1.0
+    x[4], x[4, 31] = nan, -1000.0
+    x[5, ::2] = -inf
+    x[6, 3] = inf
+    x[7, 3:9] = inf
+    x[8] = inf
+    x[9] = 0.0
+    x[10], x[10, 7:] = 1.0, 2.0
+    x[11] = 100.0 + torch.arange(E)                    # sigmoid is 1 for all: the logits differ still
+    x[12] = -1000.0 - torch.arange(E)                  # sigmoid underflows
+    x[13, 4], x[13, 5] = inf, nan
+    x[14, :] = low
+    x[14, 9] = -low
+    x[15, 8:16] = -inf                                  # a whole group
+    x[16, 8:] = -inf                                    # all groups but one
+    x[17, :24] = nan
+    x[18] = torch.where(torch.arange(E) % 8 == 3, 0.5, -inf)     # one open expert a group
+    x[19, 0] = -0.0
+    x[20] *= 1e-30                                      # a choice closer than a score can tell
+    if o.pop("bias", False):
+        b = torch.randn(E, generator=_gen(6)) * 0.1
+        b[2], b[11], b[20] = -inf, nan, 3.0
+        o["bias"] = b
+    _check_route(m, x, 9, **o)
+
+
+def test_route_infinite_bias(m):
+    b = torch.zeros(20)
+    b[7], b[3] = float("inf"), float("inf")
+    _check_route(m, torch.randn(5, 20, generator=_gen(1)), 4, bias=b)
+    _check_route(m, torch.randn(5, 20, generator=_gen(1)), 4, bias=b, groups=5, topk_groups=2, group_score="top2")
+
+
+def test_route_strided_rows_and_streams(m):
+    big = torch.randn(50, 200, generator=_gen(9)).to(DEV)
+    view = big[:, 13:13 + 96]
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    ids, w = _route(m, view, 6, stream=s)
+    rid, rw = ref.route(view.cpu().double().numpy(), 6)
+    assert np.array_equal(ids, rid) and np.allclose(w, rw, rtol=1e-6)
+    with torch.cuda.stream(s):                          # the tensors' current stream
+        ids2, _ = _route(m, view, 6)
+    assert np.array_equal(ids2, rid)
+
+
+def test_route_near_choices(m):
+    """Choices that differ by less than an FP32 step: FP64 decides, as in the plain form."""
+    g = _gen(77)
+    x = torch.randn(300, 64, generator=g)
+    x[:, 1::2] = x[:, ::2] + torch.randn(300, 32, generator=g) * 1e-7
+    _check_route(m, x, 16, score="sigmoid", bias=torch.zeros(64))
+    _check_route(m, x, 16, bias=torch.full((64,), 3.0))
+    _check_route(m, x, 16, score="sigmoid", bias=torch.full((64,), 1000.0), groups=8, topk_groups=4,
+                 group_score="top2")
+
+
+# ---------------------------------------------------------------------- gate
+def _gate(m, x, w, ld=None, out_ld=None):
+    E, D = w.shape
+    packed = torch.empty(m.moe_gate_packed_bytes(E, D, w.dtype), dtype=torch.uint8, device=DEV)
+    h = m.moe_gate_pack(w.to(DEV), packed)
+    B = x.shape[0]
+    xd = torch.zeros(B, ld or D, dtype=BF, device=DEV)[:, :D]
+    xd.copy_(x)
+    out = torch.full((B + 1, out_ld or E), -7.0, device=DEV)
+    m.moe_gate(h, xd, out[:B, :E])
+    torch.cuda.synchronize()
+    assert (out[B] == -7).all() and (out[:, E:] == -7).all()
+    return out[:B, :E].cpu().double()
+
+
+@pytest.mark.parametrize("B,E,D", [(1, 160, 3584), (8, 160, 3584), (1, 1, 512), (17, 16, 512), (64, 81, 1024),
+                                   (65, 200, 512), (129, 15, 1536), (300, 1024, 512), (256, 160, 3584), (31, 96, 512),
+                                   (2, 256, 16384)])
+@pytest.mark.parametrize("wtype", [BF, F32])
+def test_gate_whole_numbers_are_exact(m, B, E, D, wtype):
+    """Whole numbers whose sums stay below 2^24: every order of summation gives the same."""
+    log(f"gate exact {B}x{E}x{D} {wtype}")
+    g = _gen(B + E + D)
+    x = torch.randint(-8, 9, (B, D), generator=g).to(BF)
+    w = torch.randint(-100, 101, (E, D), generator=g).to(wtype)
+    want = x.double() @ w.double().T
+    assert torch.equal(_gate(m, x, w, ld=D + 64, out_ld=E + 3), want)
+
+
+def test_gate_fp32_weight_keeps_all_its_bits(m):
+    """One feature a token: the logits are the FP32 weights themselves times a power of two."""
+    g = _gen(3)
+    w = (torch.randn(48, 512, generator=g) * torch.exp2(torch.randint(-40, 40, (48, 512), generator=g).float()))
+    x = torch.zeros(512, 512)
+    x[torch.arange(512), torch.randperm(512, generator=g)] = torch.exp2(torch.randint(-8, 9, (512,), generator=g).float())
+    got = _gate(m, x.to(BF), w)
+    assert torch.equal(got, x.double() @ w.double().T)
+
+
+@pytest.mark.parametrize("B,E,D", [(8, 160, 3584), (200, 100, 1024), (1030, 160, 512)])
+@pytest.mark.parametrize("wtype", [BF, F32])
+def test_gate_normal_values(m, B, E, D, wtype):
+    """FP32 sums of D (three planes: 3 D) exact products: each addition is off by at most a step
+    2^-23 of the partial sum (the matrix unit need not round to nearest), the partial sums at
+    most sum |x w| (planes of one sign: the same)."""
+    log(f"gate normal {B}x{E}x{D} {wtype}")
+    g = _gen(D)
+    x, w = torch.randn(B, D, generator=g).to(BF), (torch.randn(E, D, generator=g) / D ** 0.5).to(wtype)
+    got = _gate(m, x, w)
+    err = (got - x.double() @ w.double().T).abs()
+    bound = (3 * D if wtype == F32 else D) * 2.0 ** -23 * (x.double().abs() @ w.double().abs().T)
+    assert (err <= bound).all()
+
+
+def test_gate_rows_do_not_meet(m):
+    """A token with a non-finite feature has non-finite logits and leaves the others alone."""
+    g = _gen(4)
+    x, w = torch.randint(-8, 9, (40, 512), generator=g).to(BF), torch.randint(1, 9, (20, 512), generator=g).to(F32)
+    want = x.double() @ w.double().T
+    x[7, 100], x[33, 0] = float("inf"), float("nan")
+    got = _gate(m, x, w)
+    bad = torch.zeros(40, dtype=torch.bool)
+    bad[[7, 33]] = True
+    assert not got[bad].isfinite().any() and torch.equal(got[~bad], want[~bad])
+
+
+# --------------------------------------------------------------------- quant
+def _check_quant(m, x, ldx=0, ldc=0):
+    M, K = x.shape
+    xd = torch.zeros(M, K + ldx, dtype=x.dtype, device=DEV)[:, :K]
+    xd.copy_(x)
+    q = torch.full((M + 1, K + ldc), 99, dtype=torch.int8, device=DEV)
+    s = torch.full((M + 1,), -7.0, device=DEV)
+    m.moe_quant_i8(xd, q[:M, :K], s[:M])
+    torch.cuda.synchronize()
+    assert (q[M] == 99).all() and (q[:, K:] == 99).all() and s[M] == -7
+    rq, rs = ref.quant(x.double().numpy())
+    assert np.array_equal(q[:M, :K].cpu().numpy(), rq)
+    assert np.array_equal(s[:M].cpu().numpy(), rs, equal_nan=True)
+
+
+@pytest.mark.parametrize("M,K,ldx,ldc", [(1, 1, 0, 0), (8, 3584, 0, 0), (3, 384, 0, 0), (5, 17, 0, 0), (4, 64, 3, 5),
+                                         (2, 4096, 8, 16), (9, 1000, 0, 0), (1, 131072, 0, 0), (300, 129, 0, 0),
+                                         (2, 8191, 1, 0), (3, 20000, 0, 0), (1031, 512, 0, 0), (2, 16392, 0, 0)])
+@pytest.mark.parametrize("dtype", [BF, F16, F32])
+def test_quant_sizes(m, M, K, ldx, ldc, dtype):
+    log(f"quant {M}x{K}+{ldx} {dtype}")
+    g = _gen(M + K)
+    _check_quant(m, (torch.randn(M, K, generator=g) * torch.exp2(torch.randint(-6, 7, (M, 1), generator=g))).to(dtype),
+                 ldx, ldc)
+
+
+@pytest.mark.parametrize("dtype", [BF, F16, F32])
+def test_quant_halves_and_extremes(m, dtype):
+    """Quotients at exactly a half (even wins) and one step beside it, zeros, subnormals, the
+    type's largest values, infinities and NaN."""
+    fi = torch.finfo(dtype)
+    K = 254
+    x = torch.zeros(14, K)
+    x[0] = torch.arange(K) / 2 - 63.5                 # amax 63.5: x * 127 / amax = 2 x
+    x[1] = (torch.arange(K) - 127) * 1.0              # amax 127
+    x[1, 0] = 254.0                                    # amax 254: halves of whole numbers
+    x[2] = 0.0
+    x[3] = -0.0
+    x[4, 3], x[4, 4] = fi.max, -fi.max / 2
+    x[5] = fi.tiny * (torch.arange(K) / K)            # subnormal or just above
+    x[6, 0] = fi.smallest_normal
+    x[7, 9] = float("inf")
+    x[8, 9] = float("-inf")
+    x[9, 0] = float("nan")
+    x[10] = torch.randn(K, generator=_gen(1))
+    x[10, 200], x[10, 3] = float("nan"), float("inf")
+    x[11, 100] = -3.0
+    x = x.to(dtype)
+    # amax with halves in reach, each neighboured by the next value of the type up and down
+    up = (x[1].view(torch.int32 if dtype == F32 else torch.int16) + 1).view(dtype)
+    dn = (x[1].view(torch.int32 if dtype == F32 else torch.int16) - 1).view(dtype)
+    x[12], x[13] = torch.where(x[1].abs() < 127, up, x[1]), torch.where(x[1].abs() < 127, dn, x[1])
+    x[12, 127] = x[13, 127] = 0                        # 0 has no neighbour below
+    x[12, 0] = x[13, 0] = 254.0
+    _check_quant(m, x)
+
+
+@pytest.mark.parametrize("dtype", [BF, F16])
+def test_quant_every_mantissa(m, dtype):
+    """Every pair of significands of amax and x over a range of exponents."""
+    bits = 7 if dtype == BF else 10
+    top = 1 + torch.arange(2 ** bits)[:: 1 if dtype == BF else 7] / 2 ** bits
+    row = torch.cat([(1 + torch.arange(2 ** bits) / 2 ** bits) * 2.0 ** -e for e in range(1, 9)])
+    x = torch.cat([top[:, None], -row.expand(len(top), -1)], dim=1).to(dtype)
+    _check_quant(m, x)
+
+
+# -------------------------------------------------------------------- linear
+def _codes(shape, g):
+    return torch.randint(-128, 128, shape, generator=g).to(torch.int8)
+
+
+def _place(t, ld, offset=0):
+    """A copy of t [rows, cols] on the GPU with row distance ld, `offset` elements into its
+    storage, and nothing behind its last element."""
+    r, c = t.shape
+    flat = torch.zeros(offset + (r - 1) * ld + c, dtype=t.dtype, device=DEV)
+    v = torch.as_strided(flat, (r, c), (ld, 1), offset)
+    v.copy_(t)
+    return v
+
+
+def _check_linear(m, M, N, K, *, out=BF, act="none", bias=False, add=False, inplace=False, lda=0, ldw=0, ldo=0,
+                  offset=0, seed=0, codes=None):
+    log(f"linear {M}x{N}x{K} {out} {act} bias={bias} add={add} ld+={lda},{ldw},{ldo} @{offset}")
+    g = _gen(seed + M * 7 + N * 3 + K)
+    cols = N // 2 if act == "swiglu" else N
+    a, w = codes if codes is not None else (_codes((M, K), g), _codes((N, K), g))
+    sa, sw = (0.5 + torch.rand(M, generator=g)) * 0.02, (0.5 + torch.rand(N, generator=g)) * 0.02 / K ** 0.5
+    b = torch.randn(N, generator=g) if bias else None
+    d = torch.randn(M, cols, generator=g).to(out) if add else None
+    buf = torch.full((M + 1, cols + ldo), -7.0, dtype=out, device=DEV)
+    o = buf[:M, :cols]
+    if inplace:
+        o.copy_(d)
+    ad, wd = _place(a, K + lda, offset), _place(w, K + ldw, offset)
+    m.moe_linear_i8(ad, sa.to(DEV), wd, sw.to(DEV), o, act=act, bias=None if b is None else b.to(DEV),
+                    add=None if d is None else o if inplace else d.to(DEV))
+    torch.cuda.synchronize()
+    assert (buf[M] == -7).all() and (buf[:, cols:] == -7).all()
+    y, slack = ref.linear(a.numpy(), sa.numpy(), w.numpy(), sw.numpy(), act=act,
+                          bias=None if b is None else b.numpy(), add=None if d is None else d.double().numpy())
+    err = np.abs(o.cpu().double().numpy() - y)
+    tol = slack + HALF_STEP[out] * (np.abs(y) + slack) + TINY[out]
+    assert np.all(err <= tol), (err / tol).max()
+
+
+SIZES = [(1, 1, 1), (1, 768, 3584), (8, 3584, 384), (2, 16, 64), (3, 18, 65), (16, 32, 128), (17, 34, 100),
+         (31, 66, 17), (64, 64, 256), (65, 130, 1000), (64, 512, 4096), (100, 200, 48), (127, 126, 129),
+         (128, 256, 512), (129, 258, 640), (200, 1024, 384), (255, 512, 1023), (256, 768, 3584), (300, 520, 2048),
+         (1000, 384, 272), (513, 770, 144), (1, 2, 131071)]
+
+
+@pytest.mark.parametrize("M,N,K", SIZES)
+@pytest.mark.parametrize("act", ["none", "swiglu"])
+def test_linear_sizes(m, M, N, K, act):
+    if act == "swiglu" and N % 2:
+        N += 1
+    i = M + N + K
+    _check_linear(m, M, N, K, act=act, out=(BF, F16, F32)[i % 3] if act == "none" else (BF, F32)[i % 2],
+                  bias=i % 2 == 0, add=i % 4 < 2)
+
+
+@pytest.mark.parametrize("out", [BF, F16, F32])
+@pytest.mark.parametrize("M", [1, 5, 24, 40, 70, 300])
+def test_linear_epilogues(m, out, M):
+    for act in ("none", "swiglu"):
+        for bias in (False, True):
+            for add in (False, True):
+                _check_linear(m, M, 96, 256, out=out, act=act, bias=bias, add=add, ldo=5 if add else 0)
+    _check_linear(m, M, 96, 256, out=out, add=True, inplace=True)
+
+
+@pytest.mark.parametrize("M", [1, 20, 64, 150, 600])
+@pytest.mark.parametrize("lda,ldw,offset,K", [(16, 0, 0, 256), (0, 32, 16, 256), (1, 0, 0, 256), (0, 3, 0, 256),
+                                              (0, 0, 5, 256), (7, 9, 3, 250), (6, 6, 0, 250), (1000, 2000, 0, 320)])
+def test_linear_strides(m, M, lda, ldw, offset, K):
+    _check_linear(m, M, 130, K, lda=lda, ldw=ldw, ldo=3, offset=offset)
+    _check_linear(m, M, 130, K, lda=lda, ldw=ldw, offset=offset, act="swiglu", out=F32)
+
+
+@pytest.mark.parametrize("M,N,K", [(2, 32, 131071), (40, 64, 131056), (300, 320, 20000)])
+def test_linear_extreme_codes(m, M, N, K):
+    """-128 times -128 over the longest rows: the sum's largest value, 2^31 - 2^14."""
+    a, w = torch.full((M, K), -128, dtype=torch.int8), torch.full((N, K), -128, dtype=torch.int8)
+    w[1] = 127
+    _check_linear(m, M, N, K, out=F32, codes=(a, w))
+
+
+def test_linear_non_finite_scales(m):
+    """A NaN scale makes its row or column NaN and no other; so the quantization of a row with an
+    infinity reaches the result."""
+    g = _gen(8)
+    x = torch.randn(40, 64, generator=g).to(BF)
+    x[11, 5] = float("inf")
+    q, s = torch.empty(40, 64, dtype=torch.int8, device=DEV), torch.empty(40, device=DEV)
+    m.moe_quant_i8(x.to(DEV), q, s)
+    w, sw = _codes((48, 64), g).to(DEV), torch.rand(48, generator=g).to(DEV)
+    sw[7] = float("nan")
+    out = torch.empty(40, 48, dtype=BF, device=DEV)
+    m.moe_linear_i8(q, s, w, sw, out)
+    bad = out.cpu().isnan()
+    want = torch.zeros(40, 48, dtype=torch.bool)
+    want[11], want[:, 7] = True, True
+    assert torch.equal(bad, want)
+
+
+def test_linear_rows_past_32_bit_offsets(m):
+    """A row distance that puts the last rows of a and out beyond 2^32 bytes."""
+    M, K, N, ld = 1100, 64, 32, (1 << 22) - 16
+    store = torch.zeros((M - 1) * ld + K, dtype=torch.int8, device=DEV)
+    a = torch.as_strided(store, (M, K), (ld, 1))
+    g = _gen(2)
+    codes, w = _codes((M, K), g), _codes((N, K), g)
+    a.copy_(codes)
+    sa, sw = torch.ones(M), torch.ones(N)
+    ostore = torch.zeros((M - 1) * ld + N, dtype=F32, device=DEV)
+    o = torch.as_strided(ostore, (M, N), (ld, 1))
+    m.moe_linear_i8(a, sa.to(DEV), w.to(DEV), sw.to(DEV), o)
+    want = codes.double() @ w.double().T
+    assert torch.equal(o.cpu().double(), want)
+
+
+# ----------------------------------------------------------- graphs and chains
+def test_captured_and_replayed(m):
+    """All operators in one graph, replayed with eager work and new inputs between."""
+    g = _gen(21)
+    B, D, E, K, I = 24, 512, 40, 6, 96
+    w = torch.randn(E, D, generator=g).to(DEV)
+    packed = torch.empty(m.moe_gate_packed_bytes(E, D, F32), dtype=torch.uint8, device=DEV)
+    h = m.moe_gate_pack(w, packed)
+    wq, ws = _codes((2 * I, D), g).to(DEV), torch.rand(2 * I, generator=g).to(DEV) * 1e-3
+    x = torch.randn(B, D, generator=g).to(BF).to(DEV)
+
+    def buffers():
+        return dict(lg=torch.empty(B, E, device=DEV), ids=torch.empty(B, K, dtype=torch.int32, device=DEV),
+                    w=torch.empty(B, K, device=DEV), q=torch.empty(B, D, dtype=torch.int8, device=DEV),
+                    s=torch.empty(B, device=DEV), y=torch.empty(B, I, dtype=BF, device=DEV))
+
+    def step(b):
+        m.moe_gate(h, x, b["lg"])
+        m.moe_route(b["lg"], b["ids"], b["w"], score="sigmoid", groups=4, topk_groups=2)
+        m.moe_quant_i8(x, b["q"], b["s"])
+        m.moe_linear_i8(b["q"], b["s"], wq, ws, b["y"], act="swiglu")
+
+    cap, eager = buffers(), buffers()
+    step(cap)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step(cap)
+    for i in range(4):
+        x.copy_(torch.randn(B, D, generator=g).to(BF))
+        step(eager)
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        for k in cap:
+            assert torch.equal(cap[k], eager[k]), (i, k)
+
+
+def test_two_streams_at_once(m):
+    """Calls that overlap on two streams give what they give alone (no shared state)."""
+    g = _gen(23)
+    sets = []
+    for i in range(2):
+        a, w = _codes((300, 1024), g).to(DEV), _codes((512, 1024), g).to(DEV)
+        sets.append((a, torch.rand(300, generator=g).to(DEV), w, torch.rand(512, generator=g).to(DEV),
+                     torch.empty(300, 512, dtype=F32, device=DEV)))
+    alone = []
+    for s in sets:
+        m.moe_linear_i8(*s)
+        torch.cuda.synchronize()
+        alone.append(s[4].clone())
+        s[4].zero_()
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in sets]
+    for _ in range(5):
+        for st, s in zip(streams, sets):
+            m.moe_linear_i8(*s, stream=st)
+    torch.cuda.synchronize()
+    for s, want in zip(sets, alone):
+        assert torch.equal(s[4], want)
+
+
+@pytest.mark.parametrize("B", [1, 8, 40])
+def test_block_end_to_end(m, B):
+    """The layer as it is used: router, routed experts, combine, shared expert.  Each stage is
+    checked against the plain form of the stage on the values that the GPU handed it."""
+    import workloads
+    from moe_routed_expert_mx_amd.block import MoeBlock, Router, SharedExpertI8
+    from moe_routed_expert_mx_amd.layer import MoeLayer
+    log(f"block B={B}")
+    d = workloads.generate(workloads.custom(B=B, E=24, K=4, D=512, I=64, seed=B))
+    g = _gen(B)
+    x = torch.from_numpy(d["x"]).view(BF).to(DEV)
+    gw, bias = torch.randn(24, 512, generator=g) / 22, torch.randn(24, generator=g) * 0.05
+    router = Router(gw, topk=4, B_max=48, bias=bias, score="sigmoid", groups=6, topk_groups=3, group_score="top2",
+                    scale=2.0)
+    layer = MoeLayer(d["w13"], d["s13"], d["w2"], d["s2"], B_max=48, topk=4, device=DEV)
+    w13, w2 = torch.randn(2 * 96, 512, generator=g) / 22, torch.randn(512, 96, generator=g) / 10
+    shared = SharedExpertI8.quantize(w13, w2, B_max=48)
+    y = MoeBlock(router, layer, shared).forward(x)
+    ids, wts = router.forward(x)
+    rows = layer.forward(x, ids)
+    comb = layer.combine(rows, wts)
+    torch.cuda.synchronize()
+    logits = router.logits[:B].cpu()
+    rid, rw = ref.route(logits.double().numpy(), 4, score="sigmoid", bias=bias.numpy(), groups=6, topk_groups=3,
+                        group_score="top2", scale=2.0)
+    assert np.array_equal(ids.cpu().numpy(), rid)
+    assert np.allclose(wts.cpu().numpy(), rw, rtol=2.0 ** -23)
+    q, s = ref.quant(x.cpu().double().numpy())
+    h, eh = ref.linear(q, s, shared.w13.cpu().numpy(), shared.s13.cpu().numpy(), act="swiglu")
+    hid = shared.hidden[:B].cpu()
+    assert np.all(np.abs(hid.double().numpy() - h) <= eh + 2.0 ** -8 * (np.abs(h) + eh))
+    q2, s2 = ref.quant(hid.double().numpy())
+    out, eo = ref.linear(q2, s2, shared.w2.cpu().numpy(), shared.s2.cpu().numpy(), add=comb.cpu().double().numpy())
+    assert np.all(np.abs(y.cpu().double().numpy() - out) <= eo + 2.0 ** -8 * (np.abs(out) + eo))
+    # the int8 shared expert stands for the float one: two quantizations of a hundredth each
+    f = x.cpu().double() @ w13.double().T
+    f = (torch.nn.functional.silu(f[:, :96]) * f[:, 96:]) @ w2.double().T + comb.cpu().double()
+    assert (y.cpu().double() - f).norm() <= 0.05 * f.norm()
+    # without the shared expert: the combined rows
+    assert torch.equal(MoeBlock(router, layer).forward(x), comb)
+
+
+def test_shared_expert_twice_with_other_batches(m):
+    """One object, batches of different sizes in turn: nothing of an earlier call is left."""
+    from moe_routed_expert_mx_amd.block import SharedExpertI8
+    g = _gen(31)
+    sh = SharedExpertI8.quantize(torch.randn(128, 512, generator=g), torch.randn(512, 64, generator=g), B_max=100)
+    xs = [torch.randn(b, 512, generator=g).to(BF).to(DEV) for b in (100, 3, 64, 100, 1)]
+    first = [sh.forward(x).clone() for x in xs]
+    for x, want in list(zip(xs, first))[::-1]:
+        assert torch.equal(sh.forward(x), want)
+    with pytest.raises(ValueError):
+        sh.forward(torch.zeros(101, 512, dtype=BF, device=DEV))
