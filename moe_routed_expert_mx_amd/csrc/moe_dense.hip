@@ -3,6 +3,7 @@
 // shared expert beside them, behind the C ABI of include/moe_mx.h.
 #include <hip/hip_runtime.h>
 
+#include <atomic>
 #include <cmath>
 #include <cstdint>
 #include <cstring>
@@ -12,8 +13,11 @@
 namespace {
 
 typedef int v4i __attribute__((ext_vector_type(4)));
+typedef int v16i __attribute__((ext_vector_type(16)));
 typedef float v4f __attribute__((ext_vector_type(4)));
 typedef __bf16 v8bf __attribute__((ext_vector_type(8)));
+
+__device__ __forceinline__ void compiler_fence() { asm volatile("" ::: "memory"); }
 
 // ------------------------------------------------------------------ elements
 __device__ __forceinline__ float bf16_to_f32(uint16_t b) { return __uint_as_float(static_cast<uint32_t>(b) << 16); }
@@ -298,35 +302,88 @@ struct GateArgs {
   int64_t ldl;
 };
 
-template <int P>
-__global__ __launch_bounds__(256) void gate_kernel(GateArgs a) {
-  constexpr int ET = 5;
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int64_t t = static_cast<int64_t>(blockIdx.x) * 64 + wave * 16 + (lane & 15);
-  const int et0 = blockIdx.y * ET, tiles = (a.E + 15) / 16, steps = a.D / 32;
-  const uint16_t* xr = a.x + (t < a.B ? t : a.B - 1) * a.ldx + (lane >> 4) * 8;
-  v4f acc[ET] = {};
-  for (int s = 0; s < steps; ++s) {
-    const v8bf b = *reinterpret_cast<const v8bf*>(xr + s * 32);
+// A workgroup's tile is 16 TT tokens x 16 ET experts; its WV waves take a share of the features
+// each, read both operands straight into registers (no byte is read twice in a workgroup, so
+// LDS would serve nothing) and add their FP32 tiles through LDS in wave order.
+template <int P, int TT, int ET, int WV>
+__global__ __launch_bounds__(64 * WV) void gate_kernel(GateArgs a, uint32_t cols, uint32_t rows) {
+  extern __shared__ float gate_lds[];
+  constexpr int kOut = 256 * TT * ET;           // outputs of the tile
+  // steps in flight: of x, which comes from HBM, and of the weight, which L2 holds
+  constexpr int UX = TT * ET >= 8 ? 8 : 4, UW = TT * ET >= 8 ? 2 : 4;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  // the tiles of one token range run on one XCD (workgroups go round the eight), so that its L2
+  // serves x to all of them
+  const uint32_t span = 8 * cols, row = blockIdx.x / span * 8 + blockIdx.x % 8, col = blockIdx.x % span / 8;
+  if (row >= rows) return;
+  const int64_t t0 = static_cast<int64_t>(row) * (16 * TT);
+  const int tiles = (a.E + 15) / 16, steps = a.D / 32, n = steps / WV, s0 = wave * n;
+  const uint16_t* xp[TT];
+  const uint16_t* wp[ET];
 #pragma unroll
-    for (int i = 0; i < ET; ++i) {
-      const int et = et0 + i < tiles ? et0 + i : tiles - 1;
+  for (int i = 0; i < TT; ++i) {
+    const int64_t t = t0 + i * 16 + (lane & 15);
+    xp[i] = a.x + (t < a.B ? t : a.B - 1) * a.ldx + s0 * 32 + (lane >> 4) * 8;
+  }
 #pragma unroll
-      for (int p = 0; p < P; ++p) {
-        const v8bf w = *reinterpret_cast<const v8bf*>(
-            a.packed + ((static_cast<int64_t>(et) * steps + s) * P + p) * 512 + lane * 8);
-        acc[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(w, b, acc[i], 0, 0, 0);
+  for (int i = 0; i < ET; ++i) {
+    const int et = static_cast<int>(col) * ET + i;
+    wp[i] = a.packed + (static_cast<int64_t>(et < tiles ? et : tiles - 1) * steps + s0) * (P * 512) + lane * 8;
+  }
+  v4f acc[TT][ET] = {};
+  v8bf xb[UX][TT], wb[UW][ET][P];
+  auto load_x = [&](int u, int s) {
+    s = s < n ? s : n - 1;  // past the end: loaded again, not used
+#pragma unroll
+    for (int i = 0; i < TT; ++i) xb[u][i] = *reinterpret_cast<const v8bf*>(xp[i] + s * 32);
+  };
+  auto load_w = [&](int u, int s) {
+    s = s < n ? s : n - 1;
+#pragma unroll
+    for (int i = 0; i < ET; ++i)
+#pragma unroll
+      for (int p = 0; p < P; ++p) wb[u][i][p] = *reinterpret_cast<const v8bf*>(wp[i] + (s * P + p) * 512);
+  };
+#pragma unroll
+  for (int u = 0; u < UX; ++u) load_x(u, u);
+#pragma unroll
+  for (int u = 0; u < UW; ++u) load_w(u, u);
+  compiler_fence();  // the loads stay where they are written, steps ahead of their use
+  for (int s = 0; s < n; s += UX) {
+#pragma unroll
+    for (int u = 0; u < UX; ++u) {
+      if (s + u < n) {
+#pragma unroll
+        for (int p = 0; p < P; ++p)
+#pragma unroll
+          for (int i = 0; i < ET; ++i)
+#pragma unroll
+            for (int j = 0; j < TT; ++j)
+              acc[j][i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wb[u % UW][i][p], xb[u][j], acc[j][i], 0, 0, 0);
+        load_x(u, s + u + UX);
+        load_w(u % UW, s + u + UW);
+        compiler_fence();
       }
     }
   }
-  if (t >= a.B) return;
+  // [wave][token][expert], padded by a word a row
+  constexpr int kRow = 16 * ET + 4;
 #pragma unroll
-  for (int i = 0; i < ET; ++i)
+  for (int j = 0; j < TT; ++j)
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int e = (et0 + i) * 16 + (lane >> 4) * 4 + j;
-      if (e < a.E) a.logits[t * a.ldl + e] = acc[i][j];
-    }
+    for (int i = 0; i < ET; ++i)
+      *reinterpret_cast<v4f*>(gate_lds + (wave * 16 * TT + j * 16 + (lane & 15)) * kRow + i * 16 + (lane >> 4) * 4) =
+          acc[j][i];
+  __syncthreads();
+  for (int o = threadIdx.x; o < kOut; o += 64 * WV) {
+    const int tok = o / (16 * ET), e = o % (16 * ET);
+    float v = gate_lds[tok * kRow + e];
+#pragma unroll
+    for (int w = 1; w < WV; ++w) v += gate_lds[(w * 16 * TT + tok) * kRow + e];
+    const int64_t t = t0 + tok;
+    const int ge = static_cast<int>(col) * 16 * ET + e;
+    if (t < a.B && ge < a.E) a.logits[t * a.ldl + ge] = v;
+  }
 }
 
 // -------------------------------------------------------------------- linear
@@ -357,7 +414,277 @@ __device__ __forceinline__ uint4 row16(const int8_t* row, int k, int K, bool liv
   return v;
 }
 
+__device__ __forceinline__ v4i bits(uint4 v) {
+  return v4i{static_cast<int>(v.x), static_cast<int>(v.y), static_cast<int>(v.z), static_cast<int>(v.w)};
+}
 __device__ __forceinline__ float silu(float g) { return g / (1.0f + __expf(-g)); }
+
+// ------------------------------------------------- linear: up to 64 tokens
+// The weight is read once, so its bytes bound the product.  A workgroup takes 16 weight rows
+// (SwiGLU: 16 gate rows and their 16 up rows) and all tokens; its WV waves split K, read both
+// operands straight into registers some chunks of 64 bytes ahead, and add their 32-bit sums
+// through LDS.
+template <int OUT, bool SWIGLU, bool ALIGNED, int TT, int WV>
+__global__ __launch_bounds__(64 * WV) void linear_stream_kernel(LinearArgs a) {
+  extern __shared__ int stream_lds[];
+  constexpr int RT = SWIGLU ? 2 : 1, U = RT + TT >= 5 ? 4 : 8;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int H = SWIGLU ? a.N / 2 : a.N, n0 = blockIdx.x * 16;
+  const int chunks = (a.K + 63) / 64, per = (chunks + WV - 1) / WV, c0 = wave * per;
+  const int n = chunks - c0 < per ? (chunks > c0 ? chunks - c0 : 0) : per;
+  const int r = lane & 15, q = lane >> 4;
+  const int8_t *wp[RT], *ap[TT];
+  const int row = n0 + r < H ? n0 + r : H - 1;
+#pragma unroll
+  for (int i = 0; i < RT; ++i) wp[i] = a.w + (static_cast<int64_t>(row) + i * H) * a.ldw;
+#pragma unroll
+  for (int i = 0; i < TT; ++i) ap[i] = a.a + static_cast<int64_t>(i * 16 + r < a.M ? i * 16 + r : a.M - 1) * a.lda;
+  v4i acc[RT][TT] = {}, wb[U][RT], ab[U][TT];
+  // aligned: an operand's 16 bytes lie wholly inside the row or wholly behind it; those behind
+  // are read from the row's last 16 and set to zero when used
+  auto load = [&](int u, int c) {
+    const int k = (c0 + c) * 64 + q * 16;
+    if constexpr (ALIGNED) {
+      const int kc = k < a.K ? k : a.K - 16;
+#pragma unroll
+      for (int i = 0; i < RT; ++i) wb[u][i] = *reinterpret_cast<const v4i*>(wp[i] + kc);
+#pragma unroll
+      for (int i = 0; i < TT; ++i) ab[u][i] = *reinterpret_cast<const v4i*>(ap[i] + kc);
+    } else {
+#pragma unroll
+      for (int i = 0; i < RT; ++i) wb[u][i] = bits(row16(wp[i], k, a.K, true));
+#pragma unroll
+      for (int i = 0; i < TT; ++i) ab[u][i] = bits(row16(ap[i], k, a.K, true));
+    }
+  };
+  if (n > 0) {
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+      if (u < n) load(u, u);
+    compiler_fence();
+    for (int c = 0; c < n; c += U) {
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+        if (c + u < n) {
+          if (ALIGNED && (c0 + c + u) * 64 + 64 > a.K) {
+            const bool in = (c0 + c + u) * 64 + q * 16 < a.K;
+#pragma unroll
+            for (int i = 0; i < RT; ++i) wb[u][i] = in ? wb[u][i] : v4i{0, 0, 0, 0};
+          }
+#pragma unroll
+          for (int i = 0; i < RT; ++i)
+#pragma unroll
+            for (int j = 0; j < TT; ++j)
+              acc[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(wb[u][i], ab[u][j], acc[i][j], 0, 0, 0);
+          if (c + u + U < n) load(u, c + u + U);
+          compiler_fence();
+        }
+    }
+  }
+  // [wave][token][weight row], padded by four words a row
+  constexpr int kRow = 16 * RT + 4, kTile = 16 * TT * kRow;
+#pragma unroll
+  for (int i = 0; i < RT; ++i)
+#pragma unroll
+    for (int j = 0; j < TT; ++j)
+      *reinterpret_cast<v4i*>(stream_lds + wave * kTile + (j * 16 + r) * kRow + i * 16 + q * 4) = acc[i][j];
+  __syncthreads();
+  using T = typename Elem<OUT>::T;
+  for (int o = threadIdx.x; o < 256 * TT; o += 64 * WV) {
+    const int m = o >> 4, c = n0 + (o & 15);
+    if (m >= a.M || c >= H) continue;
+    const int* p = stream_lds + m * kRow + (o & 15);
+    int sum = 0, sum_up = 0;
+#pragma unroll
+    for (int v = 0; v < WV; ++v) {
+      sum += p[v * kTile];
+      if (SWIGLU) sum_up += p[v * kTile + 16];
+    }
+    const float sa = a.sa[m];
+    float y = static_cast<float>(sum) * sa * a.sw[c] + (a.bias ? a.bias[c] : 0.0f);
+    if (SWIGLU) y = silu(y) * (static_cast<float>(sum_up) * sa * a.sw[H + c] + (a.bias ? a.bias[H + c] : 0.0f));
+    if (a.add) y += to_f32<OUT>(static_cast<const T*>(a.add)[m * a.ldadd + c]);
+    static_cast<T*>(a.out)[m * a.ldo + c] = from_f32<OUT>(y);
+  }
+}
+
+// ------------------------------------------------- linear: many tokens
+// 16 bytes a lane from a buffer (base, extent in bytes) to LDS at lds + 16 * lane; lanes whose
+// offset lies outside the extent write zeros and read nothing.  Written as asm so that the
+// compiler does not drain the stream before every LDS read: its landing is awaited by count.
+constexpr uint32_t kOutside = 0x80000000u;
+__device__ __forceinline__ void dma16(v4i rsrc, uint32_t voff, uint32_t soff, uint32_t lds) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds"
+               :
+               : "s"(lds), "v"(voff), "s"(rsrc), "s"(soff)
+               : "memory");
+}
+__device__ __forceinline__ v4i make_rsrc(const void* base, uint32_t bytes) {
+  const uint64_t b = reinterpret_cast<uint64_t>(base);
+  v4i r;
+  r[0] = __builtin_amdgcn_readfirstlane(static_cast<int>(b));
+  r[1] = __builtin_amdgcn_readfirstlane(static_cast<int>((b >> 32) & 0xffffu));
+  r[2] = __builtin_amdgcn_readfirstlane(static_cast<int>(bytes));
+  r[3] = 0x00020000;
+  return r;
+}
+template <int N>
+__device__ __forceinline__ void wait_vm() {
+  asm volatile("s_waitcnt vmcnt(%0)" : : "n"(N) : "memory");
+}
+
+// Workgroup tile of BM tokens x BN weight rows, four waves of half by half each, 32x32x32
+// MFMAs with the weight as the row operand (a lane then holds four neighbouring columns of out).
+// K goes through LDS in stages of 64 bytes a row, four in flight; a row's four 16-byte parts lie
+// permuted by its index, so that eight neighbouring rows' reads meet all banks once.
+template <int BM, int BN, int OUT, bool SWIGLU>
+__global__ __launch_bounds__(256, BM * BN >= 65536 ? 1 : 2) void linear_dma_kernel(LinearArgs a, uint32_t nm,
+                                                                                   uint32_t nn, uint32_t per_xcd) {
+  extern __shared__ __attribute__((aligned(16))) unsigned char smem[];
+  constexpr int NS = 4, kStage = (BM + BN) * 64, RA = BM / 64, RW = BN / 64;
+  static_assert(!SWIGLU || BN >= 128, "a wave holds whole gate and up pairs");
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  // each XCD (workgroups go round the eight) takes a contiguous range of tiles, in groups of
+  // eight token tiles: what runs at once on an XCD shares operands in its L2
+  const uint32_t tile = blockIdx.x % 8 * per_xcd + blockIdx.x / 8;
+  if (blockIdx.x / 8 >= per_xcd || tile >= nm * nn) return;
+  const uint32_t band = tile / (8 * nn), left = nm - band * 8, height = left < 8 ? left : 8, in = tile - band * 8 * nn;
+  const int64_t m0 = static_cast<int64_t>(band * 8 + in % height) * BM;
+  const int H = SWIGLU ? a.N / 2 : a.N, n0 = static_cast<int>(in / height) * (SWIGLU ? BN / 2 : BN);
+  const uint32_t lds0 = static_cast<uint32_t>(reinterpret_cast<uintptr_t>((__attribute__((address_space(3))) void*)smem));
+
+  // what this lane moves: 16-byte part `ch` of rows lane / 4 of its wave's 16-row blocks
+  const int ch = (lane & 3) ^ ((lane >> 3) & 3), lr = lane >> 2;
+  const int mrows = a.M - m0 < BM ? static_cast<int>(a.M - m0) : BM;
+  const v4i ra = make_rsrc(a.a + m0 * a.lda, static_cast<uint32_t>((mrows - 1) * a.lda + a.K));
+  uint32_t va[RA], vw[RW];
+  v4i rw[RW];
+  {
+    const int cols = SWIGLU ? BN / 2 : BN, nrows = H - n0 < cols ? H - n0 : cols;
+    const uint32_t bytes = static_cast<uint32_t>((nrows - 1) * a.ldw + a.K);
+#pragma unroll
+    for (int i = 0; i < RA; ++i) {
+      const int row = (wave * RA + i) * 16 + lr;
+      va[i] = row < mrows ? static_cast<uint32_t>(row * a.lda) + ch * 16 : kOutside;
+    }
+#pragma unroll
+    for (int i = 0; i < RW; ++i) {
+      // SwiGLU: 32 gate rows, then their 32 up rows, and so on
+      const int b = wave * RW + i, row = SWIGLU ? (b >> 2) * 32 + (b & 1) * 16 + lr : b * 16 + lr;
+      rw[i] = make_rsrc(a.w + (n0 + (SWIGLU ? static_cast<int64_t>((b >> 1) & 1) * H : 0)) * a.ldw, bytes);
+      vw[i] = row < nrows ? static_cast<uint32_t>(row * a.ldw) + ch * 16 : kOutside;
+    }
+  }
+  auto issue = [&](int s) {
+    const int k0 = s * 64;
+    const uint32_t dst = lds0 + (s % NS) * kStage;
+    const bool in_k = k0 + ch * 16 < a.K;  // parts behind K, and whole stages behind it: zeros
+#pragma unroll
+    for (int i = 0; i < RA; ++i) dma16(ra, in_k ? va[i] : kOutside, k0, dst + (wave * RA + i) * 1024);
+#pragma unroll
+    for (int i = 0; i < RW; ++i) dma16(rw[i], in_k ? vw[i] : kOutside, k0, dst + BM * 64 + (wave * RW + i) * 1024);
+  };
+
+  const int wm = (wave & 1) * (BM / 2), wn = (wave >> 1) * (BN / 2);
+  constexpr int TM = BM / 64, TN = BN / 64;
+  uint32_t la[2];  // this lane's operand inside a 32-row tile, for the stage's two halves
+#pragma unroll
+  for (int h = 0; h < 2; ++h) la[h] = (lane & 31) * 64 + (((h * 2 + (lane >> 5)) ^ ((lane >> 1) & 3)) << 4);
+  v16i acc[TN][TM] = {};
+  v4i fa[2][TM], fw[2][TN];
+  auto read = [&](int buf, int h) {
+    const unsigned char* p = smem + buf * kStage + la[h];
+#pragma unroll
+    for (int j = 0; j < TM; ++j) fa[h][j] = *reinterpret_cast<const v4i*>(p + (wm + j * 32) * 64);
+#pragma unroll
+    for (int i = 0; i < TN; ++i) fw[h][i] = *reinterpret_cast<const v4i*>(p + (BM + wn + i * 32) * 64);
+  };
+  auto mult = [&](int h) {
+#pragma unroll
+    for (int i = 0; i < TN; ++i)
+#pragma unroll
+      for (int j = 0; j < TM; ++j) acc[i][j] = __builtin_amdgcn_mfma_i32_32x32x32_i8(fw[h][i], fa[h][j], acc[i][j], 0, 0, 0);
+  };
+  const int n = (a.K + 63) / 64;
+  constexpr int kIssue = RA + RW;
+#pragma unroll
+  for (int s = 0; s < NS; ++s) issue(s);
+  wait_vm<kIssue * (NS - 1)>();
+  __builtin_amdgcn_s_barrier();
+  compiler_fence();
+  read(0, 0);
+  for (int s = 0; s < n; ++s) {
+    read(s % NS, 1);
+    mult(0);
+    // this stage is read out and the next has landed, for every wave
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+    wait_vm<kIssue * (NS - 2)>();
+    __builtin_amdgcn_s_barrier();
+    compiler_fence();
+    issue(s + NS);
+    read((s + 1) % NS, 0);
+    mult(1);
+  }
+  wait_vm<0>();
+  __syncthreads();
+
+  // 32 tokens at a time through LDS, so that whole rows' pieces are stored
+  using T = typename Elem<OUT>::T;
+  constexpr int kCols = SWIGLU ? BN / 4 : BN / 2, kRow = kCols + 4, PER = 16 / sizeof(T);
+  static_assert(4 * 32 * kRow * 4 <= NS * kStage, "epilogue fits the stages");
+  float* buf = reinterpret_cast<float*>(smem) + wave * 32 * kRow;
+  const int nw = n0 + (SWIGLU ? wn / 2 : wn);
+  const bool vec = (reinterpret_cast<uintptr_t>(a.out) | (a.ldo * sizeof(T))) % 16 == 0 &&
+                   (!a.add || (reinterpret_cast<uintptr_t>(a.add) | (a.ldadd * sizeof(T))) % 16 == 0);
+#pragma unroll
+  for (int j = 0; j < TM; ++j) {
+    const int64_t mt = m0 + wm + j * 32, mrow = mt + (lane & 31);
+    const float sa = a.sa[mrow < a.M ? mrow : a.M - 1];
+#pragma unroll
+    for (int i = 0; i < TN; i += SWIGLU ? 2 : 1)
+#pragma unroll
+      for (int g = 0; g < 4; ++g) {
+        const int c = (SWIGLU ? i * 16 : i * 32) + g * 8 + (lane >> 5) * 4;
+        v4f y;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int col = nw + c + e < H ? nw + c + e : H - 1;
+          y[e] = static_cast<float>(acc[i][j][g * 4 + e]) * sa * a.sw[col] + (a.bias ? a.bias[col] : 0.0f);
+          if (SWIGLU)
+            y[e] = silu(y[e]) * (static_cast<float>(acc[i + (SWIGLU ? 1 : 0)][j][g * 4 + e]) * sa * a.sw[H + col] +
+                                 (a.bias ? a.bias[H + col] : 0.0f));
+        }
+        *reinterpret_cast<v4f*>(buf + (lane & 31) * kRow + c) = y;
+      }
+    __builtin_amdgcn_wave_barrier();
+    constexpr int kPieces = kCols / PER;  // 16-byte pieces of a row
+    for (int p = lane; p < 32 * kPieces; p += 64) {
+      const int row = p / kPieces, c = p % kPieces * PER, col = nw + c;
+      const int64_t m = mt + row;
+      if (m >= a.M || col >= H) continue;
+      float y[PER];
+#pragma unroll
+      for (int e = 0; e < PER; ++e) y[e] = buf[row * kRow + c + e];
+      T* out = static_cast<T*>(a.out) + m * a.ldo + col;
+      const T* add = static_cast<const T*>(a.add) + m * a.ldadd + col;
+      if (vec && col + PER <= H) {
+        T v[PER];
+        if (a.add) {
+          __builtin_memcpy(v, __builtin_assume_aligned(add, 16), 16);
+#pragma unroll
+          for (int e = 0; e < PER; ++e) y[e] += to_f32<OUT>(v[e]);
+        }
+#pragma unroll
+        for (int e = 0; e < PER; ++e) v[e] = from_f32<OUT>(y[e]);
+        __builtin_memcpy(__builtin_assume_aligned(out, 16), v, 16);
+      } else {
+        for (int e = 0; e < PER && col + e < H; ++e)
+          out[e] = from_f32<OUT>(a.add ? y[e] + to_f32<OUT>(add[e]) : y[e]);
+      }
+    }
+    __builtin_amdgcn_wave_barrier();
+  }
+}
 
 // Workgroup tile of 64 tokens x 64 weight rows, 128 bytes of K a step, through LDS.
 template <int OUT, bool SWIGLU>
@@ -440,12 +767,86 @@ void launch_route(const RouteArgs& a, hipStream_t st) {
   else hipLaunchKernelGGL((route_kernel<TYPE, SIG, 16>), grid, dim3(256), lds, st, a);
 }
 
-template <int OUT>
-void launch_linear(const LinearArgs& a, bool swiglu, hipStream_t st) {
+// Allow a kernel more than 64 KB of LDS, once per device.
+template <typename F>
+bool allow_lds(F fn, size_t bytes, std::atomic<uint64_t>& done) {
+  int dev = 0;
+  if (bytes <= 65536) return true;
+  if (hipGetDevice(&dev) != hipSuccess || dev < 0 || dev >= 64) return false;
+  if (done.load(std::memory_order_relaxed) >> dev & 1) return true;
+  if (hipFuncSetAttribute(reinterpret_cast<const void*>(fn), hipFuncAttributeMaxDynamicSharedMemorySize,
+                          static_cast<int>(bytes)) != hipSuccess)
+    return false;
+  done.fetch_or(1ull << dev, std::memory_order_relaxed);
+  return true;
+}
+
+template <int P, int TT, int ET, int WV>
+int launch_gate_tile(const GateArgs& a, hipStream_t st) {
+  static std::atomic<uint64_t> done{0};
+  constexpr size_t lds = sizeof(float) * WV * 16 * TT * (16 * ET + 4);
+  static_assert(lds <= 160 * 1024, "gate tile");
+  if (!allow_lds(gate_kernel<P, TT, ET, WV>, lds, done)) return MOE_EHIP;
+  const uint32_t cols = ((a.E + 15) / 16 + ET - 1) / ET, rows = static_cast<uint32_t>((a.B + 16 * TT - 1) / (16 * TT));
+  hipLaunchKernelGGL((gate_kernel<P, TT, ET, WV>), dim3((rows + 7) / 8 * 8 * cols), dim3(64 * WV), lds, st, a, cols,
+                     rows);
+  return launch_status();
+}
+
+template <int P>
+int launch_gate(const GateArgs& a, hipStream_t st) {
+  if (a.B <= 1024) return launch_gate_tile<P, 1, 1, 16>(a, st);
+  return launch_gate_tile<P, 4, 5, 4>(a, st);
+}
+
+template <int OUT, bool SWIGLU, bool ALIGNED, int TT, int WV>
+int launch_stream(const LinearArgs& a, hipStream_t st) {
+  static std::atomic<uint64_t> done{0};
+  constexpr size_t lds = sizeof(int) * WV * 16 * TT * ((SWIGLU ? 32 : 16) + 4);
+  if (!allow_lds(linear_stream_kernel<OUT, SWIGLU, ALIGNED, TT, WV>, lds, done)) return MOE_EHIP;
+  const int cols = SWIGLU ? a.N / 2 : a.N;
+  hipLaunchKernelGGL((linear_stream_kernel<OUT, SWIGLU, ALIGNED, TT, WV>), dim3((cols + 15) / 16), dim3(64 * WV), lds, st,
+                     a);
+  return launch_status();
+}
+
+template <int BM, int BN, int OUT, bool SWIGLU>
+int launch_dma(const LinearArgs& a, hipStream_t st) {
+  static std::atomic<uint64_t> done{0};
+  constexpr size_t lds = 4 * (BM + BN) * 64;
+  if (!allow_lds(linear_dma_kernel<BM, BN, OUT, SWIGLU>, lds, done)) return MOE_EHIP;
+  const uint32_t nm = static_cast<uint32_t>((a.M + BM - 1) / BM), bn = SWIGLU ? BN / 2 : BN,
+                 nn = static_cast<uint32_t>(((SWIGLU ? a.N / 2 : a.N) + bn - 1) / bn), per = (nm * nn + 7) / 8;
+  hipLaunchKernelGGL((linear_dma_kernel<BM, BN, OUT, SWIGLU>), dim3(per * 8), dim3(256), lds, st, a, nm, nn, per);
+  return launch_status();
+}
+
+template <int OUT, bool SWIGLU, bool ALIGNED>
+int launch_linear(const LinearArgs& a, hipStream_t st) {
+  if (a.M <= 16) return launch_stream<OUT, SWIGLU, ALIGNED, 1, 16>(a, st);
+  if (a.M <= 32) return launch_stream<OUT, SWIGLU, ALIGNED, 2, 8>(a, st);
+  if (a.M <= 64) return launch_stream<OUT, SWIGLU, ALIGNED, 4, 8>(a, st);
+  if constexpr (ALIGNED) {
+    // rounds of tiles over the CUs, weighed with the time of a tile
+    const int64_t cols = SWIGLU ? a.N / 2 : a.N;
+    auto rounds = [&](int bm, int bn) {
+      const int64_t b = SWIGLU ? bn / 2 : bn;
+      return (((a.M + bm - 1) / bm) * ((cols + b - 1) / b) + 255) / 256;
+    };
+    const int64_t big = rounds(256, 256) * 40, mid = rounds(128, 128) * 16;
+    if (big <= mid) return launch_dma<256, 256, OUT, SWIGLU>(a, st);
+    return launch_dma<128, 128, OUT, SWIGLU>(a, st);
+  }
   const unsigned my = static_cast<unsigned>((a.M + 63) / 64);
-  const unsigned nx = static_cast<unsigned>(swiglu ? (a.N / 2 + 31) / 32 : (a.N + 63) / 64);
-  if (swiglu) hipLaunchKernelGGL((linear_tile_kernel<OUT, true>), dim3(nx * my), dim3(256), 0, st, a, nx);
-  else hipLaunchKernelGGL((linear_tile_kernel<OUT, false>), dim3(nx * my), dim3(256), 0, st, a, nx);
+  const unsigned nx = static_cast<unsigned>(SWIGLU ? (a.N / 2 + 31) / 32 : (a.N + 63) / 64);
+  hipLaunchKernelGGL((linear_tile_kernel<OUT, SWIGLU>), dim3(nx * my), dim3(256), 0, st, a, nx);
+  return launch_status();
+}
+
+template <int OUT>
+int launch_linear(const LinearArgs& a, bool swiglu, bool aligned, hipStream_t st) {
+  if (aligned) return swiglu ? launch_linear<OUT, true, true>(a, st) : launch_linear<OUT, false, true>(a, st);
+  return swiglu ? launch_linear<OUT, true, false>(a, st) : launch_linear<OUT, false, false>(a, st);
 }
 
 }  // namespace
@@ -478,10 +879,7 @@ int moe_gate(const moe_gate_t* g, const void* x, int64_t ldx, int32_t B, float* 
     return MOE_EINVAL;
   const GateArgs a = {static_cast<const uint16_t*>(x), ldx,    static_cast<const uint16_t*>(g->packed), B, g->E, g->D,
                       logits,                          ldl};
-  const dim3 grid(static_cast<unsigned>((B + 63LL) / 64), ((g->E + 15) / 16 + 4) / 5);
-  if (g->wtype == MOE_F32) hipLaunchKernelGGL(gate_kernel<3>, grid, dim3(256), 0, as_stream(stream), a);
-  else hipLaunchKernelGGL(gate_kernel<1>, grid, dim3(256), 0, as_stream(stream), a);
-  return launch_status();
+  return g->wtype == MOE_F32 ? launch_gate<3>(a, as_stream(stream)) : launch_gate<1>(a, as_stream(stream));
 }
 
 int moe_route(const void* logits, int32_t type, int64_t ldl, int32_t B, int32_t E, int32_t topk,
@@ -539,11 +937,12 @@ int moe_linear_i8(const int8_t* a, int64_t lda, const float* sa, const int8_t* w
   const int32_t cols = o.act == 1 ? N / 2 : N;
   if (ldo < cols || (o.add_dev && o.ldadd < cols)) return MOE_EINVAL;
   const LinearArgs r = {a, w, sa, sw, o.bias_dev, o.add_dev, out, lda, ldw, ldo, o.ldadd, M, N, K};
+  const bool aligned =
+      (reinterpret_cast<uintptr_t>(a) | reinterpret_cast<uintptr_t>(w) | lda | ldw | static_cast<uintptr_t>(K)) % 16 == 0;
   hipStream_t st = as_stream(stream);
-  if (out_type == MOE_F32) launch_linear<MOE_F32>(r, o.act == 1, st);
-  else if (out_type == MOE_F16) launch_linear<MOE_F16>(r, o.act == 1, st);
-  else launch_linear<MOE_BF16>(r, o.act == 1, st);
-  return launch_status();
+  if (out_type == MOE_F32) return launch_linear<MOE_F32>(r, o.act == 1, aligned, st);
+  if (out_type == MOE_F16) return launch_linear<MOE_F16>(r, o.act == 1, aligned, st);
+  return launch_linear<MOE_BF16>(r, o.act == 1, aligned, st);
 }
 
 }  // extern "C"
