@@ -66,196 +66,349 @@ constexpr size_t elem_size(int type) { return type == MOE_F32 ? 4 : 2; }
 struct RouteArgs {
   const void* logits;
   int64_t ldl;
-  int32_t B, E, topk, groups, kept, group_score, renorm;
+  int32_t B, E, topk, type, sigmoid, groups, kept, sums, renorm;
   float scale;
   const float* bias;
   int32_t* ids;
   float* weights;
 };
 
-// One wave per token; lane l holds experts l, l + 64, ...  The choice stays in FP64.
-template <int TYPE, bool SIGMOID, int NV>
-__global__ __launch_bounds__(256) void route_kernel(RouteArgs a) {
-  extern __shared__ double route_lds[];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int64_t t = static_cast<int64_t>(blockIdx.x) * 4 + wave;
-  double* vals = route_lds + static_cast<size_t>(wave) * (a.E + 64);
-  double* rank = vals + a.E;
-  const bool live = t < a.B;
-  const double kNone = -__builtin_huge_val();
-  const typename Elem<TYPE>::T* row =
-      static_cast<const typename Elem<TYPE>::T*>(a.logits) + (live ? t : 0) * a.ldl;
-  float l[NV];
-  float m = -__builtin_huge_valf();
+// Order between the lanes of one wave through LDS.
+__device__ __forceinline__ void wave_sync() {
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+}
+template <int N>
+__device__ __forceinline__ uint32_t rotate_row(uint32_t v) {  // among 16 lanes
+  return static_cast<uint32_t>(__builtin_amdgcn_update_dpp(0, static_cast<int>(v), 0x120 + N, 0xf, 0xf, false));
+}
+template <int LPT>
+__device__ __forceinline__ uint32_t lanes_max(uint32_t v) {
+  auto up = [&](uint32_t o) { v = o > v ? o : v; };
+  up(rotate_row<8>(v));
+  up(rotate_row<4>(v));
+  up(rotate_row<2>(v));
+  up(rotate_row<1>(v));
+  if constexpr (LPT == 64) {
+    uint32_t r = 0;
 #pragma unroll
-  for (int j = 0; j < NV; ++j) {
-    const int e = lane + 64 * j;
-    float v = -__builtin_huge_valf();
-    if (e < a.E) {
-      v = to_f32<TYPE>(row[e]);
-      if (v != v) v = -__builtin_huge_valf();
+    for (int i = 0; i < 64; i += 16) {
+      const uint32_t o = static_cast<uint32_t>(__builtin_amdgcn_readlane(static_cast<int>(v), i));
+      r = o > r ? o : r;
     }
-    l[j] = v;
-    m = fmaxf(m, v);
+    return r;
   }
+  return v;
+}
+template <int LPT>
+__device__ __forceinline__ double lanes_sum(double v) {
 #pragma unroll
-  for (int d = 32; d; d >>= 1) m = fmaxf(m, __shfl_xor(m, d));
-  auto score_of = [&](float v) -> double {  // softmax: without the common denominator
-    if (v == -__builtin_huge_valf()) return 0.0;
-    if (SIGMOID) return 1.0 / (1.0 + exp(-static_cast<double>(v)));
-    return v == m ? 1.0 : exp(static_cast<double>(v) - static_cast<double>(m));
+  for (int d = LPT / 2; d; d >>= 1) v += __shfl_xor(v, d);
+  return v;
+}
+// Bits of a number as an unsigned word that orders as the number does.
+__device__ __forceinline__ uint32_t ordered(float f) {
+  const uint32_t u = __float_as_uint(f);
+  return u ^ (static_cast<uint32_t>(static_cast<int32_t>(u) >> 31) | 0x80000000u);
+}
+__device__ __forceinline__ float unordered(uint32_t u) {
+  return __uint_as_float(u ^ (u >> 31 ? 0x80000000u : 0xffffffffu));
+}
+__device__ __forceinline__ uint64_t ordered(double f) {
+  const uint64_t u = static_cast<uint64_t>(__double_as_longlong(f));
+  return u ^ (static_cast<uint64_t>(static_cast<int64_t>(u) >> 63) | 0x8000000000000000ull);
+}
+// exp within about a step: 2^n exp(r), |r| <= ln(2) / 2, exp(r) by its series to r^13 / 13!
+// (the next term is below 2^-57).
+__device__ __forceinline__ double exp_f64(double x) {
+  x = __builtin_fmin(__builtin_fmax(x, -800.0), 800.0);
+  const double n = __builtin_rint(x * 1.4426950408889634);
+  double r = __builtin_fma(n, -2977044471.0 / 4294967296.0, x);  // ln 2 cut at 2^-32: n times it is exact
+  r = __builtin_fma(n, -1.9082149292705877e-10, r);  // and the rest
+  double p = 1.0 / 6227020800.0;
+  p = __builtin_fma(p, r, 1.0 / 479001600.0);
+  p = __builtin_fma(p, r, 1.0 / 39916800.0);
+  p = __builtin_fma(p, r, 1.0 / 3628800.0);
+  p = __builtin_fma(p, r, 1.0 / 362880.0);
+  p = __builtin_fma(p, r, 1.0 / 40320.0);
+  p = __builtin_fma(p, r, 1.0 / 5040.0);
+  p = __builtin_fma(p, r, 1.0 / 720.0);
+  p = __builtin_fma(p, r, 1.0 / 120.0);
+  p = __builtin_fma(p, r, 1.0 / 24.0);
+  p = __builtin_fma(p, r, 1.0 / 6.0);
+  p = __builtin_fma(p, r, 0.5);
+  p = __builtin_fma(p, r, 1.0);
+  p = __builtin_fma(p, r, 1.0);
+  return __builtin_ldexp(p, static_cast<int>(n));
+}
+
+// LPT lanes per token, lane l of them holding experts l, l + LPT, ..., NV of them at most.
+// Each lane sorts its choices (stably, so that equal ones stay in index order) into LDS; then
+// the lanes' heads compete topk times: the largest upper word by rotations among the lanes,
+// and only where several lanes share it the lower word and the index.
+template <int LPT, int NV>
+__global__ __launch_bounds__(256) void route_kernel(RouteArgs a) {
+  constexpr int TPW = 64 / LPT;
+  __shared__ uint64_t lds_key[4][NV][64];
+  __shared__ uint16_t lds_id[4][NV][64];
+  __shared__ uint16_t lds_out[4][TPW][64];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, l = lane % LPT, sub = lane / LPT;
+  const int64_t tok = (static_cast<int64_t>(blockIdx.x) * 4 + wave) * TPW + sub, t = tok < a.B ? tok : a.B - 1;
+  const float kMasked = -__builtin_huge_valf();
+  const double kNone = -__builtin_huge_val();
+  auto logit_at = [&](int e) {
+    const int64_t i = t * a.ldl + e;
+    float v;
+    if (a.type == MOE_F32) v = static_cast<const float*>(a.logits)[i];
+    else if (a.type == MOE_F16) v = f16_to_f32(static_cast<const uint16_t*>(a.logits)[i]);
+    else v = bf16_to_f32(static_cast<const uint16_t*>(a.logits)[i]);
+    return v == v ? v : kMasked;
   };
-  double denom = 1.0;
-  if (!SIGMOID && (!a.renorm || a.bias)) {
-    denom = 0.0;
-#pragma unroll
-    for (int j = 0; j < NV; ++j) denom += score_of(l[j]);
-#pragma unroll
-    for (int d = 32; d; d >>= 1) denom += __shfl_xor(denom, d);
-    if (denom < 1.0) denom = 1.0;  // every expert masked
-  }
-  double c[NV];
+  float x[NV], m = kMasked;
 #pragma unroll
   for (int j = 0; j < NV; ++j) {
-    const int e = lane + 64 * j;
-    double v = l[j];
-    if (a.bias && e < a.E) v = score_of(l[j]) / denom + static_cast<double>(a.bias[e]);
-    if (l[j] == -__builtin_huge_valf() || v != v) v = kNone;
-    c[j] = v;
+    const int e = l + LPT * j;
+    x[j] = e < a.E ? logit_at(e) : kMasked;
   }
-  bool taken[NV];
 #pragma unroll
-  for (int j = 0; j < NV; ++j) taken[j] = lane + 64 * j >= a.E;
+  for (int j = 0; j < NV; ++j) m = fmaxf(m, x[j]);
+  m = unordered(lanes_max<LPT>(ordered(m)));
+  auto score_of = [&](float v) -> double {  // softmax: without the common denominator
+    if (v == kMasked) return 0.0;
+    if (a.sigmoid) return 1.0 / (1.0 + exp_f64(-static_cast<double>(v)));
+    return v == m ? 1.0 : exp_f64(static_cast<double>(v) - static_cast<double>(m));
+  };
+  // the choice needs no score without a bias, but a sum of two does
+  const bool scored = a.bias || (a.groups && a.sums);
+  double c[NV], inv = 1.0;
+  if (scored) {
+#pragma unroll
+    for (int j = 0; j < NV; ++j) c[j] = score_of(x[j]);
+  }
+  if (!a.sigmoid && (a.bias || !a.renorm)) {
+    double d = 0.0;
+#pragma unroll
+    for (int j = 0; j < NV; ++j) d += scored ? c[j] : score_of(x[j]);
+    d = lanes_sum<LPT>(d);
+    inv = d > 0.0 ? 1.0 / d : 1.0;  // 0: every expert masked
+  }
+  uint64_t key[NV];
+  double* const vals = reinterpret_cast<double*>(lds_key[wave]) + sub * a.E;
+#pragma unroll
+  for (int j = 0; j < NV; ++j) {
+    const int e = l + LPT * j;
+    double v = x[j];
+    if (a.bias) v = c[j] * inv + static_cast<double>(e < a.E ? a.bias[e] : 0.0f);
+    if (x[j] == kMasked || v != v) v = kNone;
+    if (a.groups && e < a.E) vals[e] = scored && !a.bias && v != kNone ? c[j] : v;
+    key[j] = e < a.E ? ordered(v + 0.0) : 0;  // one zero; 0: not there
+  }
   if (a.groups) {
     const int size = a.E / a.groups;
-    const bool sums = a.group_score == 1;
-#pragma unroll
-    for (int j = 0; j < NV; ++j) {
-      const int e = lane + 64 * j;
-      if (e < a.E) vals[e] = sums && !a.bias && c[j] != kNone ? score_of(l[j]) / denom : c[j];
-    }
-    __syncthreads();
-    double r = kNone;
-    if (lane < a.groups) {
-      double v1 = kNone, v2 = kNone;
+    wave_sync();
+    double v1 = kNone, v2 = kNone;
+    if (l < a.groups)
       for (int i = 0; i < size; ++i) {
-        const double v = vals[lane * size + i];
-        if (v > v1) {
-          v2 = v1;
-          v1 = v;
-        } else if (v > v2) {
-          v2 = v;
-        }
+        const double v = vals[l * size + i];
+        v2 = v > v1 ? v1 : v > v2 ? v : v2;
+        v1 = v > v1 ? v : v1;
       }
-      r = sums && v2 != kNone ? v1 + v2 : v1;
-      rank[lane] = r;
+    const double r = a.sums && v2 != kNone ? v1 + v2 : v1;
+    wave_sync();
+    if (l < a.groups) vals[l] = r;
+    wave_sync();
+    int before = 0;
+    for (int g = 0; g < a.groups; ++g) {
+      const double o = vals[g];
+      before += o > r || (o == r && g < l);
     }
-    __syncthreads();
-    bool keep = false;
-    if (lane < a.groups) {
-      int before = 0;
-      for (int g = 0; g < a.groups; ++g) before += rank[g] > r || (rank[g] == r && g < lane);
-      keep = before < a.kept;
-    }
-    const uint64_t kept = __ballot(keep);
+    const uint64_t kept = __ballot(l < a.groups && before < a.kept) >> (LPT == 64 ? 0 : sub * LPT);
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-      const int e = lane + 64 * j;
-      if (e < a.E && !((kept >> (e / size)) & 1)) taken[j] = true;
+      const int e = l + LPT * j;
+      if (e < a.E && !((kept >> (e / size)) & 1)) key[j] = 0;
     }
+    wave_sync();
   }
-  int my_id = 0;
-  float my_logit = -__builtin_huge_valf();
+  uint32_t id[NV];
+#pragma unroll
+  for (int j = 0; j < NV; ++j) id[j] = l + LPT * j;
+#pragma unroll
+  for (int round = 0; round < NV; ++round)
+#pragma unroll
+    for (int j = round & 1; j + 1 < NV; j += 2) {
+      const bool swap = key[j] < key[j + 1];
+      const uint64_t k0 = key[j], k1 = key[j + 1];
+      const uint32_t i0 = id[j], i1 = id[j + 1];
+      key[j] = swap ? k1 : k0;
+      key[j + 1] = swap ? k0 : k1;
+      id[j] = swap ? i1 : i0;
+      id[j + 1] = swap ? i0 : i1;
+    }
+#pragma unroll
+  for (int j = 1; j < NV; ++j) {
+    lds_key[wave][j][lane] = key[j];
+    lds_id[wave][j][lane] = static_cast<uint16_t>(id[j]);
+  }
+  uint64_t head = key[0];
+  uint32_t head_id = id[0];
+  int next = 1;
   for (int k = 0; k < a.topk; ++k) {
-    double bv = kNone;
-    int bi = 0x7fffffff;
-    float bl = -__builtin_huge_valf();
-#pragma unroll
-    for (int j = 0; j < NV; ++j)
-      if (!taken[j] && (bi == 0x7fffffff || c[j] > bv)) {
-        bv = c[j];
-        bi = lane + 64 * j;
-        bl = l[j];
-      }
-#pragma unroll
-    for (int d = 32; d; d >>= 1) {
-      const double ov = __shfl_xor(bv, d);
-      const int oi = __shfl_xor(bi, d);
-      const float ol = __shfl_xor(bl, d);
-      if (ov > bv || (ov == bv && oi < bi)) {
-        bv = ov;
-        bi = oi;
-        bl = ol;
+    const uint32_t hi = static_cast<uint32_t>(head >> 32), lo = static_cast<uint32_t>(head);
+    bool win = hi == lanes_max<LPT>(hi);
+    // (the maxima are taken by all lanes, outside any condition on `win`)
+    if (__popcll(__ballot(win)) != TPW) {
+      const uint32_t top = lanes_max<LPT>(win ? lo : 0u);
+      win &= lo == top;
+      if (__popcll(__ballot(win)) != TPW) {
+        const uint32_t first = lanes_max<LPT>(win ? ~head_id : 0u);
+        win &= ~head_id == first;
       }
     }
-#pragma unroll
-    for (int j = 0; j < NV; ++j)
-      if (lane + 64 * j == bi) taken[j] = true;
-    if (lane == k) {
-      my_id = bi;
-      my_logit = bl;
+    if (win) {
+      lds_out[wave][sub][k] = static_cast<uint16_t>(head_id);
+      head = next < NV ? lds_key[wave][next][lane] : 0;
+      head_id = next < NV ? lds_id[wave][next][lane] : 0;
+      ++next;
     }
   }
-  double w = lane < a.topk ? score_of(my_logit) : 0.0;
+  wave_sync();
+  constexpr int KP = 64 / LPT;  // selected experts per lane
+  double w[KP], total = 0.0;
+#pragma unroll
+  for (int i = 0; i < KP; ++i) {
+    const int k = l + LPT * i;
+    w[i] = 0.0;
+    if (k < a.topk) {
+      const int e = lds_out[wave][sub][k];
+      w[i] = score_of(logit_at(e));
+      if (tok < a.B) a.ids[t * a.topk + k] = e;
+    }
+    total += w[i];
+  }
   if (a.renorm) {
-    double total = w;
-#pragma unroll
-    for (int d = 32; d; d >>= 1) total += __shfl_xor(total, d);
-    w = total > 0.0 ? w / total : 0.0;
-  } else {
-    w /= denom;
+    total = lanes_sum<LPT>(total);
+    inv = total > 0.0 ? 1.0 / total : 0.0;
   }
-  if (live && lane < a.topk) {
-    a.ids[t * a.topk + lane] = my_id;
-    a.weights[t * a.topk + lane] = static_cast<float>(w * static_cast<double>(a.scale));
+#pragma unroll
+  for (int i = 0; i < KP; ++i) {
+    const int k = l + LPT * i;
+    if (k < a.topk && tok < a.B) a.weights[t * a.topk + k] = static_cast<float>(w[i] * inv * static_cast<double>(a.scale));
   }
 }
 
 // --------------------------------------------------------------------- quant
-// One workgroup per token: the row's largest magnitude, then the codes.
-// code = x * 127 / amax, half to even, exactly: x * 127 - r * amax is exact in FP64, so the
-// rounded guess r is corrected by comparing it with half a step.
-__device__ __forceinline__ int quant_code(double x, double amax, double inv) {
-  const double n = x * 127.0;
-  double r = __builtin_rint(n * inv);
-  const double d = 2.0 * (n - r * amax);
-  const bool odd = (static_cast<int>(r) & 1) != 0;
-  if (d > amax || (d == amax && odd)) r += 1.0;
-  else if (d < -amax || (d == -amax && odd)) r -= 1.0;
-  return static_cast<int>(r);
+// code = x * 127 / amax, half to even, exactly.  Both are first scaled by the power of two
+// that brings amax into [1, 2), exactly but for values whose code is 0.  In BF16 and FP16, x * 127 and x * 127 - r * amax
+// are exact in FP32, and a quotient that is no half lies 2^-12 or more away from one, far
+// beyond the guess's error: only exact halves need the remainder.  FP32 goes through FP64.
+struct QuantScale {
+  int exp;
+  float amax, inv;  // scaled; 127 / amax
+};
+template <int TYPE>
+__device__ __forceinline__ int quant_code(float x, const QuantScale& q) {
+  const float xs = __builtin_ldexpf(x, -q.exp);
+  if constexpr (TYPE == MOE_F32) {
+    const double n = static_cast<double>(xs) * 127.0, amax = static_cast<double>(q.amax);
+    const float r0 = __builtin_rintf(xs * q.inv);
+    const double d = 2.0 * __builtin_fma(-static_cast<double>(r0), amax, n);
+    const int r = static_cast<int>(r0);
+    const double far = __builtin_fabs(d);
+    return far > amax || (far == amax && (r & 1)) ? r + (d > 0.0 ? 1 : -1) : r;
+  } else {
+    const float r0 = __builtin_rintf(xs * q.inv);
+    const float d = __builtin_fmaf(-r0, q.amax, xs * 127.0f);
+    const int r = static_cast<int>(r0);
+    return 2.0f * __builtin_fabsf(d) == q.amax && (r & 1) ? r + (d > 0.0f ? 1 : -1) : r;
+  }
 }
 
-template <int TYPE>
+// W waves per token, which they hold in registers: NV 16-byte pieces a lane (NV 0: any length,
+// the row is read twice).  One pass over the data: bytes bound it.
+template <int TYPE, int W, int NV>
 __global__ __launch_bounds__(256) void quant_kernel(const void* x, int64_t ldx, int32_t M, int32_t K,
                                                     int8_t* codes, int64_t ldc, float* scales) {
+  using T = typename Elem<TYPE>::T;
+  constexpr int VE = 16 / sizeof(T), HELD = NV ? NV : 1;
   __shared__ uint32_t part[4];
-  const int64_t row = blockIdx.x;
-  const typename Elem<TYPE>::T* p = static_cast<const typename Elem<TYPE>::T*>(x) + row * ldx;
-  uint32_t top = 0;  // magnitudes order as their bits, infinity and NaN above all
-  for (int k = threadIdx.x; k < K; k += 256) {
-    const uint32_t b = __float_as_uint(to_f32<TYPE>(p[k])) & 0x7fffffffu;
-    top = b > top ? b : top;
-  }
-#pragma unroll
-  for (int d = 32; d; d >>= 1) {
-    const uint32_t o = static_cast<uint32_t>(__shfl_xor(static_cast<int>(top), d));
-    top = o > top ? o : top;
-  }
-  if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = top;
-  __syncthreads();
-  for (int i = 0; i < 4; ++i) top = part[i] > top ? part[i] : top;
-  const float amax = __uint_as_float(top);
-  const bool finite = top < 0x7f800000u;
+  const int lane = threadIdx.x % (64 * W), wave = threadIdx.x >> 6;
+  const int64_t row = static_cast<int64_t>(blockIdx.x) * (4 / W) + threadIdx.x / (64 * W);
+  if (W == 1 && row >= M) return;
+  const T* p = static_cast<const T*>(x) + row * ldx;
   int8_t* q = codes + row * ldc;
-  if (top == 0 || !finite) {
-    for (int k = threadIdx.x; k < K; k += 256) q[k] = 0;
-    if (threadIdx.x == 0) scales[row] = finite ? 0.0f : __builtin_nanf("");
-    return;
+  const int pieces = (K + VE - 1) / VE;
+  struct Piece {
+    T v[VE];
+  };
+  auto load = [&](int i) {  // any alignment; zeros behind K
+    Piece r;
+    if ((i + 1) * VE <= K) {
+      __builtin_memcpy(&r, p + i * VE, 16);
+    } else {
+#pragma unroll
+      for (int e = 0; e < VE; ++e) r.v[e] = i * VE + e < K ? p[i * VE + e] : T(0);
+    }
+    return r;
+  };
+  uint32_t top = 0;  // magnitudes order as their bits, infinity and NaN above all
+  auto raise = [&](const Piece& r) {
+#pragma unroll
+    for (int e = 0; e < VE; ++e) {
+      const uint32_t b = __float_as_uint(to_f32<TYPE>(r.v[e])) & 0x7fffffffu;
+      top = b > top ? b : top;
+    }
+  };
+  Piece held[HELD];
+  if constexpr (NV > 0) {
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      const int i = lane + 64 * W * j;
+      if (i < pieces) held[j] = load(i);
+    }
+#pragma unroll
+    for (int j = 0; j < NV; ++j)
+      if (lane + 64 * W * j < pieces) raise(held[j]);
+  } else {
+    for (int i = lane; i < pieces; i += 64 * W) raise(load(i));
   }
-  const double inv = 1.0 / static_cast<double>(amax);
-  for (int k = threadIdx.x; k < K; k += 256)
-    q[k] = static_cast<int8_t>(quant_code(static_cast<double>(to_f32<TYPE>(p[k])), static_cast<double>(amax), inv));
-  if (threadIdx.x == 0) scales[row] = amax / 127.0f;
+  top = lanes_max<64>(top);
+  if constexpr (W > 1) {
+    if ((threadIdx.x & 63) == 0) part[wave] = top;
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < 4; ++i) top = part[i] > top ? part[i] : top;
+  }
+  const float amax = __uint_as_float(top);
+  const bool finite = top < 0x7f800000u, some = top != 0 && finite;
+  QuantScale s = {0, 1.0f, 0.0f};
+  if (some) {
+    s.exp = __builtin_amdgcn_frexp_expf(amax) - 1;
+    s.amax = __builtin_ldexpf(amax, -s.exp);
+    s.inv = 127.0f / s.amax;
+  }
+  auto store = [&](int i, const Piece& r) {
+    int8_t c[VE];
+#pragma unroll
+    for (int e = 0; e < VE; ++e) c[e] = some ? static_cast<int8_t>(quant_code<TYPE>(to_f32<TYPE>(r.v[e]), s)) : 0;
+    if ((i + 1) * VE <= K) {
+      __builtin_memcpy(q + i * VE, c, VE);
+    } else {
+#pragma unroll
+      for (int e = 0; e < VE; ++e)
+        if (i * VE + e < K) q[i * VE + e] = c[e];
+    }
+  };
+  if constexpr (NV > 0) {
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      const int i = lane + 64 * W * j;
+      if (i < pieces) store(i, held[j]);
+    }
+  } else {
+    for (int i = lane; i < pieces; i += 64 * W) store(i, load(i));
+  }
+  if (lane == 0) scales[row] = finite ? amax / 127.0f : __builtin_nanf("");
 }
 
 // ---------------------------------------------------------------------- gate
@@ -417,7 +570,8 @@ __device__ __forceinline__ uint4 row16(const int8_t* row, int k, int K, bool liv
 __device__ __forceinline__ v4i bits(uint4 v) {
   return v4i{static_cast<int>(v.x), static_cast<int>(v.y), static_cast<int>(v.z), static_cast<int>(v.w)};
 }
-__device__ __forceinline__ float silu(float g) { return g / (1.0f + __expf(-g)); }
+// g / (1 + exp(-g)) with the hardware's exp2 and reciprocal (an ulp each).
+__device__ __forceinline__ float silu(float g) { return g * __builtin_amdgcn_rcpf(1.0f + __expf(-g)); }
 
 // ------------------------------------------------- linear: up to 64 tokens
 // The weight is read once, so its bytes bound the product.  A workgroup takes 16 weight rows
@@ -537,12 +691,14 @@ __device__ __forceinline__ void wait_vm() {
 // MFMAs with the weight as the row operand (a lane then holds four neighbouring columns of out).
 // K goes through LDS in stages of 64 bytes a row, four in flight; a row's four 16-byte parts lie
 // permuted by its index, so that eight neighbouring rows' reads meet all banks once.
-template <int BM, int BN, int OUT, bool SWIGLU>
-__global__ __launch_bounds__(256, BM * BN >= 65536 ? 1 : 2) void linear_dma_kernel(LinearArgs a, uint32_t nm,
-                                                                                   uint32_t nn, uint32_t per_xcd) {
+template <int BM, int BN, int WM, int WN, int NS, int OUT, bool SWIGLU>
+__global__ __launch_bounds__(64 * WM * WN, BM * BN >= 65536 ? 1 : 2) void linear_dma_kernel(LinearArgs a, uint32_t nm,
+                                                                                            uint32_t nn,
+                                                                                            uint32_t per_xcd) {
   extern __shared__ __attribute__((aligned(16))) unsigned char smem[];
-  constexpr int NS = 4, kStage = (BM + BN) * 64, RA = BM / 64, RW = BN / 64;
-  static_assert(!SWIGLU || BN >= 128, "a wave holds whole gate and up pairs");
+  constexpr int kStage = (BM + BN) * 64, RA = BM / 16 / (WM * WN), RW = BN / 16 / (WM * WN);
+  constexpr int TM = BM / WM / 32, TN = BN / WN / 32;
+  static_assert(!SWIGLU || TN % 2 == 0, "a wave holds whole gate and up pairs");
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   // each XCD (workgroups go round the eight) takes a contiguous range of tiles, in groups of
   // eight token tiles: what runs at once on an XCD shares operands in its L2
@@ -554,7 +710,7 @@ __global__ __launch_bounds__(256, BM * BN >= 65536 ? 1 : 2) void linear_dma_kern
   const uint32_t lds0 = static_cast<uint32_t>(reinterpret_cast<uintptr_t>((__attribute__((address_space(3))) void*)smem));
 
   // what this lane moves: 16-byte part `ch` of rows lane / 4 of its wave's 16-row blocks
-  const int ch = (lane & 3) ^ ((lane >> 3) & 3), lr = lane >> 2;
+  const int ch = (lane & 3) ^ (lane >> 4), lr = lane >> 2;
   const int mrows = a.M - m0 < BM ? static_cast<int>(a.M - m0) : BM;
   const v4i ra = make_rsrc(a.a + m0 * a.lda, static_cast<uint32_t>((mrows - 1) * a.lda + a.K));
   uint32_t va[RA], vw[RW];
@@ -575,86 +731,130 @@ __global__ __launch_bounds__(256, BM * BN >= 65536 ? 1 : 2) void linear_dma_kern
       vw[i] = row < nrows ? static_cast<uint32_t>(row * a.ldw) + ch * 16 : kOutside;
     }
   }
-  auto issue = [&](int s) {
+  // parts behind K, and whole stages behind it, are zeros
+  auto issue_a = [&](int s, int buf, int i) {
     const int k0 = s * 64;
-    const uint32_t dst = lds0 + (s % NS) * kStage;
-    const bool in_k = k0 + ch * 16 < a.K;  // parts behind K, and whole stages behind it: zeros
-#pragma unroll
-    for (int i = 0; i < RA; ++i) dma16(ra, in_k ? va[i] : kOutside, k0, dst + (wave * RA + i) * 1024);
-#pragma unroll
-    for (int i = 0; i < RW; ++i) dma16(rw[i], in_k ? vw[i] : kOutside, k0, dst + BM * 64 + (wave * RW + i) * 1024);
+    dma16(ra, k0 + ch * 16 < a.K ? va[i] : kOutside, k0, lds0 + buf + (wave * RA + i) * 1024);
+  };
+  auto issue_w = [&](int s, int buf, int i) {
+    const int k0 = s * 64;
+    dma16(rw[i], k0 + ch * 16 < a.K ? vw[i] : kOutside, k0, lds0 + buf + BM * 64 + (wave * RW + i) * 1024);
   };
 
-  const int wm = (wave & 1) * (BM / 2), wn = (wave >> 1) * (BN / 2);
-  constexpr int TM = BM / 64, TN = BN / 64;
+  const int wm = wave % WM * (BM / WM), wn = wave / WM * (BN / WN);
   uint32_t la[2];  // this lane's operand inside a 32-row tile, for the stage's two halves
 #pragma unroll
-  for (int h = 0; h < 2; ++h) la[h] = (lane & 31) * 64 + (((h * 2 + (lane >> 5)) ^ ((lane >> 1) & 3)) << 4);
+  for (int h = 0; h < 2; ++h) la[h] = (lane & 31) * 64 + (((h * 2 + (lane >> 5)) ^ ((lane >> 2) & 3)) << 4);
   v16i acc[TN][TM] = {};
   v4i fa[2][TM], fw[2][TN];
-  auto read = [&](int buf, int h) {
-    const unsigned char* p = smem + buf * kStage + la[h];
+  // the TM + TN reads of a half stage, `part` of them in each of the first groups of MFMAs
+  auto read = [&](int buf, int h, int from, int to) {
+    const unsigned char* p = smem + buf + la[h];
 #pragma unroll
-    for (int j = 0; j < TM; ++j) fa[h][j] = *reinterpret_cast<const v4i*>(p + (wm + j * 32) * 64);
-#pragma unroll
-    for (int i = 0; i < TN; ++i) fw[h][i] = *reinterpret_cast<const v4i*>(p + (BM + wn + i * 32) * 64);
+    for (int f = from; f < to && f < TM + TN; ++f) {
+      if (f < TM) fa[h][f] = *reinterpret_cast<const v4i*>(p + (wm + f * 32) * 64);
+      else fw[h][f - TM] = *reinterpret_cast<const v4i*>(p + (BM + wn + (f - TM) * 32) * 64);
+    }
   };
-  auto mult = [&](int h) {
+  auto mult = [&](int h, int i, auto&& issue) {
 #pragma unroll
-    for (int i = 0; i < TN; ++i)
-#pragma unroll
-      for (int j = 0; j < TM; ++j) acc[i][j] = __builtin_amdgcn_mfma_i32_32x32x32_i8(fw[h][i], fa[h][j], acc[i][j], 0, 0, 0);
+    for (int j = 0; j < TM; ++j) {
+      acc[i][j] = __builtin_amdgcn_mfma_i32_32x32x32_i8(fw[h][i], fa[h][j], acc[i][j], 0, 0, 0);
+      if (j == 0) issue();
+    }
   };
   const int n = (a.K + 63) / 64;
-  constexpr int kIssue = RA + RW;
+  // scales and bias of the tile, behind the stages, in the order of its rows
+  float* const sw = reinterpret_cast<float*>(smem + NS * kStage);
+  float* const bias = sw + BN;
+  float* const sa = bias + BN;
+  constexpr int kIssue = RA + RW, kPart = TN > 1 ? (TM + TN) / (TN / 2) : TM + TN;
 #pragma unroll
-  for (int s = 0; s < NS; ++s) issue(s);
-  wait_vm<kIssue * (NS - 1)>();
+  for (int s = 0; s < NS; ++s) {
+#pragma unroll
+    for (int i = 0; i < RA; ++i) issue_a(s, s * kStage, i);
+    if (s < NS - 1) {
+#pragma unroll
+      for (int i = 0; i < RW; ++i) issue_w(s, s * kStage, i);
+    }
+  }
+  for (int r = threadIdx.x; r < BN; r += 64 * WM * WN) {
+    const int c = n0 + (SWIGLU ? (r >> 6) * 32 + (r & 31) : r), row = c + (SWIGLU ? ((r >> 5) & 1) * H : 0);
+    sw[r] = c < H ? a.sw[row] : 0.0f;
+    bias[r] = c < H && a.bias ? a.bias[row] : 0.0f;
+  }
+  for (int r = threadIdx.x; r < BM; r += 64 * WM * WN) sa[r] = r < mrows ? a.sa[m0 + r] : 0.0f;
+  wait_vm<kIssue * (NS - 2) + RA>();
+  asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
   __builtin_amdgcn_s_barrier();
   compiler_fence();
-  read(0, 0);
+  read(0, 0, 0, TM + TN);
+  compiler_fence();
+  // Each half of a stage multiplies what the half before read, a row of MFMAs at a time; reads of
+  // the next half and DMA issues (which hold a wave up for some 90 cycles each) go between the
+  // rows, in the order written.
+  int prev = (NS - 1) * kStage, cur = 0;  // LDS offsets of stages s - 1 and s
   for (int s = 0; s < n; ++s) {
-    read(s % NS, 1);
-    mult(0);
+#pragma unroll
+    for (int i = 0; i < TN; ++i) {
+      read(cur, 1, i * kPart, (i + 1) * kPart);
+      mult(0, i, [&] {
+#pragma unroll
+        for (int d = i * RW / TN; d < (i + 1) * RW / TN; ++d) issue_w(s + NS - 1, prev, d);
+      });
+      __builtin_amdgcn_sched_barrier(0);
+    }
     // this stage is read out and the next has landed, for every wave
     asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
     wait_vm<kIssue * (NS - 2)>();
     __builtin_amdgcn_s_barrier();
     compiler_fence();
-    issue(s + NS);
-    read((s + 1) % NS, 0);
-    mult(1);
+    __builtin_amdgcn_sched_barrier(0);
+    const int next = cur + kStage == NS * kStage ? 0 : cur + kStage;
+#pragma unroll
+    for (int i = 0; i < TN; ++i) {
+      read(next, 0, i * kPart, (i + 1) * kPart);
+      mult(1, i, [&] {
+#pragma unroll
+        for (int d = i * RA / TN; d < (i + 1) * RA / TN; ++d) issue_a(s + NS, cur, d);
+      });
+      __builtin_amdgcn_sched_barrier(0);
+    }
+    prev = cur;
+    cur = next;
+    compiler_fence();
   }
   wait_vm<0>();
   __syncthreads();
 
   // 32 tokens at a time through LDS, so that whole rows' pieces are stored
   using T = typename Elem<OUT>::T;
-  constexpr int kCols = SWIGLU ? BN / 4 : BN / 2, kRow = kCols + 4, PER = 16 / sizeof(T);
-  static_assert(4 * 32 * kRow * 4 <= NS * kStage, "epilogue fits the stages");
+  constexpr int kCols = SWIGLU ? TN * 16 : TN * 32, kRow = kCols + 4, PER = 16 / sizeof(T);
+  static_assert(WM * WN * 32 * kRow * 4 <= NS * kStage, "epilogue fits the stages");
   float* buf = reinterpret_cast<float*>(smem) + wave * 32 * kRow;
   const int nw = n0 + (SWIGLU ? wn / 2 : wn);
   const bool vec = (reinterpret_cast<uintptr_t>(a.out) | (a.ldo * sizeof(T))) % 16 == 0 &&
                    (!a.add || (reinterpret_cast<uintptr_t>(a.add) | (a.ldadd * sizeof(T))) % 16 == 0);
 #pragma unroll
   for (int j = 0; j < TM; ++j) {
-    const int64_t mt = m0 + wm + j * 32, mrow = mt + (lane & 31);
-    const float sa = a.sa[mrow < a.M ? mrow : a.M - 1];
+    const int64_t mt = m0 + wm + j * 32;
+    const float scale = sa[wm + j * 32 + (lane & 31)];
 #pragma unroll
     for (int i = 0; i < TN; i += SWIGLU ? 2 : 1)
 #pragma unroll
       for (int g = 0; g < 4; ++g) {
-        const int c = (SWIGLU ? i * 16 : i * 32) + g * 8 + (lane >> 5) * 4;
+        const int r = g * 8 + (lane >> 5) * 4, row = wn + i * 32 + r;
+        const v4f ws = *reinterpret_cast<const v4f*>(sw + row), wb = *reinterpret_cast<const v4f*>(bias + row);
         v4f y;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const int col = nw + c + e < H ? nw + c + e : H - 1;
-          y[e] = static_cast<float>(acc[i][j][g * 4 + e]) * sa * a.sw[col] + (a.bias ? a.bias[col] : 0.0f);
-          if (SWIGLU)
-            y[e] = silu(y[e]) * (static_cast<float>(acc[i + (SWIGLU ? 1 : 0)][j][g * 4 + e]) * sa * a.sw[H + col] +
-                                 (a.bias ? a.bias[H + col] : 0.0f));
+        for (int e = 0; e < 4; ++e) y[e] = static_cast<float>(acc[i][j][g * 4 + e]) * scale * ws[e] + wb[e];
+        if constexpr (SWIGLU) {
+          const v4f us = *reinterpret_cast<const v4f*>(sw + row + 32), ub = *reinterpret_cast<const v4f*>(bias + row + 32);
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            y[e] = silu(y[e]) * (static_cast<float>(acc[i + 1][j][g * 4 + e]) * scale * us[e] + ub[e]);
         }
-        *reinterpret_cast<v4f*>(buf + (lane & 31) * kRow + c) = y;
+        *reinterpret_cast<v4f*>(buf + (lane & 31) * kRow + (SWIGLU ? i * 16 : i * 32) + r) = y;
       }
     __builtin_amdgcn_wave_barrier();
     constexpr int kPieces = kCols / PER;  // 16-byte pieces of a row
@@ -759,12 +959,37 @@ bool gate_ok(int32_t E, int32_t D, int32_t wtype) {
   return E >= 1 && E <= 1024 && D >= 512 && D <= 16384 && D % 512 == 0 && (wtype == MOE_BF16 || wtype == MOE_F32);
 }
 
-template <int TYPE, bool SIG>
-void launch_route(const RouteArgs& a, hipStream_t st) {
-  const dim3 grid(static_cast<unsigned>((a.B + 3LL) / 4));
-  const size_t lds = a.groups ? 4 * sizeof(double) * (a.E + 64) : 0;
-  if (a.E <= 256) hipLaunchKernelGGL((route_kernel<TYPE, SIG, 4>), grid, dim3(256), lds, st, a);
-  else hipLaunchKernelGGL((route_kernel<TYPE, SIG, 16>), grid, dim3(256), lds, st, a);
+template <int LPT, int NV>
+int launch_route(const RouteArgs& a, hipStream_t st) {
+  constexpr int per = 4 * (64 / LPT);
+  hipLaunchKernelGGL((route_kernel<LPT, NV>), dim3(static_cast<unsigned>((a.B + per - 1) / per)), dim3(256), 0, st, a);
+  return launch_status();
+}
+
+template <int TYPE, int W, int NV>
+int launch_quant(const void* x, int64_t ldx, int32_t M, int32_t K, int8_t* codes, int64_t ldc, float* scales,
+                 hipStream_t st) {
+  constexpr int per = 4 / W;
+  hipLaunchKernelGGL((quant_kernel<TYPE, W, NV>), dim3(static_cast<unsigned>((M + per - 1) / per)), dim3(256), 0, st, x,
+                     ldx, M, K, codes, ldc, scales);
+  return launch_status();
+}
+
+template <int TYPE>
+int launch_quant(const void* x, int64_t ldx, int32_t M, int32_t K, int8_t* codes, int64_t ldc, float* scales,
+                 hipStream_t st) {
+  constexpr int VE = 16 / static_cast<int>(elem_size(TYPE));
+  const int pieces = (K + VE - 1) / VE;
+  // many tokens: a wave each, no step waits for another wave; few: four waves each
+  if (M >= 1024 && pieces <= 8 * 64) {
+    if (pieces <= 64) return launch_quant<TYPE, 1, 1>(x, ldx, M, K, codes, ldc, scales, st);
+    if (pieces <= 2 * 64) return launch_quant<TYPE, 1, 2>(x, ldx, M, K, codes, ldc, scales, st);
+    if (pieces <= 4 * 64) return launch_quant<TYPE, 1, 4>(x, ldx, M, K, codes, ldc, scales, st);
+    return launch_quant<TYPE, 1, 8>(x, ldx, M, K, codes, ldc, scales, st);
+  }
+  if (pieces <= 2 * 256) return launch_quant<TYPE, 4, 2>(x, ldx, M, K, codes, ldc, scales, st);
+  if (pieces <= 8 * 256) return launch_quant<TYPE, 4, 8>(x, ldx, M, K, codes, ldc, scales, st);
+  return launch_quant<TYPE, 4, 0>(x, ldx, M, K, codes, ldc, scales, st);
 }
 
 // Allow a kernel more than 64 KB of LDS, once per device.
@@ -810,14 +1035,14 @@ int launch_stream(const LinearArgs& a, hipStream_t st) {
   return launch_status();
 }
 
-template <int BM, int BN, int OUT, bool SWIGLU>
+template <int BM, int BN, int WM, int WN, int NS, int OUT, bool SWIGLU>
 int launch_dma(const LinearArgs& a, hipStream_t st) {
   static std::atomic<uint64_t> done{0};
-  constexpr size_t lds = 4 * (BM + BN) * 64;
-  if (!allow_lds(linear_dma_kernel<BM, BN, OUT, SWIGLU>, lds, done)) return MOE_EHIP;
+  constexpr size_t lds = NS * (BM + BN) * 64 + 4 * (BM + 2 * BN);
+  if (!allow_lds(linear_dma_kernel<BM, BN, WM, WN, NS, OUT, SWIGLU>, lds, done)) return MOE_EHIP;
   const uint32_t nm = static_cast<uint32_t>((a.M + BM - 1) / BM), bn = SWIGLU ? BN / 2 : BN,
                  nn = static_cast<uint32_t>(((SWIGLU ? a.N / 2 : a.N) + bn - 1) / bn), per = (nm * nn + 7) / 8;
-  hipLaunchKernelGGL((linear_dma_kernel<BM, BN, OUT, SWIGLU>), dim3(per * 8), dim3(256), lds, st, a, nm, nn, per);
+  hipLaunchKernelGGL((linear_dma_kernel<BM, BN, WM, WN, NS, OUT, SWIGLU>), dim3(per * 8), dim3(64 * WM * WN), lds, st, a, nm, nn, per);
   return launch_status();
 }
 
@@ -834,8 +1059,8 @@ int launch_linear(const LinearArgs& a, hipStream_t st) {
       return (((a.M + bm - 1) / bm) * ((cols + b - 1) / b) + 255) / 256;
     };
     const int64_t big = rounds(256, 256) * 40, mid = rounds(128, 128) * 16;
-    if (big <= mid) return launch_dma<256, 256, OUT, SWIGLU>(a, st);
-    return launch_dma<128, 128, OUT, SWIGLU>(a, st);
+    if (big <= mid) return launch_dma<256, 256, 2, 4, 4, OUT, SWIGLU>(a, st);
+    return launch_dma<128, 128, 2, 2, 4, OUT, SWIGLU>(a, st);
   }
   const unsigned my = static_cast<unsigned>((a.M + 63) / 64);
   const unsigned nx = static_cast<unsigned>(SWIGLU ? (a.N / 2 + 31) / 32 : (a.N + 63) / 64);
@@ -895,32 +1120,27 @@ int moe_route(const void* logits, int32_t type, int64_t ldl, int32_t B, int32_t 
                     : E % o.groups || o.topk_groups < 1 || o.topk_groups > o.groups ||
                           topk > o.topk_groups * (E / o.groups))
     return MOE_EINVAL;
-  const RouteArgs a = {logits,        ldl,      B,      E,   topk,   o.groups, o.topk_groups,
+  const RouteArgs a = {logits,   ldl,           B,             E,        topk,
+                       type,     o.score,       o.groups,      o.topk_groups,
                        o.group_score, o.renorm, o.scale == 0.0f ? 1.0f : o.scale, o.bias_dev, ids, weights};
   hipStream_t st = as_stream(stream);
-  const int v = type * 2 + o.score;
-  switch (v) {
-    case MOE_BF16 * 2: launch_route<MOE_BF16, false>(a, st); break;
-    case MOE_BF16 * 2 + 1: launch_route<MOE_BF16, true>(a, st); break;
-    case MOE_F16 * 2: launch_route<MOE_F16, false>(a, st); break;
-    case MOE_F16 * 2 + 1: launch_route<MOE_F16, true>(a, st); break;
-    case MOE_F32 * 2: launch_route<MOE_F32, false>(a, st); break;
-    default: launch_route<MOE_F32, true>(a, st); break;
+  // 16 lanes a token do less work in all, 64 finish a token sooner
+  if (B >= 2048 && E <= 256 && o.groups <= 16) {
+    if (E <= 64) return launch_route<16, 4>(a, st);
+    if (E <= 160) return launch_route<16, 10>(a, st);
+    return launch_route<16, 16>(a, st);
   }
-  return launch_status();
+  return E <= 256 ? launch_route<64, 4>(a, st) : launch_route<64, 16>(a, st);
 }
 
 int moe_quant_i8(const void* x, int32_t type, int64_t ldx, int32_t M, int32_t K, int8_t* codes, int64_t ldc,
                  float* scales, void* stream) {
   if (!x || !codes || !scales || !type_ok(type) || M < 1 || M > kMaxRows || K < 1 || K > 131072 || ldx < K || ldc < K)
     return MOE_EINVAL;
-  const dim3 grid(static_cast<unsigned>(M));
   hipStream_t st = as_stream(stream);
-  if (type == MOE_F32) hipLaunchKernelGGL(quant_kernel<MOE_F32>, grid, dim3(256), 0, st, x, ldx, M, K, codes, ldc, scales);
-  else if (type == MOE_F16)
-    hipLaunchKernelGGL(quant_kernel<MOE_F16>, grid, dim3(256), 0, st, x, ldx, M, K, codes, ldc, scales);
-  else hipLaunchKernelGGL(quant_kernel<MOE_BF16>, grid, dim3(256), 0, st, x, ldx, M, K, codes, ldc, scales);
-  return launch_status();
+  if (type == MOE_F32) return launch_quant<MOE_F32>(x, ldx, M, K, codes, ldc, scales, st);
+  if (type == MOE_F16) return launch_quant<MOE_F16>(x, ldx, M, K, codes, ldc, scales, st);
+  return launch_quant<MOE_BF16>(x, ldx, M, K, codes, ldc, scales, st);
 }
 
 int moe_linear_i8(const int8_t* a, int64_t lda, const float* sa, const int8_t* w, int64_t ldw, const float* sw,
