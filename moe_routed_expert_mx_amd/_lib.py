@@ -9,6 +9,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 
 # PyTorch first: the library runs on torch's streams and memory, so it must bind to the
 # HIP runtime torch has loaded.  Loaded the other way round, the process holds two HIP
@@ -103,11 +104,10 @@ def _load():
         "moe_gate_packed_bytes": (c.c_size_t, [c.c_int32] * 3),
         "moe_gate_pack": (c.c_int, [P, c.c_int32, c.c_int32, c.c_int32, P, c.c_size_t, P]),
         "moe_gate": (c.c_int, [c.POINTER(moe_gate_t), P, c.c_int64, c.c_int32, P, c.c_int64, P]),
-        "moe_route": (c.c_int, [P, c.c_int32, c.c_int64, c.c_int32, c.c_int32, c.c_int32,
-                                c.POINTER(moe_route_opts_t), P, P, P]),
+        "moe_route": (c.c_int, [P, c.c_int32, c.c_int64, c.c_int32, c.c_int32, c.c_int32, P, P, P, P]),
         "moe_quant_i8": (c.c_int, [P, c.c_int32, c.c_int64, c.c_int32, c.c_int32, P, c.c_int64, P, P]),
-        "moe_linear_i8": (c.c_int, [P, c.c_int64, P, P, c.c_int64, P, c.c_int32, c.c_int32, c.c_int32,
-                                    c.POINTER(moe_linear_opts_t), P, c.c_int32, c.c_int64, P]),
+        "moe_linear_i8": (c.c_int, [P, c.c_int64, P, P, c.c_int64, P, c.c_int32, c.c_int32, c.c_int32, P, P, c.c_int32,
+                                    c.c_int64, P]),
         "moe_work_split": (c.c_int, [c.c_int32] * 6 + [P, P]),
         "moe_grouped_runs": (c.c_int, [c.c_int32, P, c.c_int32, c.c_int32, c.c_int32, P]),
     }
@@ -280,57 +280,70 @@ def moe_combine(rows, weights, out, stream=None):
 # --------------------------------------------------------------- dense side
 # These entry points check their tensors (the library sees pointers only): types, shapes,
 # unit stride within rows and one GPU for all of them raise ValueError.  They run on that
-# GPU's current stream, whichever GPU is current.
+# GPU's current stream, whichever GPU is current.  A call takes some microseconds of host
+# time, as long as the smallest kernels run, so the checks are few and plain, and options go
+# as packed bytes.
 _MOE_TYPE = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
+_BF16, _F32, _I32, _I8, _U8 = torch.bfloat16, torch.float32, torch.int32, torch.int8, torch.uint8
+_ROUTE_OPTS = struct.Struct("@5ifP2i")   # moe_route_opts_t
+_LINEAR_OPTS = struct.Struct("@2iPPq")   # moe_linear_opts_t
+assert _ROUTE_OPTS.size == ctypes.sizeof(moe_route_opts_t) and _LINEAR_OPTS.size == ctypes.sizeof(moe_linear_opts_t)
+_current_device = torch._C._cuda_getDevice
+_current_stream = torch._C._cuda_getCurrentRawStream
 
 
-def _need(ok: bool, what: str):
-    if not ok:
-        raise ValueError(what)
+def _refuse(what: str):
+    raise ValueError(what)
 
 
-def _rows(t, name: str, dtype=None):
-    """Row distance of a [rows, columns] tensor whose rows are contiguous."""
-    _need(t.dim() == 2, f"{name}: expected two dimensions, got {t.dim()}")
-    _need(t.dtype == dtype if dtype is not None else t.dtype in _MOE_TYPE, f"{name}: type {t.dtype} not taken")
-    cols = t.shape[1]
+def _rows(t, name: str, shape: tuple) -> int:
+    """Row distance of a tensor [rows, columns] whose rows are contiguous."""
+    if t.shape != shape:
+        _refuse(f"{name}: expected {list(shape)}, got {list(t.shape)}")
     ld, inner = t.stride()
-    _need(inner == 1 or cols == 1, f"{name}: the elements of a row must be contiguous")
-    if t.shape[0] == 1:
-        return max(cols, 1)
-    _need(ld >= cols, f"{name}: rows overlap (stride {ld}, {cols} columns)")
+    rows, cols = shape
+    if inner != 1 and cols != 1:
+        _refuse(f"{name}: the elements of a row must be contiguous")
+    if rows == 1:
+        return cols
+    if ld < cols:
+        _refuse(f"{name}: rows overlap (stride {ld}, {cols} columns)")
     return ld
 
 
-def _vector(t, name: str, n: int, dtype=torch.float32):
-    _need(t.dtype == dtype and t.dim() == 1 and t.shape[0] == n, f"{name}: expected {dtype} [{n}]")
-    _need(n == 1 or t.stride(0) == 1, f"{name}: must be contiguous")
+def _matrix(t, name: str) -> tuple:
+    return t.shape if t.dim() == 2 else _refuse(f"{name}: expected two dimensions, got {t.dim()}")
+
+
+def _vector(t, name: str, n: int) -> int:
+    if t.dtype != _F32 or t.shape != (n,) or (n != 1 and t.stride(0) != 1):
+        _refuse(f"{name}: expected contiguous FP32 [{n}]")
     return t.data_ptr()
 
 
-def _on(stream, first, *others):
-    """(device guard or None, raw stream) of a call on `first`'s GPU."""
-    dev = first.device
-    _need(dev.type == "cuda", "the tensors must be on a GPU")
-    for t in others:
-        _need(t is None or t.device == dev, "the tensors must be on one GPU")
+def _enqueue(name: str, fn, stream, tensors: tuple, *args):
+    """Run a library call, its stream appended, on the one GPU that holds the tensors."""
+    dev = tensors[0].get_device()
+    for t in tensors:
+        if t.get_device() != dev:
+            _refuse("the tensors must be on one GPU")
+    if dev < 0:
+        _refuse("the tensors must be on a GPU")
     if stream is None:
-        raw = torch.cuda.current_stream(dev).cuda_stream
+        raw = _current_stream(dev)
     elif hasattr(stream, "cuda_stream"):
-        _need(stream.device == dev, "the stream belongs to another GPU than the tensors")
         raw = stream.cuda_stream
+        if stream.device_index != dev:
+            _refuse("the stream belongs to another GPU than the tensors")
     else:
         raw = int(stream)
-    return (None if torch.cuda.current_device() == dev.index else torch.cuda.device(dev)), raw
-
-
-def _enqueue(name: str, guard, *args):
-    if guard is None:
-        status = getattr(lib, name)(*args)
+    if _current_device() == dev:
+        status = fn(*args, raw)
     else:
-        with guard:
-            status = getattr(lib, name)(*args)
-    _check(name, status)
+        with torch.cuda.device(dev):
+            status = fn(*args, raw)
+    if status:
+        raise MoeError(name, status)
 
 
 def moe_gate_packed_bytes(E: int, D: int, wdtype=torch.bfloat16) -> int:
@@ -341,23 +354,23 @@ def moe_gate_packed_bytes(E: int, D: int, wdtype=torch.bfloat16) -> int:
 def moe_gate_pack(w, packed, stream=None) -> moe_gate_t:
     """Lay a router weight (BF16 or FP32 [E, D], contiguous) out into `packed` (uint8, moe_gate_packed_bytes)
     and return its handle for moe_gate.  The caller keeps `packed` alive."""
-    _need(w.dim() == 2 and w.dtype in (torch.bfloat16, torch.float32) and w.is_contiguous(),
-          "w: expected contiguous BF16 or FP32 [E, D]")
-    _need(packed.dtype == torch.uint8 and packed.is_contiguous(), "packed: expected contiguous uint8")
-    E, D = w.shape
-    guard, st = _on(stream, w, packed)
-    _enqueue("moe_gate_pack", guard, w.data_ptr(), _MOE_TYPE[w.dtype], E, D, packed.data_ptr(), packed.numel(), st)
+    E, D = _matrix(w, "w")
+    if w.dtype not in (_BF16, _F32) or not w.is_contiguous():
+        _refuse("w: expected contiguous BF16 or FP32 [E, D]")
+    if packed.dtype != _U8 or not packed.is_contiguous():
+        _refuse("packed: expected contiguous uint8")
+    _enqueue("moe_gate_pack", lib.moe_gate_pack, stream, (w, packed), w.data_ptr(), _MOE_TYPE[w.dtype], E, D,
+             packed.data_ptr(), packed.numel())
     return moe_gate_t(E, D, _MOE_TYPE[w.dtype], packed.data_ptr())
 
 
 def moe_gate(gate: moe_gate_t, x, logits, stream=None):
     """Router product: x BF16 [B, D] (rows may be strided) -> logits FP32 [B, E]."""
-    ldx, ldl = _rows(x, "x", torch.bfloat16), _rows(logits, "logits", torch.float32)
-    B = x.shape[0]
-    _need(x.shape[1] == gate.D, f"x: expected {gate.D} features")
-    _need(logits.shape == (B, gate.E), f"logits: expected [{B}, {gate.E}]")
-    guard, st = _on(stream, x, logits)
-    _enqueue("moe_gate", guard, ctypes.byref(gate), x.data_ptr(), ldx, B, logits.data_ptr(), ldl, st)
+    B = _matrix(x, "x")[0]
+    if x.dtype != _BF16 or logits.dtype != _F32:
+        _refuse("x: expected BF16, logits: FP32")
+    ldx, ldl = _rows(x, "x", (B, gate.D)), _rows(logits, "logits", (B, gate.E))
+    _enqueue("moe_gate", lib.moe_gate, stream, (x, logits), gate, x.data_ptr(), ldx, B, logits.data_ptr(), ldl)
 
 
 _SCORES = {"softmax": 0, "sigmoid": 1}
@@ -370,32 +383,38 @@ def moe_route(logits, ids, weights, *, score: str = "softmax", bias=None, groups
     the largest choice (score + bias) first, as the expert calls and moe_combine take them.  score "softmax" or
     "sigmoid"; groups experts groups of which topk_groups stay, ranked by group_score "max" or "top2"; renorm
     divides a token's weights by their sum; scale multiplies them."""
-    ldl = _rows(logits, "logits")
-    B, E = logits.shape
-    _need(score in _SCORES, f"unknown score {score!r}")
-    _need(group_score in _GROUP_SCORES, f"unknown group_score {group_score!r}")
-    _need(ids.dim() == 2 and ids.shape[0] == B and ids.dtype == torch.int32 and ids.is_contiguous(),
-          f"ids: expected contiguous int32 [{B}, topk]")
-    K = ids.shape[1]
-    _need(weights.shape == ids.shape and weights.dtype == torch.float32 and weights.is_contiguous(),
-          f"weights: expected contiguous FP32 [{B}, {K}]")
-    _need(scale != 0.0, "scale must not be 0")
-    opts = moe_route_opts_t(_SCORES[score], groups, topk_groups, _GROUP_SCORES[group_score], bool(renorm), scale,
-                            None if bias is None else _vector(bias, "bias", E))
-    guard, st = _on(stream, logits, ids, weights, bias)
-    _enqueue("moe_route", guard, logits.data_ptr(), _MOE_TYPE[logits.dtype], ldl, B, E, K, ctypes.byref(opts),
-             ids.data_ptr(), weights.data_ptr(), st)
+    shape = _matrix(logits, "logits")
+    B, E = shape
+    kind, sc, gs = _MOE_TYPE.get(logits.dtype), _SCORES.get(score), _GROUP_SCORES.get(group_score)
+    if kind is None or sc is None or gs is None:
+        _refuse(f"logits of {logits.dtype}, score {score!r} or group_score {group_score!r} not taken")
+    ldl = _rows(logits, "logits", shape)
+    out = ids.shape
+    if len(out) != 2 or out[0] != B or ids.dtype != _I32 or not ids.is_contiguous():
+        _refuse(f"ids: expected contiguous int32 [{B}, topk]")
+    if weights.shape != out or weights.dtype != _F32 or not weights.is_contiguous():
+        _refuse(f"weights: expected contiguous FP32 {list(out)}")
+    if scale == 0.0:
+        _refuse("scale must not be 0")
+    tensors, pb = (logits, ids, weights), 0
+    if bias is not None:
+        tensors, pb = (logits, ids, weights, bias), _vector(bias, "bias", E)
+    _enqueue("moe_route", lib.moe_route, stream, tensors, logits.data_ptr(), kind, ldl, B, E, out[1],
+             _ROUTE_OPTS.pack(sc, groups, topk_groups, gs, 1 if renorm else 0, scale, pb, 0, 0), ids.data_ptr(),
+             weights.data_ptr())
 
 
 def moe_quant_i8(x, codes, scales, stream=None):
     """Int8 quantization with one scale for each token: x [M, K] (FP32, BF16 or FP16) -> codes int8 [M, K], scales
     FP32 [M]; code * scale stands for x."""
-    ldx, ldc = _rows(x, "x"), _rows(codes, "codes", torch.int8)
-    M, K = x.shape
-    _need(codes.shape == x.shape, f"codes: expected [{M}, {K}]")
-    ps = _vector(scales, "scales", M)
-    guard, st = _on(stream, x, codes, scales)
-    _enqueue("moe_quant_i8", guard, x.data_ptr(), _MOE_TYPE[x.dtype], ldx, M, K, codes.data_ptr(), ldc, ps, st)
+    shape = _matrix(x, "x")
+    kind = _MOE_TYPE.get(x.dtype)
+    if kind is None or codes.dtype != _I8:
+        _refuse(f"x of {x.dtype} or codes of {codes.dtype} not taken")
+    ldx, ldc = _rows(x, "x", shape), _rows(codes, "codes", shape)
+    M, K = shape
+    _enqueue("moe_quant_i8", lib.moe_quant_i8, stream, (x, codes, scales), x.data_ptr(), kind, ldx, M, K,
+             codes.data_ptr(), ldc, _vector(scales, "scales", M))
 
 
 _ACTS = {"none": 0, "swiglu": 1}
@@ -405,19 +424,26 @@ def moe_linear_i8(a, a_scales, w, w_scales, out, *, act: str = "none", bias=None
     """Int8 product with scales for each token and channel: a int8 [M, K], w int8 [N, K] -> out [M, N] (FP32, BF16 or
     FP16), y = (a . w) * a_scales * w_scales + bias (FP32 [N]); act "swiglu": the first N/2 rows of w are the gate,
     the others up, and out is [M, N/2]; add (as out, may be out itself) is added last."""
-    _need(act in _ACTS, f"unknown act {act!r}")
-    lda, ldw, ldo = _rows(a, "a", torch.int8), _rows(w, "w", torch.int8), _rows(out, "out")
-    (M, K), N = a.shape, w.shape[0]
-    _need(w.shape[1] == K, f"w: expected {K} columns")
-    _need(act != "swiglu" or N % 2 == 0, "w: SwiGLU needs an even number of rows")
-    cols = N // 2 if act == "swiglu" else N
-    _need(out.shape == (M, cols), f"out: expected [{M}, {cols}]")
-    opts = moe_linear_opts_t(_ACTS[act], 0, None if bias is None else _vector(bias, "bias", N))
-    if add is not None:
-        opts.ldadd = _rows(add, "add", out.dtype)
-        _need(add.shape == out.shape, f"add: expected [{M}, {cols}]")
-        opts.add_dev = add.data_ptr()
+    shape, mode, kind = _matrix(a, "a"), _ACTS.get(act), _MOE_TYPE.get(out.dtype)
+    M, K = shape
+    N = _matrix(w, "w")[0]
+    if mode is None or kind is None or a.dtype != _I8 or w.dtype != _I8:
+        _refuse(f"act {act!r}, a of {a.dtype}, w of {w.dtype} or out of {out.dtype} not taken")
+    cols = N
+    if mode:
+        cols = N // 2
+        if N % 2:
+            _refuse("w: SwiGLU needs an even number of rows")
+    lda, ldw, ldo = _rows(a, "a", shape), _rows(w, "w", (N, K)), _rows(out, "out", (M, cols))
     psa, psw = _vector(a_scales, "a_scales", M), _vector(w_scales, "w_scales", N)
-    guard, st = _on(stream, a, a_scales, w, w_scales, out, bias, add)
-    _enqueue("moe_linear_i8", guard, a.data_ptr(), lda, psa, w.data_ptr(), ldw, psw, M, N, K, ctypes.byref(opts),
-             out.data_ptr(), _MOE_TYPE[out.dtype], ldo, st)
+    tensors, pb, pd, ldd = (a, a_scales, w, w_scales, out), 0, 0, 0
+    if bias is not None:
+        pb = _vector(bias, "bias", N)
+        tensors += (bias,)
+    if add is not None:
+        if add.dtype != out.dtype:
+            _refuse(f"add: expected {out.dtype}")
+        ldd, pd = _rows(add, "add", (M, cols)), add.data_ptr()
+        tensors += (add,)
+    _enqueue("moe_linear_i8", lib.moe_linear_i8, stream, tensors, a.data_ptr(), lda, psa, w.data_ptr(), ldw, psw, M, N,
+             K, _LINEAR_OPTS.pack(mode, 0, pb, pd, ldd), out.data_ptr(), kind, ldo)
