@@ -352,16 +352,14 @@ int moe_combine(const void* rows_dev, size_t rows_bytes, const float* weights_de
 
 enum moe_dtype { MOE_BF16 = 0, MOE_F16 = 1, MOE_F32 = 2 };
 
-/* Bytes of the router weight [E, D] laid out by moe_gate_pack.  wtype MOE_BF16: one BF16
- * plane; MOE_F32: three, the weight's upper, middle and lower eight mantissa bits, whose
- * sum is the FP32 weight.  E is padded to a multiple of 16.  0 on invalid sizes (1 <= E <=
+/* Bytes of the router weight [E, D] laid out by moe_gate_pack: its own (wtype MOE_BF16 or
+ * MOE_F32), E padded to a multiple of 16.  0 on invalid sizes (1 <= E <=
  * 1024, 512 <= D <= 16384 with D % 512 == 0, as the experts). */
 size_t moe_gate_packed_bytes(int32_t E, int32_t D, int32_t wtype);
 
 /* One-time re-layout of a router weight, row-major [E, D] of wtype, into the order
- * moe_gate reads: per 16 experts and 32 features, one contiguous 1 KB run of the matrix
- * instruction's operand, its planes one after another.  Weights below 2^-100 in magnitude lose
- * mantissa bits under 2^-133.  MOE_ENOSPACE if packed_bytes < moe_gate_packed_bytes. */
+ * moe_gate reads: per 16 experts and 32 features, one contiguous run in the order of the
+ * matrix instruction's operand.  MOE_ENOSPACE if packed_bytes < moe_gate_packed_bytes. */
 int moe_gate_pack(const void* w_dev, int32_t wtype, int32_t E, int32_t D, void* packed_dev,
                   size_t packed_bytes, void* stream);
 
@@ -372,7 +370,8 @@ typedef struct {
 } moe_gate_t;
 
 /* Router product: logits[t, e] = sum over d of x[t, d] * w[e, d], FP32 sums of exact
- * products, in a fixed order.  x_dev BF16 [B, D], ldx >= D and a multiple of 8, x_dev
+ * products, in a fixed order (an FP32 weight counts as the sum of its upper, middle and lower
+ * eight significant bits; below 2^-100 in magnitude it loses those under 2^-133).  x_dev BF16 [B, D], ldx >= D and a multiple of 8, x_dev
  * 16-byte aligned; logits_dev FP32 [B, E], ldl >= E.   The logits of a token
  * with an infinite or NaN feature are not finite (with an FP32 weight: NaN).
  * MOE_EINVAL for a null pointer, size, stride or alignment outside these. */

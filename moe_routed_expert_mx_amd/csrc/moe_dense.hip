@@ -3,10 +3,12 @@
 // shared expert beside them, behind the C ABI of include/moe_mx.h.
 #include <hip/hip_runtime.h>
 
+#include <algorithm>
 #include <atomic>
 #include <cmath>
 #include <cstdint>
 #include <cstring>
+#include <type_traits>
 
 #include "moe_mx.h"
 
@@ -412,11 +414,10 @@ __global__ __launch_bounds__(256) void quant_kernel(const void* x, int64_t ldx, 
 }
 
 // ---------------------------------------------------------------------- gate
-// Packed router weight: [E/16][D/32][plane][64 lanes][8 BF16], lane l of a run holding
-// expert l % 16, features 8 * (l / 16) .. + 7 of the step: an operand of the 16x16x32 MFMA.
-template <int WTYPE>
-__global__ __launch_bounds__(256) void gate_pack_kernel(const void* w, int32_t E, int32_t D, uint16_t* packed) {
-  constexpr int P = WTYPE == MOE_F32 ? 3 : 1;
+// Packed router weight: [E/16][D/32][64 lanes][8 weights], lane l of a run holding expert l % 16,
+// features 8 * (l / 16) .. + 7 of the step: the order of the 16x16x32 MFMA's operand.
+template <typename T>
+__global__ __launch_bounds__(256) void gate_pack_kernel(const T* w, int32_t E, int32_t D, T* packed) {
   const int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
   const int steps = D / 32;
   const int64_t n = static_cast<int64_t>((E + 15) / 16) * steps * 64;
@@ -426,30 +427,42 @@ __global__ __launch_bounds__(256) void gate_pack_kernel(const void* w, int32_t E
   const int s = static_cast<int>(run % steps);
   const int e = static_cast<int>(run / steps) * 16 + (lane & 15);
   const int k = s * 32 + (lane >> 4) * 8;
-  for (int j = 0; j < 8; ++j) {
-    uint16_t* out = packed + run * P * 512 + lane * 8 + j;
-    if constexpr (WTYPE == MOE_F32) {
-      // upper, middle and lower eight bits of the significand, each cut off towards zero
-      // and exactly a BF16; the differences are exact
-      float v = e < E ? static_cast<const float*>(w)[static_cast<int64_t>(e) * D + k + j] : 0.0f;
-      for (int p = 0; p < 3; ++p) {
-        const uint32_t b = __float_as_uint(v);
-        const bool finite = (b & 0x7fffffffu) < 0x7f800000u;
-        uint16_t h = static_cast<uint16_t>(b >> 16);
-        if (!finite && (b & 0x7fffffu)) h |= 0x40;
-        out[p * 512] = h;
-        v = finite ? v - bf16_to_f32(h) : 0.0f;
-      }
-    } else {
-      out[0] = e < E ? static_cast<const uint16_t*>(w)[static_cast<int64_t>(e) * D + k + j] : 0;
-    }
-  }
+  for (int j = 0; j < 8; ++j) packed[i * 8 + j] = e < E ? w[static_cast<int64_t>(e) * D + k + j] : T(0);
 }
+
+// Eight weights as they lie in memory, and as P BF16 operands whose sum they are.  An FP32
+// weight is cut into its upper, middle and lower eight significant bits, each a BF16 exactly:
+// three MFMAs at the BF16 rate then do what FP32 ones would need sixteen times the time for.
+template <int P>
+struct GateWeights;
+template <>
+struct GateWeights<1> {
+  v8bf w;
+  __device__ __forceinline__ void split(v8bf (&o)[1]) const { o[0] = w; }
+};
+template <>
+struct GateWeights<3> {
+  uint32_t w[8];
+  __device__ __forceinline__ void split(v8bf (&o)[3]) const {
+    uint32_t p[3][4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      uint32_t a = w[2 * j], b = w[2 * j + 1];
+#pragma unroll
+      for (int i = 0; i < 3; ++i) {
+        p[i][j] = __builtin_amdgcn_perm(b, a, 0x07060302);  // both upper halves
+        a = __float_as_uint(__uint_as_float(a) - __uint_as_float(a & 0xffff0000u));
+        b = __float_as_uint(__uint_as_float(b) - __uint_as_float(b & 0xffff0000u));
+      }
+    }
+    __builtin_memcpy(&o, &p, sizeof(p));
+  }
+};
 
 struct GateArgs {
   const uint16_t* x;
   int64_t ldx;
-  const uint16_t* packed;
+  const void* packed;
   int32_t B, E, D;
   float* logits;
   int64_t ldl;
@@ -472,7 +485,7 @@ __global__ __launch_bounds__(64 * WV) void gate_kernel(GateArgs a, uint32_t cols
   const int64_t t0 = static_cast<int64_t>(row) * (16 * TT);
   const int tiles = (a.E + 15) / 16, steps = a.D / 32, n = steps / WV, s0 = wave * n;
   const uint16_t* xp[TT];
-  const uint16_t* wp[ET];
+  const GateWeights<P>* wp[ET];
 #pragma unroll
   for (int i = 0; i < TT; ++i) {
     const int64_t t = t0 + i * 16 + (lane & 15);
@@ -481,10 +494,12 @@ __global__ __launch_bounds__(64 * WV) void gate_kernel(GateArgs a, uint32_t cols
 #pragma unroll
   for (int i = 0; i < ET; ++i) {
     const int et = static_cast<int>(col) * ET + i;
-    wp[i] = a.packed + (static_cast<int64_t>(et < tiles ? et : tiles - 1) * steps + s0) * (P * 512) + lane * 8;
+    wp[i] = static_cast<const GateWeights<P>*>(a.packed) +
+            (static_cast<int64_t>(et < tiles ? et : tiles - 1) * steps + s0) * 64 + lane;
   }
   v4f acc[TT][ET] = {};
-  v8bf xb[UX][TT], wb[UW][ET][P];
+  v8bf xb[UX][TT];
+  GateWeights<P> wb[UW][ET];
   auto load_x = [&](int u, int s) {
     s = s < n ? s : n - 1;  // past the end: loaded again, not used
 #pragma unroll
@@ -493,9 +508,7 @@ __global__ __launch_bounds__(64 * WV) void gate_kernel(GateArgs a, uint32_t cols
   auto load_w = [&](int u, int s) {
     s = s < n ? s : n - 1;
 #pragma unroll
-    for (int i = 0; i < ET; ++i)
-#pragma unroll
-      for (int p = 0; p < P; ++p) wb[u][i][p] = *reinterpret_cast<const v8bf*>(wp[i] + (s * P + p) * 512);
+    for (int i = 0; i < ET; ++i) wb[u][i] = wp[i][s * 64];
   };
 #pragma unroll
   for (int u = 0; u < UX; ++u) load_x(u, u);
@@ -507,12 +520,15 @@ __global__ __launch_bounds__(64 * WV) void gate_kernel(GateArgs a, uint32_t cols
     for (int u = 0; u < UX; ++u) {
       if (s + u < n) {
 #pragma unroll
-        for (int p = 0; p < P; ++p)
+        for (int i = 0; i < ET; ++i) {
+          v8bf w[P];
+          wb[u % UW][i].split(w);
 #pragma unroll
-          for (int i = 0; i < ET; ++i)
+          for (int p = 0; p < P; ++p)
 #pragma unroll
             for (int j = 0; j < TT; ++j)
-              acc[j][i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wb[u % UW][i][p], xb[u][j], acc[j][i], 0, 0, 0);
+              acc[j][i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(w[p], xb[u][j], acc[j][i], 0, 0, 0);
+        }
         load_x(u, s + u + UX);
         load_w(u % UW, s + u + UW);
         compiler_fence();
@@ -552,48 +568,73 @@ struct LinearArgs {
   int32_t M, N, K;
 };
 
-// 16 bytes of a row from k on, zeros from K on; any alignment, nothing read past the row.
-__device__ __forceinline__ uint4 row16(const int8_t* row, int k, int K, bool live) {
-  uint4 v = {0, 0, 0, 0};
-  if (!live || k >= K) return v;
-  if (k + 16 <= K) {
-    __builtin_memcpy(&v, row + k, 16);
-    return v;
+// 16 bytes from any address, as the aligned words they lie in: loads that straddle words are
+// several times slower than aligned ones (64 x 4096 x 4095: 47 us against 15).  `whole`: all 16 bytes
+// belong to the row; else words from `end` on are zero.  Every word read holds a byte of the row.
+struct Words {
+  v4i v;
+  int x;
+};
+__device__ __forceinline__ Words words16(const int8_t* p, bool whole, const int8_t* end) {
+  typedef int v4i_word __attribute__((ext_vector_type(4), aligned(4)));
+  const uintptr_t b = reinterpret_cast<uintptr_t>(p) & ~static_cast<uintptr_t>(3);
+  Words r = {{0, 0, 0, 0}, 0};
+  if (whole) {
+    r.v = *reinterpret_cast<const v4i_word*>(b);
+    r.x = *reinterpret_cast<const int*>((reinterpret_cast<uintptr_t>(p) + 15) & ~static_cast<uintptr_t>(3));
+  } else {
+    const uintptr_t e = reinterpret_cast<uintptr_t>(end);
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (b + 4 * i < e) r.v[i] = *reinterpret_cast<const int*>(b + 4 * i);
+    if (b + 16 < e) r.x = *reinterpret_cast<const int*>(b + 16);
   }
-  uint32_t u[4] = {0, 0, 0, 0};
-  for (int i = 0; i < K - k; ++i)
-    u[i >> 2] |= static_cast<uint32_t>(static_cast<uint8_t>(row[k + i])) << (8 * (i & 3));
-  v = {u[0], u[1], u[2], u[3]};
-  return v;
+  return r;
 }
-
-__device__ __forceinline__ v4i bits(uint4 v) {
-  return v4i{static_cast<int>(v.x), static_cast<int>(v.y), static_cast<int>(v.z), static_cast<int>(v.w)};
+// The 16 bytes, `skip` bytes into their words; only the first n of them if n < 16.
+__device__ __forceinline__ v4i bytes16(const Words& r, uint32_t skip, int n) {
+  v4i o;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t hi = static_cast<uint32_t>(i < 3 ? r.v[i + 1] : r.x);
+    uint32_t w = __builtin_amdgcn_alignbyte(hi, static_cast<uint32_t>(r.v[i]), skip);
+    if (n < 16) w &= n >= 4 * i + 4 ? ~0u : n <= 4 * i ? 0u : (1u << (8 * (n - 4 * i))) - 1;
+    o[i] = static_cast<int>(w);
+  }
+  return o;
+}
+__device__ __forceinline__ uint32_t skip_of(const int8_t* p) {
+  return static_cast<uint32_t>(reinterpret_cast<uintptr_t>(p) & 3);
 }
 // g / (1 + exp(-g)) with the hardware's exp2 and reciprocal (an ulp each).
 __device__ __forceinline__ float silu(float g) { return g * __builtin_amdgcn_rcpf(1.0f + __expf(-g)); }
 
 // ------------------------------------------------- linear: up to 64 tokens
-// The weight is read once, so its bytes bound the product.  A workgroup takes 16 weight rows
+// The weight is read once, so its bytes bound the product.  A workgroup takes 16 RT weight rows
 // (SwiGLU: 16 gate rows and their 16 up rows) and all tokens; its WV waves split K, read both
 // operands straight into registers some chunks of 64 bytes ahead, and add their 32-bit sums
 // through LDS.
-template <int OUT, bool SWIGLU, bool ALIGNED, int TT, int WV>
-__global__ __launch_bounds__(64 * WV) void linear_stream_kernel(LinearArgs a) {
+template <int OUT, bool SWIGLU, bool ALIGNED, int RT, int TT, int WV>
+__global__ __launch_bounds__(64 * WV) void linear_stream_kernel(LinearArgs a, uint32_t nx) {
   extern __shared__ int stream_lds[];
-  constexpr int RT = SWIGLU ? 2 : 1, U = RT + TT >= 5 ? 4 : 8;
+  constexpr int U = RT + TT >= 5 ? (ALIGNED ? 7 : 4) : ALIGNED ? 8 : 6, COLS = SWIGLU ? 16 : 16 * RT;  // chunks in flight; columns of out
+  static_assert(!SWIGLU || RT == 2, "a gate and an up tile");
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int H = SWIGLU ? a.N / 2 : a.N, n0 = blockIdx.x * 16;
+  const int H = SWIGLU ? a.N / 2 : a.N, n0 = blockIdx.x % nx * COLS, m0 = blockIdx.x / nx * (16 * TT);
   const int chunks = (a.K + 63) / 64, per = (chunks + WV - 1) / WV, c0 = wave * per;
   const int n = chunks - c0 < per ? (chunks > c0 ? chunks - c0 : 0) : per;
   const int r = lane & 15, q = lane >> 4;
   const int8_t *wp[RT], *ap[TT];
-  const int row = n0 + r < H ? n0 + r : H - 1;
 #pragma unroll
-  for (int i = 0; i < RT; ++i) wp[i] = a.w + (static_cast<int64_t>(row) + i * H) * a.ldw;
+  for (int i = 0; i < RT; ++i) {
+    const int c = n0 + (SWIGLU ? 0 : i * 16) + r;
+    wp[i] = a.w + ((c < H ? c : H - 1) + (SWIGLU ? static_cast<int64_t>(i) * H : 0)) * a.ldw;
+  }
 #pragma unroll
-  for (int i = 0; i < TT; ++i) ap[i] = a.a + static_cast<int64_t>(i * 16 + r < a.M ? i * 16 + r : a.M - 1) * a.lda;
-  v4i acc[RT][TT] = {}, wb[U][RT], ab[U][TT];
+  for (int i = 0; i < TT; ++i) ap[i] = a.a + static_cast<int64_t>(m0 + i * 16 + r < a.M ? m0 + i * 16 + r : a.M - 1) * a.lda;
+  using Held = std::conditional_t<ALIGNED, v4i, Words>;
+  v4i acc[RT][TT] = {};
+  Held wb[U][RT], ab[U][TT];
   // aligned: an operand's 16 bytes lie wholly inside the row or wholly behind it; those behind
   // are read from the row's last 16 and set to zero when used
   auto load = [&](int u, int c) {
@@ -605,10 +646,11 @@ __global__ __launch_bounds__(64 * WV) void linear_stream_kernel(LinearArgs a) {
 #pragma unroll
       for (int i = 0; i < TT; ++i) ab[u][i] = *reinterpret_cast<const v4i*>(ap[i] + kc);
     } else {
+      const bool whole = (c0 + c) * 64 + 64 <= a.K;
 #pragma unroll
-      for (int i = 0; i < RT; ++i) wb[u][i] = bits(row16(wp[i], k, a.K, true));
+      for (int i = 0; i < RT; ++i) wb[u][i] = words16(wp[i] + k, whole, wp[i] + a.K);
 #pragma unroll
-      for (int i = 0; i < TT; ++i) ab[u][i] = bits(row16(ap[i], k, a.K, true));
+      for (int i = 0; i < TT; ++i) ab[u][i] = words16(ap[i] + k, whole, ap[i] + a.K);
     }
   };
   if (n > 0) {
@@ -620,16 +662,24 @@ __global__ __launch_bounds__(64 * WV) void linear_stream_kernel(LinearArgs a) {
 #pragma unroll
       for (int u = 0; u < U; ++u)
         if (c + u < n) {
-          if (ALIGNED && (c0 + c + u) * 64 + 64 > a.K) {
-            const bool in = (c0 + c + u) * 64 + q * 16 < a.K;
+          // bytes behind K count as zero; it takes one operand to see to that
+          const int k = (c0 + c + u) * 64 + q * 16;
+          const bool whole = (c0 + c + u) * 64 + 64 <= a.K;
+          v4i fw[RT], fa[TT];
 #pragma unroll
-            for (int i = 0; i < RT; ++i) wb[u][i] = in ? wb[u][i] : v4i{0, 0, 0, 0};
+          for (int i = 0; i < RT; ++i) {
+            if constexpr (ALIGNED) fw[i] = whole || k < a.K ? wb[u][i] : v4i{0, 0, 0, 0};
+            else fw[i] = bytes16(wb[u][i], skip_of(wp[i]), whole ? 16 : a.K - k);
+          }
+#pragma unroll
+          for (int j = 0; j < TT; ++j) {
+            if constexpr (ALIGNED) fa[j] = ab[u][j];
+            else fa[j] = bytes16(ab[u][j], skip_of(ap[j]), 16);
           }
 #pragma unroll
           for (int i = 0; i < RT; ++i)
 #pragma unroll
-            for (int j = 0; j < TT; ++j)
-              acc[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(wb[u][i], ab[u][j], acc[i][j], 0, 0, 0);
+            for (int j = 0; j < TT; ++j) acc[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(fw[i], fa[j], acc[i][j], 0, 0, 0);
           if (c + u + U < n) load(u, c + u + U);
           compiler_fence();
         }
@@ -644,10 +694,11 @@ __global__ __launch_bounds__(64 * WV) void linear_stream_kernel(LinearArgs a) {
       *reinterpret_cast<v4i*>(stream_lds + wave * kTile + (j * 16 + r) * kRow + i * 16 + q * 4) = acc[i][j];
   __syncthreads();
   using T = typename Elem<OUT>::T;
-  for (int o = threadIdx.x; o < 256 * TT; o += 64 * WV) {
-    const int m = o >> 4, c = n0 + (o & 15);
+  for (int o = threadIdx.x; o < COLS * 16 * TT; o += 64 * WV) {
+    const int64_t m = m0 + o / COLS;
+    const int c = n0 + o % COLS;
     if (m >= a.M || c >= H) continue;
-    const int* p = stream_lds + m * kRow + (o & 15);
+    const int* p = stream_lds + o / COLS * kRow + o % COLS;
     int sum = 0, sum_up = 0;
 #pragma unroll
     for (int v = 0; v < WV; ++v) {
@@ -673,6 +724,12 @@ __device__ __forceinline__ void dma16(v4i rsrc, uint32_t voff, uint32_t soff, ui
                : "s"(lds), "v"(voff), "s"(rsrc), "s"(soff)
                : "memory");
 }
+__device__ __forceinline__ void dma4(v4i rsrc, uint32_t voff, uint32_t lds) {  // 4 bytes a lane
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dword %1, %2, 0 offen lds"
+               :
+               : "s"(lds), "v"(voff), "s"(rsrc)
+               : "memory");
+}
 __device__ __forceinline__ v4i make_rsrc(const void* base, uint32_t bytes) {
   const uint64_t b = reinterpret_cast<uint64_t>(base);
   v4i r;
@@ -687,151 +744,18 @@ __device__ __forceinline__ void wait_vm() {
   asm volatile("s_waitcnt vmcnt(%0)" : : "n"(N) : "memory");
 }
 
-// Workgroup tile of BM tokens x BN weight rows, four waves of half by half each, 32x32x32
-// MFMAs with the weight as the row operand (a lane then holds four neighbouring columns of out).
-// K goes through LDS in stages of 64 bytes a row, four in flight; a row's four 16-byte parts lie
-// permuted by its index, so that eight neighbouring rows' reads meet all banks once.
-template <int BM, int BN, int WM, int WN, int NS, int OUT, bool SWIGLU>
-__global__ __launch_bounds__(64 * WM * WN, BM * BN >= 65536 ? 1 : 2) void linear_dma_kernel(LinearArgs a, uint32_t nm,
-                                                                                            uint32_t nn,
-                                                                                            uint32_t per_xcd) {
-  extern __shared__ __attribute__((aligned(16))) unsigned char smem[];
-  constexpr int kStage = (BM + BN) * 64, RA = BM / 16 / (WM * WN), RW = BN / 16 / (WM * WN);
-  constexpr int TM = BM / WM / 32, TN = BN / WN / 32;
-  static_assert(!SWIGLU || TN % 2 == 0, "a wave holds whole gate and up pairs");
-  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  // each XCD (workgroups go round the eight) takes a contiguous range of tiles, in groups of
-  // eight token tiles: what runs at once on an XCD shares operands in its L2
-  const uint32_t tile = blockIdx.x % 8 * per_xcd + blockIdx.x / 8;
-  if (blockIdx.x / 8 >= per_xcd || tile >= nm * nn) return;
-  const uint32_t band = tile / (8 * nn), left = nm - band * 8, height = left < 8 ? left : 8, in = tile - band * 8 * nn;
-  const int64_t m0 = static_cast<int64_t>(band * 8 + in % height) * BM;
-  const int H = SWIGLU ? a.N / 2 : a.N, n0 = static_cast<int>(in / height) * (SWIGLU ? BN / 2 : BN);
-  const uint32_t lds0 = static_cast<uint32_t>(reinterpret_cast<uintptr_t>((__attribute__((address_space(3))) void*)smem));
-
-  // what this lane moves: 16-byte part `ch` of rows lane / 4 of its wave's 16-row blocks
-  const int ch = (lane & 3) ^ (lane >> 4), lr = lane >> 2;
-  const int mrows = a.M - m0 < BM ? static_cast<int>(a.M - m0) : BM;
-  const v4i ra = make_rsrc(a.a + m0 * a.lda, static_cast<uint32_t>((mrows - 1) * a.lda + a.K));
-  uint32_t va[RA], vw[RW];
-  v4i rw[RW];
-  {
-    const int cols = SWIGLU ? BN / 2 : BN, nrows = H - n0 < cols ? H - n0 : cols;
-    const uint32_t bytes = static_cast<uint32_t>((nrows - 1) * a.ldw + a.K);
-#pragma unroll
-    for (int i = 0; i < RA; ++i) {
-      const int row = (wave * RA + i) * 16 + lr;
-      va[i] = row < mrows ? static_cast<uint32_t>(row * a.lda) + ch * 16 : kOutside;
-    }
-#pragma unroll
-    for (int i = 0; i < RW; ++i) {
-      // SwiGLU: 32 gate rows, then their 32 up rows, and so on
-      const int b = wave * RW + i, row = SWIGLU ? (b >> 2) * 32 + (b & 1) * 16 + lr : b * 16 + lr;
-      rw[i] = make_rsrc(a.w + (n0 + (SWIGLU ? static_cast<int64_t>((b >> 1) & 1) * H : 0)) * a.ldw, bytes);
-      vw[i] = row < nrows ? static_cast<uint32_t>(row * a.ldw) + ch * 16 : kOutside;
-    }
-  }
-  // parts behind K, and whole stages behind it, are zeros
-  auto issue_a = [&](int s, int buf, int i) {
-    const int k0 = s * 64;
-    dma16(ra, k0 + ch * 16 < a.K ? va[i] : kOutside, k0, lds0 + buf + (wave * RA + i) * 1024);
-  };
-  auto issue_w = [&](int s, int buf, int i) {
-    const int k0 = s * 64;
-    dma16(rw[i], k0 + ch * 16 < a.K ? vw[i] : kOutside, k0, lds0 + buf + BM * 64 + (wave * RW + i) * 1024);
-  };
-
-  const int wm = wave % WM * (BM / WM), wn = wave / WM * (BN / WN);
-  uint32_t la[2];  // this lane's operand inside a 32-row tile, for the stage's two halves
-#pragma unroll
-  for (int h = 0; h < 2; ++h) la[h] = (lane & 31) * 64 + (((h * 2 + (lane >> 5)) ^ ((lane >> 2) & 3)) << 4);
-  v16i acc[TN][TM] = {};
-  v4i fa[2][TM], fw[2][TN];
-  // the TM + TN reads of a half stage, `part` of them in each of the first groups of MFMAs
-  auto read = [&](int buf, int h, int from, int to) {
-    const unsigned char* p = smem + buf + la[h];
-#pragma unroll
-    for (int f = from; f < to && f < TM + TN; ++f) {
-      if (f < TM) fa[h][f] = *reinterpret_cast<const v4i*>(p + (wm + f * 32) * 64);
-      else fw[h][f - TM] = *reinterpret_cast<const v4i*>(p + (BM + wn + (f - TM) * 32) * 64);
-    }
-  };
-  auto mult = [&](int h, int i, auto&& issue) {
-#pragma unroll
-    for (int j = 0; j < TM; ++j) {
-      acc[i][j] = __builtin_amdgcn_mfma_i32_32x32x32_i8(fw[h][i], fa[h][j], acc[i][j], 0, 0, 0);
-      if (j == 0) issue();
-    }
-  };
-  const int n = (a.K + 63) / 64;
-  // scales and bias of the tile, behind the stages, in the order of its rows
-  float* const sw = reinterpret_cast<float*>(smem + NS * kStage);
-  float* const bias = sw + BN;
-  float* const sa = bias + BN;
-  constexpr int kIssue = RA + RW, kPart = TN > 1 ? (TM + TN) / (TN / 2) : TM + TN;
-#pragma unroll
-  for (int s = 0; s < NS; ++s) {
-#pragma unroll
-    for (int i = 0; i < RA; ++i) issue_a(s, s * kStage, i);
-    if (s < NS - 1) {
-#pragma unroll
-      for (int i = 0; i < RW; ++i) issue_w(s, s * kStage, i);
-    }
-  }
-  for (int r = threadIdx.x; r < BN; r += 64 * WM * WN) {
-    const int c = n0 + (SWIGLU ? (r >> 6) * 32 + (r & 31) : r), row = c + (SWIGLU ? ((r >> 5) & 1) * H : 0);
-    sw[r] = c < H ? a.sw[row] : 0.0f;
-    bias[r] = c < H && a.bias ? a.bias[row] : 0.0f;
-  }
-  for (int r = threadIdx.x; r < BM; r += 64 * WM * WN) sa[r] = r < mrows ? a.sa[m0 + r] : 0.0f;
-  wait_vm<kIssue * (NS - 2) + RA>();
-  asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-  __builtin_amdgcn_s_barrier();
-  compiler_fence();
-  read(0, 0, 0, TM + TN);
-  compiler_fence();
-  // Each half of a stage multiplies what the half before read, a row of MFMAs at a time; reads of
-  // the next half and DMA issues (which hold a wave up for some 90 cycles each) go between the
-  // rows, in the order written.
-  int prev = (NS - 1) * kStage, cur = 0;  // LDS offsets of stages s - 1 and s
-  for (int s = 0; s < n; ++s) {
-#pragma unroll
-    for (int i = 0; i < TN; ++i) {
-      read(cur, 1, i * kPart, (i + 1) * kPart);
-      mult(0, i, [&] {
-#pragma unroll
-        for (int d = i * RW / TN; d < (i + 1) * RW / TN; ++d) issue_w(s + NS - 1, prev, d);
-      });
-      __builtin_amdgcn_sched_barrier(0);
-    }
-    // this stage is read out and the next has landed, for every wave
-    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-    wait_vm<kIssue * (NS - 2)>();
-    __builtin_amdgcn_s_barrier();
-    compiler_fence();
-    __builtin_amdgcn_sched_barrier(0);
-    const int next = cur + kStage == NS * kStage ? 0 : cur + kStage;
-#pragma unroll
-    for (int i = 0; i < TN; ++i) {
-      read(next, 0, i * kPart, (i + 1) * kPart);
-      mult(1, i, [&] {
-#pragma unroll
-        for (int d = i * RA / TN; d < (i + 1) * RA / TN; ++d) issue_a(s + NS, cur, d);
-      });
-      __builtin_amdgcn_sched_barrier(0);
-    }
-    prev = cur;
-    cur = next;
-    compiler_fence();
-  }
-  wait_vm<0>();
-  __syncthreads();
-
-  // 32 tokens at a time through LDS, so that whole rows' pieces are stored
+// Floats of LDS a wave needs to store its tile, and the storing: scales, bias, activation; 32
+// tokens at a time go through LDS, so that whole rows' pieces are added to and stored.  acc is
+// the wave's part of a tile (tokens m0 + wm.., tile rows wn..); sw, bias and sa are the whole
+// tile's, in LDS.
+template <int TM, int TN, bool SWIGLU>
+constexpr int kEpilogue = 32 * ((SWIGLU ? TN * 16 : TN * 32) + 4);
+template <int TM, int TN, int OUT, bool SWIGLU>
+__device__ __forceinline__ void store_tile(const LinearArgs& a, const v16i (&acc)[TN][TM], float* buf, const float* sw,
+                                           const float* bias, const float* sa, int64_t m0, int wm, int n0, int wn) {
   using T = typename Elem<OUT>::T;
   constexpr int kCols = SWIGLU ? TN * 16 : TN * 32, kRow = kCols + 4, PER = 16 / sizeof(T);
-  static_assert(WM * WN * 32 * kRow * 4 <= NS * kStage, "epilogue fits the stages");
-  float* buf = reinterpret_cast<float*>(smem) + wave * 32 * kRow;
+  const int lane = threadIdx.x & 63, H = SWIGLU ? a.N / 2 : a.N;
   const int nw = n0 + (SWIGLU ? wn / 2 : wn);
   const bool vec = (reinterpret_cast<uintptr_t>(a.out) | (a.ldo * sizeof(T))) % 16 == 0 &&
                    (!a.add || (reinterpret_cast<uintptr_t>(a.add) | (a.ldadd * sizeof(T))) % 16 == 0);
@@ -886,68 +810,246 @@ __global__ __launch_bounds__(64 * WM * WN, BM * BN >= 65536 ? 1 : 2) void linear
   }
 }
 
-// Workgroup tile of 64 tokens x 64 weight rows, 128 bytes of K a step, through LDS.
-template <int OUT, bool SWIGLU>
-__global__ __launch_bounds__(256) void linear_tile_kernel(LinearArgs a, uint32_t nx) {
-  __shared__ uint4 lds_a[64 * 8], lds_w[64 * 8];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int64_t m0 = static_cast<int64_t>(blockIdx.x / nx) * 64;
-  const int H = SWIGLU ? a.N / 2 : a.N;
-  const int n0 = (blockIdx.x % nx) * (SWIGLU ? 32 : 64);
-  // weight row of the tile's row r: with SwiGLU 16 gate rows, then their 16 up rows, twice
-  auto wrow = [&](int r) {
-    if (!SWIGLU) return n0 + r < a.N ? n0 + r : -1;
-    const int j = n0 + (r >> 5) * 16 + (r & 15);
-    return j < H ? j + ((r >> 4) & 1) * H : -1;
+// Workgroup tile of BM tokens x BN weight rows, WM x WN waves, 32x32x32 MFMAs with the weight
+// as the row operand (a lane then holds four neighbouring columns of out).  K goes through LDS
+// in NS stages of KB bytes a row.  A row's 16-byte parts lie permuted by its index, so that the
+// 16 lanes that LDS serves at once (0-3, 12-15, 20-27 and so on) meet all 64 banks once.
+template <int BM, int BN, int WM, int WN, int KB, int NS, int OUT, bool SWIGLU>
+__global__ __launch_bounds__(64 * WM * WN, (BM + BN) * KB * NS > 78 * 1024 ? 1 : 2) void linear_dma_kernel(
+    LinearArgs a, uint32_t nm, uint32_t nn, uint32_t per_xcd) {
+  extern __shared__ __attribute__((aligned(16))) unsigned char smem[];
+  constexpr int NW = WM * WN, kStage = (BM + BN) * KB, PARTS = KB / 16, DR = 1024 / KB;  // rows of one DMA
+  constexpr int RA = BM / DR / NW, RW = BN / DR / NW, US = KB / 32;
+  constexpr int TM = BM / WM / 32, TN = BN / WN / 32;
+  static_assert(!SWIGLU || TN % 2 == 0, "a wave holds whole gate and up pairs");
+  static_assert(BM % (DR * NW) == 0 && BN % (DR * NW) == 0 && (KB == 64 || KB == 128), "whole DMAs");
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  // each XCD (workgroups go round the eight) takes a contiguous range of tiles, in groups of
+  // eight token tiles: what runs at once on an XCD shares operands in its L2
+  const uint32_t tile = blockIdx.x % 8 * per_xcd + blockIdx.x / 8;
+  if (blockIdx.x / 8 >= per_xcd || tile >= nm * nn) return;
+  const uint32_t band = tile / (8 * nn), left = nm - band * 8, height = left < 8 ? left : 8, in = tile - band * 8 * nn;
+  const int64_t m0 = static_cast<int64_t>(band * 8 + in % height) * BM;
+  const int H = SWIGLU ? a.N / 2 : a.N, n0 = static_cast<int>(in / height) * (SWIGLU ? BN / 2 : BN);
+  const uint32_t lds0 = static_cast<uint32_t>(reinterpret_cast<uintptr_t>((__attribute__((address_space(3))) void*)smem));
+
+  // place of part `c` of row r: parts go round by the row, by every second with 128-byte rows
+  // (two rows span the banks) and every fourth with 64-byte rows
+  auto place = [](int r, int c) { return c ^ ((KB == 128 ? r >> 1 : r >> 2) & (PARTS - 1)); };
+  // what this lane moves: a part of row lane / PARTS of its wave's blocks of DR rows
+  const int lr = lane / PARTS;
+  const int mrows = a.M - m0 < BM ? static_cast<int>(a.M - m0) : BM;
+  const v4i ra = make_rsrc(a.a + m0 * a.lda, static_cast<uint32_t>((mrows - 1) * a.lda + a.K));
+  uint32_t va[RA], vw[RW];
+  int ka[RA], kw[RW];  // the part's offset in the stage
+  v4i rw[RW];
+  {
+    const int cols = SWIGLU ? BN / 2 : BN, nrows = H - n0 < cols ? H - n0 : cols;
+    const uint32_t bytes = static_cast<uint32_t>((nrows - 1) * a.ldw + a.K);
+#pragma unroll
+    for (int i = 0; i < RA; ++i) {
+      const int row = (wave * RA + i) * DR + lr;
+      ka[i] = place(row, lane % PARTS) * 16;
+      va[i] = row < mrows ? static_cast<uint32_t>(row * a.lda) + ka[i] : kOutside;
+    }
+#pragma unroll
+    for (int i = 0; i < RW; ++i) {
+      // SwiGLU: 32 gate rows, then their 32 up rows, and so on
+      const int first = (wave * RW + i) * DR, slot = first + lr, row = SWIGLU ? (slot >> 6) * 32 + (slot & 31) : slot;
+      kw[i] = place(slot, lane % PARTS) * 16;
+      rw[i] = make_rsrc(a.w + (n0 + (SWIGLU ? static_cast<int64_t>((first >> 5) & 1) * H : 0)) * a.ldw, bytes);
+      vw[i] = row < nrows ? static_cast<uint32_t>(row * a.ldw) + kw[i] : kOutside;
+    }
+  }
+  constexpr int kIssue = RA + RW;
+  // DMA d of this wave for stage s into the LDS at buf; parts behind K, and whole stages behind
+  // it, are zeros
+  auto issue = [&](int s, int buf, int d) {
+    const int k0 = s * KB;
+    if (d < RA) {
+      dma16(ra, k0 + ka[d] < a.K ? va[d] : kOutside, k0, lds0 + buf + (wave * RA + d) * 1024);
+    } else {
+      d -= RA;
+      dma16(rw[d], k0 + kw[d] < a.K ? vw[d] : kOutside, k0, lds0 + buf + BM * KB + (wave * RW + d) * 1024);
+    }
   };
-  const int wm = (wave & 1) * 32, wn = (wave >> 1) * 32;
-  v4i acc[2][2] = {};
-  for (int k0 = 0; k0 < a.K; k0 += 128) {
-    __syncthreads();
+
+  const int wm = wave % WM * (BM / WM), wn = wave / WM * (BN / WN);
+  uint32_t la[US];  // this lane's operand inside a 32-row tile, for each 32 of K
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const int c = threadIdx.x + 256 * i, r = c >> 3, ch = c & 7;
-      lds_a[r * 8 + (ch ^ (r & 7))] = row16(a.a + (m0 + r) * a.lda, k0 + ch * 16, a.K, m0 + r < a.M);
-      const int n = wrow(r);
-      lds_w[r * 8 + (ch ^ (r & 7))] = row16(a.w + static_cast<int64_t>(n) * a.ldw, k0 + ch * 16, a.K, n >= 0);
+  for (int u = 0; u < US; ++u) la[u] = (lane & 31) * KB + place(lane & 31, u * 2 + (lane >> 5)) * 16;
+  v16i acc[TN][TM] = {};
+  v4i fa[2][TM], fw[2][TN];
+  // the TM + TN reads of a step, spread over the first half of the rows of MFMAs before it
+  constexpr int kPart = TN > 1 ? (TM + TN + TN / 2 - 1) / (TN / 2) : TM + TN;
+  auto read = [&](int buf, int u, int from) {
+    const unsigned char* p = smem + buf + la[u];
+#pragma unroll
+    for (int f = from; f < from + kPart && f < TM + TN; ++f) {
+      if (f < TM) fa[u & 1][f] = *reinterpret_cast<const v4i*>(p + (wm + f * 32) * KB);
+      else fw[u & 1][f - TM] = *reinterpret_cast<const v4i*>(p + (BM + wn + (f - TM) * 32) * KB);
     }
-    __syncthreads();
+  };
+  auto mult = [&](int h, int i) {
 #pragma unroll
-    for (int s = 0; s < 2; ++s) {
-      v4i fw[2], fa[2];
+    for (int j = 0; j < TM; ++j) acc[i][j] = __builtin_amdgcn_mfma_i32_32x32x32_i8(fw[h][i], fa[h][j], acc[i][j], 0, 0, 0);
+  };
+  // a stage's DMAs are issued over the US steps after its buffer is free, some behind each row
+  auto slot = [](int p) { return p * kIssue / (US * TN); };
+  const int n = (a.K + KB - 1) / KB;
+  // scales and bias of the tile, behind the stages, in the order of its rows; they go the same
+  // way, first: an ordinary load among the DMAs would have to wait for all of them
+  const float* const sw = reinterpret_cast<const float*>(smem + NS * kStage);
+  const float* const bias = sw + BN;
+  const float* const sa = bias + BN;
+  {
+    const uint32_t dst = lds0 + NS * kStage;
+    const int cols = H - n0;  // columns from here on
+    for (int b = wave; b < BN / 64; b += NW) {
+      // 64 tile rows: 64 columns, or 32 and then the same 32 of the other half
+      const int c = SWIGLU ? b * 32 + (lane & 31) : b * 64 + lane;
+      const uint32_t off = c < cols ? (c + (SWIGLU && lane >= 32 ? H : 0)) * 4u : kOutside;
+      const uint32_t bytes = static_cast<uint32_t>(a.N - n0) * 4u;
+      dma4(make_rsrc(a.sw + n0, bytes), off, dst + b * 256);
+      dma4(make_rsrc(a.bias + n0, a.bias ? bytes : 0u), off, dst + (BN + b * 64) * 4);
+    }
+    for (int b = wave; b < BM / 64; b += NW)
+      dma4(make_rsrc(a.sa + m0, static_cast<uint32_t>(mrows) * 4u), (b * 64 + lane) * 4u, dst + (2 * BN + b * 64) * 4);
+  }
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const int rw = wn + i * 16 + (lane & 15), ra = wm + i * 16 + (lane & 15), ch = s * 4 + (lane >> 4);
-        fw[i] = *reinterpret_cast<const v4i*>(&lds_w[rw * 8 + (ch ^ (rw & 7))]);
-        fa[i] = *reinterpret_cast<const v4i*>(&lds_a[ra * 8 + (ch ^ (ra & 7))]);
+  for (int s = 0; s < NS; ++s) {
+#pragma unroll
+    for (int d = 0; d < (s < NS - 1 ? kIssue : slot(TN)); ++d) issue(s, s * kStage, d);
+  }
+  wait_vm<kIssue*(NS - 2) + slot(TN)>();
+  __builtin_amdgcn_s_barrier();
+  compiler_fence();
+#pragma unroll
+  for (int f = 0; f < TM + TN; f += kPart) read(0, 0, f);
+  compiler_fence();
+  // Each step multiplies what the step before read, a row of MFMAs at a time; the next step's
+  // reads and the DMA issues (which hold a wave up for some 90 cycles each) go between the
+  // rows, in the order written.
+  int prev = (NS - 1) * kStage, cur = 0;  // LDS offsets of stages s - 1 and s
+  for (int s = 0; s < n; ++s) {
+    const int next = cur + kStage == NS * kStage ? 0 : cur + kStage;
+#pragma unroll
+    for (int u = 0; u < US; ++u) {
+      if (u == US - 1) {
+        // this stage is read out and the next has landed, for every wave
+        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+        wait_vm<kIssue*(NS - 2)>();
+        __builtin_amdgcn_s_barrier();
+        compiler_fence();
+        __builtin_amdgcn_sched_barrier(0);
       }
 #pragma unroll
-      for (int i = 0; i < 2; ++i)
+      for (int i = 0; i < TN; ++i) {
+        read(u == US - 1 ? next : cur, (u + 1) % US, i * kPart);
+        mult(u & 1, i);
+        const int p = (u + 1) % US * TN + i;
 #pragma unroll
-        for (int j = 0; j < 2; ++j) acc[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(fw[i], fa[j], acc[i][j], 0, 0, 0);
-    }
-  }
-  using T = typename Elem<OUT>::T;
-#pragma unroll
-  for (int j = 0; j < 2; ++j) {
-    const int64_t m = m0 + wm + j * 16 + (lane & 15);
-    if (m >= a.M) continue;
-    const float sa = a.sa[m];
-#pragma unroll
-    for (int i = 0; i < (SWIGLU ? 1 : 2); ++i)
-#pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const int n = SWIGLU ? n0 + (wn >> 1) + (lane >> 4) * 4 + q : n0 + wn + i * 16 + (lane >> 4) * 4 + q;
-        if (n >= H) continue;
-        float y = static_cast<float>(acc[i][j][q]) * sa * a.sw[n] + (a.bias ? a.bias[n] : 0.0f);
-        if (SWIGLU) {
-          const float up = static_cast<float>(acc[1][j][q]) * sa * a.sw[H + n] + (a.bias ? a.bias[H + n] : 0.0f);
-          y = silu(y) * up;
+        for (int d = slot(p); d < slot(p + 1); ++d) {
+          if (u == US - 1) issue(s + NS, cur, d);
+          else issue(s + NS - 1, prev, d);
         }
-        if (a.add) y += to_f32<OUT>(static_cast<const T*>(a.add)[m * a.ldadd + n]);
-        static_cast<T*>(a.out)[m * a.ldo + n] = from_f32<OUT>(y);
+        __builtin_amdgcn_sched_barrier(0);
       }
+    }
+    prev = cur;
+    cur = next;
+    compiler_fence();
   }
+  wait_vm<0>();
+  __syncthreads();
+  static_assert(NW * kEpilogue<TM, TN, SWIGLU> * 4 <= NS * kStage, "epilogue fits the stages");
+  store_tile<TM, TN, OUT, SWIGLU>(a, acc, reinterpret_cast<float*>(smem) + wave * kEpilogue<TM, TN, SWIGLU>, sw, bias, sa, m0,
+                                  wm, n0, wn);
+}
+
+// The same product for rows of any alignment: 128 tokens x 128 weight rows, four waves, stages of
+// 128 bytes a row that pass through registers (LDS DMA wants 16-byte parts), the next stage's
+// loads in flight while one is multiplied.
+template <int OUT, bool SWIGLU>
+__global__ __launch_bounds__(256, 2) void linear_any_kernel(LinearArgs a, uint32_t nx) {
+  constexpr int BM = 128, BN = 128, KB = 128, kStage = (BM + BN) * KB, TM = 2, TN = 2;
+  extern __shared__ __attribute__((aligned(16))) unsigned char smem[];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int64_t m0 = static_cast<int64_t>(blockIdx.x / nx) * BM;
+  const int H = SWIGLU ? a.N / 2 : a.N, n0 = (blockIdx.x % nx) * (SWIGLU ? BN / 2 : BN);
+  auto place = [](int r, int c) { return c ^ ((r >> 1) & 7); };
+  auto wrow = [&](int r) -> int64_t {  // the weight row in row r of the tile, or -1
+    const int c = n0 + (SWIGLU ? (r >> 6) * 32 + (r & 31) : r);
+    return c < H ? c + (SWIGLU ? static_cast<int64_t>((r >> 5) & 1) * H : 0) : -1;
+  };
+  float* const sw = reinterpret_cast<float*>(smem + 2 * kStage);
+  float* const bias = sw + BN;
+  float* const sa = bias + BN;
+  if (threadIdx.x < BN) {
+    const int64_t r = wrow(threadIdx.x);
+    sw[threadIdx.x] = r >= 0 ? a.sw[r] : 0.0f;
+    bias[threadIdx.x] = r >= 0 && a.bias ? a.bias[r] : 0.0f;
+  } else {
+    const int r = threadIdx.x - BN;
+    sa[r] = m0 + r < a.M ? a.sa[m0 + r] : 0.0f;
+  }
+  // this thread's parts: part threadIdx.x % 8 of rows threadIdx.x / 8 + 32 i
+  const int part = threadIdx.x & 7, r0 = threadIdx.x >> 3;
+  const int8_t *pa[4], *pw[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int r = r0 + 32 * i;
+    const int64_t n = wrow(r);  // rows outside: the last one, its products are not stored
+    pa[i] = a.a + (m0 + r < a.M ? m0 + r : a.M - 1) * a.lda;
+    pw[i] = a.w + (n >= 0 ? n : static_cast<int64_t>(a.N) - 1) * a.ldw;
+  }
+  Words ga[4], gw[4];
+  auto load = [&](int s) {
+    const int k = s * KB + part * 16;
+    const bool whole = (s + 1) * KB <= a.K;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      ga[i] = words16(pa[i] + k, whole, pa[i] + a.K);
+      gw[i] = words16(pw[i] + k, whole, pw[i] + a.K);
+    }
+  };
+  auto store = [&](int s, int buf) {
+    const int left = (s + 1) * KB <= a.K ? 16 : a.K - s * KB - part * 16;  // bytes behind K count as zero
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int r = r0 + 32 * i;
+      *reinterpret_cast<v4i*>(smem + buf + r * KB + place(r, part) * 16) = bytes16(ga[i], skip_of(pa[i]), 16);
+      *reinterpret_cast<v4i*>(smem + buf + (BM + r) * KB + place(r, part) * 16) = bytes16(gw[i], skip_of(pw[i]), left);
+    }
+  };
+  const int wm = (wave & 1) * 64, wn = (wave >> 1) * 64, n = (a.K + KB - 1) / KB;
+  v16i acc[TN][TM] = {};
+  load(0);
+  store(0, 0);
+  __syncthreads();
+  for (int s = 0; s < n; ++s) {
+    const int cur = (s & 1) * kStage;
+    if (s + 1 < n) load(s + 1);
+    compiler_fence();
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const int off = (lane & 31) * KB + place(lane & 31, u * 2 + (lane >> 5)) * 16;
+      v4i fa[TM], fw[TN];
+#pragma unroll
+      for (int j = 0; j < TM; ++j) fa[j] = *reinterpret_cast<const v4i*>(smem + cur + (wm + j * 32) * KB + off);
+#pragma unroll
+      for (int i = 0; i < TN; ++i) fw[i] = *reinterpret_cast<const v4i*>(smem + cur + (BM + wn + i * 32) * KB + off);
+#pragma unroll
+      for (int i = 0; i < TN; ++i)
+#pragma unroll
+        for (int j = 0; j < TM; ++j) acc[i][j] = __builtin_amdgcn_mfma_i32_32x32x32_i8(fw[i], fa[j], acc[i][j], 0, 0, 0);
+    }
+    if (s + 1 < n) store(s + 1, kStage - cur);
+    __syncthreads();
+  }
+  static_assert(4 * kEpilogue<TM, TN, SWIGLU> * 4 <= 2 * kStage, "epilogue fits the stages");
+  store_tile<TM, TN, OUT, SWIGLU>(a, acc, reinterpret_cast<float*>(smem) + wave * kEpilogue<TM, TN, SWIGLU>, sw, bias, sa, m0,
+                                  wm, n0, wn);
 }
 
 // ---------------------------------------------------------------------- host
@@ -1024,47 +1126,64 @@ int launch_gate(const GateArgs& a, hipStream_t st) {
   return launch_gate_tile<P, 4, 5, 4>(a, st);
 }
 
-template <int OUT, bool SWIGLU, bool ALIGNED, int TT, int WV>
+template <int OUT, bool SWIGLU, bool ALIGNED, int RT, int TT, int WV>
 int launch_stream(const LinearArgs& a, hipStream_t st) {
   static std::atomic<uint64_t> done{0};
-  constexpr size_t lds = sizeof(int) * WV * 16 * TT * ((SWIGLU ? 32 : 16) + 4);
-  if (!allow_lds(linear_stream_kernel<OUT, SWIGLU, ALIGNED, TT, WV>, lds, done)) return MOE_EHIP;
-  const int cols = SWIGLU ? a.N / 2 : a.N;
-  hipLaunchKernelGGL((linear_stream_kernel<OUT, SWIGLU, ALIGNED, TT, WV>), dim3((cols + 15) / 16), dim3(64 * WV), lds, st,
-                     a);
+  constexpr size_t lds = sizeof(int) * WV * 16 * TT * (16 * RT + 4);
+  if (!allow_lds(linear_stream_kernel<OUT, SWIGLU, ALIGNED, RT, TT, WV>, lds, done)) return MOE_EHIP;
+  const int cols = SWIGLU ? a.N / 2 : a.N, per = SWIGLU ? 16 : 16 * RT;
+  const uint32_t nx = static_cast<uint32_t>((cols + per - 1) / per), ny = static_cast<uint32_t>((a.M + 16 * TT - 1) / (16 * TT));
+  hipLaunchKernelGGL((linear_stream_kernel<OUT, SWIGLU, ALIGNED, RT, TT, WV>), dim3(nx * ny), dim3(64 * WV), lds, st, a,
+                     nx);
   return launch_status();
 }
 
-template <int BM, int BN, int WM, int WN, int NS, int OUT, bool SWIGLU>
+template <int BM, int BN, int WM, int WN, int KB, int NS, int OUT, bool SWIGLU>
 int launch_dma(const LinearArgs& a, hipStream_t st) {
   static std::atomic<uint64_t> done{0};
-  constexpr size_t lds = NS * (BM + BN) * 64 + 4 * (BM + 2 * BN);
-  if (!allow_lds(linear_dma_kernel<BM, BN, WM, WN, NS, OUT, SWIGLU>, lds, done)) return MOE_EHIP;
+  constexpr size_t lds = NS * (BM + BN) * KB + 4 * (BM + 2 * BN);
+  static_assert(lds <= 160 * 1024, "LDS of a CU");
+  if (!allow_lds(linear_dma_kernel<BM, BN, WM, WN, KB, NS, OUT, SWIGLU>, lds, done)) return MOE_EHIP;
   const uint32_t nm = static_cast<uint32_t>((a.M + BM - 1) / BM), bn = SWIGLU ? BN / 2 : BN,
                  nn = static_cast<uint32_t>(((SWIGLU ? a.N / 2 : a.N) + bn - 1) / bn), per = (nm * nn + 7) / 8;
-  hipLaunchKernelGGL((linear_dma_kernel<BM, BN, WM, WN, NS, OUT, SWIGLU>), dim3(per * 8), dim3(64 * WM * WN), lds, st, a, nm, nn, per);
+  hipLaunchKernelGGL((linear_dma_kernel<BM, BN, WM, WN, KB, NS, OUT, SWIGLU>), dim3(per * 8), dim3(64 * WM * WN), lds, st, a, nm, nn, per);
   return launch_status();
 }
 
 template <int OUT, bool SWIGLU, bool ALIGNED>
 int launch_linear(const LinearArgs& a, hipStream_t st) {
-  if (a.M <= 16) return launch_stream<OUT, SWIGLU, ALIGNED, 1, 16>(a, st);
-  if (a.M <= 32) return launch_stream<OUT, SWIGLU, ALIGNED, 2, 8>(a, st);
-  if (a.M <= 64) return launch_stream<OUT, SWIGLU, ALIGNED, 4, 8>(a, st);
+  // two row tiles halve the reads of a, where there are workgroups enough without
+  constexpr int R1 = SWIGLU ? 2 : 1;
+  const bool wide = a.N >= 8192;
+  // beyond 64 tokens in blocks of 64, as long as there are few: then tiles leave most CUs idle
+  // (256 x 768 x 3584: 10.6 us against 12.8; 512 x 768: 20.1 against 13.0)
+  const int64_t blocks = static_cast<int64_t>((a.M + 63) / 64) * (((SWIGLU ? a.N / 2 : a.N) + 15) / 16);
+  if (a.M <= 16) return launch_stream<OUT, SWIGLU, ALIGNED, R1, 1, 16>(a, st);
+  if (a.M <= 32)
+    return wide ? launch_stream<OUT, SWIGLU, ALIGNED, 2, 2, 8>(a, st) : launch_stream<OUT, SWIGLU, ALIGNED, R1, 2, 8>(a, st);
+  if (a.M <= 64 || blocks <= 256)
+    return wide ? launch_stream<OUT, SWIGLU, ALIGNED, 2, 4, 8>(a, st) : launch_stream<OUT, SWIGLU, ALIGNED, R1, 4, 8>(a, st);
   if constexpr (ALIGNED) {
-    // rounds of tiles over the CUs, weighed with the time of a tile
+    // Rounds of tiles over 256 CUs, weighed with a round's time at K = 4096 (us, less what every
+    // call pays): large tiles move fewer bytes for each product, small ones fill the CUs.
     const int64_t cols = SWIGLU ? a.N / 2 : a.N;
-    auto rounds = [&](int bm, int bn) {
+    auto cost = [&](int bm, int bn, int us) {
       const int64_t b = SWIGLU ? bn / 2 : bn;
-      return (((a.M + bm - 1) / bm) * ((cols + b - 1) / b) + 255) / 256;
+      return (((a.M + bm - 1) / bm) * ((cols + b - 1) / b) + 255) / 256 * us;
     };
-    const int64_t big = rounds(256, 256) * 40, mid = rounds(128, 128) * 16;
-    if (big <= mid) return launch_dma<256, 256, 2, 4, 4, OUT, SWIGLU>(a, st);
-    return launch_dma<128, 128, 2, 2, 4, OUT, SWIGLU>(a, st);
+    const int64_t c0 = cost(64, 128, 22), c1 = cost(128, 128, 35), c2 = cost(128, 256, 64), c3 = cost(256, 256, 124);
+    const int64_t best = std::min(std::min(c0, c1), std::min(c2, c3));
+    if (best == c3) return launch_dma<256, 256, 2, 4, 128, 2, OUT, SWIGLU>(a, st);
+    if (best == c2) return launch_dma<128, 256, 2, 4, 128, 3, OUT, SWIGLU>(a, st);
+    if (best == c1) return launch_dma<128, 128, 4, 2, 128, 4, OUT, SWIGLU>(a, st);
+    return launch_dma<64, 128, 2, 2, 128, 3, OUT, SWIGLU>(a, st);
   }
-  const unsigned my = static_cast<unsigned>((a.M + 63) / 64);
-  const unsigned nx = static_cast<unsigned>(SWIGLU ? (a.N / 2 + 31) / 32 : (a.N + 63) / 64);
-  hipLaunchKernelGGL((linear_tile_kernel<OUT, SWIGLU>), dim3(nx * my), dim3(256), 0, st, a, nx);
+  static std::atomic<uint64_t> done{0};
+  constexpr size_t lds = 2 * 256 * 128 + 4 * (128 + 2 * 128);
+  if (!allow_lds(linear_any_kernel<OUT, SWIGLU>, lds, done)) return MOE_EHIP;
+  const uint32_t ny = static_cast<uint32_t>((a.M + 127) / 128);
+  const uint32_t nx = static_cast<uint32_t>(SWIGLU ? (a.N / 2 + 63) / 64 : (a.N + 127) / 128);
+  hipLaunchKernelGGL((linear_any_kernel<OUT, SWIGLU>), dim3(nx * ny), dim3(256), lds, st, a, nx);
   return launch_status();
 }
 
@@ -1080,7 +1199,7 @@ extern "C" {
 
 size_t moe_gate_packed_bytes(int32_t E, int32_t D, int32_t wtype) {
   if (!gate_ok(E, D, wtype)) return 0;
-  return static_cast<size_t>((E + 15) / 16) * 16 * D * 2 * (wtype == MOE_F32 ? 3 : 1);
+  return static_cast<size_t>((E + 15) / 16) * 16 * D * elem_size(wtype);
 }
 
 int moe_gate_pack(const void* w, int32_t wtype, int32_t E, int32_t D, void* packed, size_t packed_bytes,
@@ -1090,11 +1209,11 @@ int moe_gate_pack(const void* w, int32_t wtype, int32_t E, int32_t D, void* pack
   const int64_t n = static_cast<int64_t>((E + 15) / 16) * (D / 32) * 64;
   const dim3 grid(static_cast<unsigned>((n + 255) / 256));
   if (wtype == MOE_F32)
-    hipLaunchKernelGGL(gate_pack_kernel<MOE_F32>, grid, dim3(256), 0, as_stream(stream), w, E, D,
-                       static_cast<uint16_t*>(packed));
+    hipLaunchKernelGGL(gate_pack_kernel<float>, grid, dim3(256), 0, as_stream(stream), static_cast<const float*>(w), E, D,
+                       static_cast<float*>(packed));
   else
-    hipLaunchKernelGGL(gate_pack_kernel<MOE_BF16>, grid, dim3(256), 0, as_stream(stream), w, E, D,
-                       static_cast<uint16_t*>(packed));
+    hipLaunchKernelGGL(gate_pack_kernel<uint16_t>, grid, dim3(256), 0, as_stream(stream),
+                       static_cast<const uint16_t*>(w), E, D, static_cast<uint16_t*>(packed));
   return launch_status();
 }
 
@@ -1102,8 +1221,7 @@ int moe_gate(const moe_gate_t* g, const void* x, int64_t ldx, int32_t B, float* 
   if (!g || !g->packed || !x || !logits || !gate_ok(g->E, g->D, g->wtype) || B < 1 || B > kMaxRows || ldx < g->D || ldx % 8 ||
       ldl < g->E || reinterpret_cast<uintptr_t>(x) % 16 || reinterpret_cast<uintptr_t>(g->packed) % 16)
     return MOE_EINVAL;
-  const GateArgs a = {static_cast<const uint16_t*>(x), ldx,    static_cast<const uint16_t*>(g->packed), B, g->E, g->D,
-                      logits,                          ldl};
+  const GateArgs a = {static_cast<const uint16_t*>(x), ldx, g->packed, B, g->E, g->D, logits, ldl};
   return g->wtype == MOE_F32 ? launch_gate<3>(a, as_stream(stream)) : launch_gate<1>(a, as_stream(stream));
 }
 
