@@ -352,8 +352,9 @@ int moe_combine(const void* rows_dev, size_t rows_bytes, const float* weights_de
 
 enum moe_dtype { MOE_BF16 = 0, MOE_F16 = 1, MOE_F32 = 2 };
 
-/* Bytes of the router weight [E, D] laid out by moe_gate_pack: its own (wtype MOE_BF16 or
- * MOE_F32), E padded to a multiple of 16.  0 on invalid sizes (1 <= E <=
+/* Bytes of the router weight [E, D] laid out by moe_gate_pack, E padded to a multiple of 16:
+ * wtype MOE_BF16 as it is, MOE_F32 in three BF16 planes, the upper, middle and lower eight
+ * significant bits of a weight.  0 on invalid sizes (1 <= E <=
  * 1024, 512 <= D <= 16384 with D % 512 == 0, as the experts). */
 size_t moe_gate_packed_bytes(int32_t E, int32_t D, int32_t wtype);
 

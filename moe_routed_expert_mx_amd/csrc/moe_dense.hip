@@ -414,10 +414,16 @@ __global__ __launch_bounds__(256) void quant_kernel(const void* x, int64_t ldx, 
 }
 
 // ---------------------------------------------------------------------- gate
-// Packed router weight: [E/16][D/32][64 lanes][8 weights], lane l of a run holding expert l % 16,
-// features 8 * (l / 16) .. + 7 of the step: the order of the 16x16x32 MFMA's operand.
-template <typename T>
-__global__ __launch_bounds__(256) void gate_pack_kernel(const T* w, int32_t E, int32_t D, T* packed) {
+// Packed router weight: [E/16][D/32][plane] runs of the 16x16x32 MFMA's operand, 1 KB each: lane
+// l holds expert l % 16, features 8 * (l / 16) .. + 7 of the step.  An FP32 weight is cut into its
+// upper, middle and lower eight significant bits, each a BF16 exactly, whose three planes' products
+// are summed: the BF16 rate is sixteen times the FP32 one.  Cutting in the kernel instead (4 bytes
+// a weight instead of 6) took 44 vector instructions to a tile's 12 MFMAs and longer in all
+// (8192 tokens: 35 us against 31).
+template <int WTYPE>
+__global__ __launch_bounds__(256) void gate_pack_kernel(const typename Elem<WTYPE>::T* w, int32_t E, int32_t D,
+                                                        uint16_t* packed) {
+  constexpr int P = WTYPE == MOE_F32 ? 3 : 1;
   const int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
   const int steps = D / 32;
   const int64_t n = static_cast<int64_t>((E + 15) / 16) * steps * 64;
@@ -427,37 +433,18 @@ __global__ __launch_bounds__(256) void gate_pack_kernel(const T* w, int32_t E, i
   const int s = static_cast<int>(run % steps);
   const int e = static_cast<int>(run / steps) * 16 + (lane & 15);
   const int k = s * 32 + (lane >> 4) * 8;
-  for (int j = 0; j < 8; ++j) packed[i * 8 + j] = e < E ? w[static_cast<int64_t>(e) * D + k + j] : T(0);
-}
-
-// Eight weights as they lie in memory, and as P BF16 operands whose sum they are.  An FP32
-// weight is cut into its upper, middle and lower eight significant bits, each a BF16 exactly:
-// three MFMAs at the BF16 rate then do what FP32 ones would need sixteen times the time for.
-template <int P>
-struct GateWeights;
-template <>
-struct GateWeights<1> {
-  v8bf w;
-  __device__ __forceinline__ void split(v8bf (&o)[1]) const { o[0] = w; }
-};
-template <>
-struct GateWeights<3> {
-  uint32_t w[8];
-  __device__ __forceinline__ void split(v8bf (&o)[3]) const {
-    uint32_t p[3][4];
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      uint32_t a = w[2 * j], b = w[2 * j + 1];
-#pragma unroll
-      for (int i = 0; i < 3; ++i) {
-        p[i][j] = __builtin_amdgcn_perm(b, a, 0x07060302);  // both upper halves
-        a = __float_as_uint(__uint_as_float(a) - __uint_as_float(a & 0xffff0000u));
-        b = __float_as_uint(__uint_as_float(b) - __uint_as_float(b & 0xffff0000u));
-      }
+  for (int j = 0; j < 8; ++j) {
+    float v = e < E ? to_f32<WTYPE>(w[static_cast<int64_t>(e) * D + k + j]) : 0.0f;
+    for (int p = 0; p < P; ++p) {
+      const uint32_t b = __float_as_uint(v);
+      const bool finite = (b & 0x7fffffffu) < 0x7f800000u;
+      uint16_t h = static_cast<uint16_t>(b >> 16);  // cut off towards zero; the rest is exact
+      if (!finite && (b & 0x7fffffu)) h |= 0x40;
+      packed[(run * P + p) * 512 + lane * 8 + j] = h;
+      v = finite ? v - bf16_to_f32(h) : 0.0f;
     }
-    __builtin_memcpy(&o, &p, sizeof(p));
   }
-};
+}
 
 struct GateArgs {
   const uint16_t* x;
@@ -469,72 +456,95 @@ struct GateArgs {
 };
 
 // A workgroup's tile is 16 TT tokens x 16 ET experts; its WV waves take a share of the features
-// each, read both operands straight into registers (no byte is read twice in a workgroup, so
-// LDS would serve nothing) and add their FP32 tiles through LDS in wave order.
+// each and add their FP32 tiles through LDS in wave order.  The packed weight comes straight into
+// registers.  x is loaded eight lanes to a row, 64 features at a time, and turned into operands
+// through LDS of the wave's own: read in the operand's layout, every lane at a row of its own,
+// it took four times the L1's time and set the pace (8192 tokens, FP32 weight: 40 us).
 template <int P, int TT, int ET, int WV>
 __global__ __launch_bounds__(64 * WV) void gate_kernel(GateArgs a, uint32_t cols, uint32_t rows) {
-  extern __shared__ float gate_lds[];
-  constexpr int kOut = 256 * TT * ET;           // outputs of the tile
-  // steps in flight: of x, which comes from HBM, and of the weight, which L2 holds
-  constexpr int UX = TT * ET >= 8 ? 8 : 4, UW = TT * ET >= 8 ? 2 : 4;
+  extern __shared__ __attribute__((aligned(16))) float gate_lds[];
+  constexpr int kOut = 256 * TT * ET;  // outputs of the tile
+  // in flight, as far as the registers of a wave go: UX blocks of 64 features of x, which comes
+  // from HBM, and UW steps of 32 of the weight, which L2 holds
+  constexpr int kRegs = 2048 / WV - 4 * TT * ET - (WV == 4 ? 192 : 64);
+  constexpr int fit = (kRegs - 16 * TT) / (4 * P * ET), UW = fit >= 8 ? 8 : fit >= 4 ? 4 : 2;
+  constexpr int UX = kRegs - UW * 4 * P * ET >= 32 * TT ? 4 : 2, UN = UX > UW / 2 ? UX : UW / 2;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   // the tiles of one token range run on one XCD (workgroups go round the eight), so that its L2
   // serves x to all of them
   const uint32_t span = 8 * cols, row = blockIdx.x / span * 8 + blockIdx.x % 8, col = blockIdx.x % span / 8;
   if (row >= rows) return;
   const int64_t t0 = static_cast<int64_t>(row) * (16 * TT);
-  const int tiles = (a.E + 15) / 16, steps = a.D / 32, n = steps / WV, s0 = wave * n;
-  const uint16_t* xp[TT];
-  const GateWeights<P>* wp[ET];
+  // blocks of 64 features, shared out evenly
+  const int tiles = (a.E + 15) / 16, steps = a.D / 32, blocks = steps / 2;
+  const int b0 = wave * blocks / WV, n = (wave + 1) * blocks / WV - b0;
+  const uint16_t* xp[2 * TT];
+  const v8bf* wp[ET];
 #pragma unroll
-  for (int i = 0; i < TT; ++i) {
-    const int64_t t = t0 + i * 16 + (lane & 15);
-    xp[i] = a.x + (t < a.B ? t : a.B - 1) * a.ldx + s0 * 32 + (lane >> 4) * 8;
+  for (int i = 0; i < 2 * TT; ++i) {
+    const int64_t t = t0 + i * 8 + (lane >> 3);
+    xp[i] = a.x + (t < a.B ? t : a.B - 1) * a.ldx + b0 * 64 + (lane & 7) * 8;
   }
 #pragma unroll
   for (int i = 0; i < ET; ++i) {
     const int et = static_cast<int>(col) * ET + i;
-    wp[i] = static_cast<const GateWeights<P>*>(a.packed) +
-            (static_cast<int64_t>(et < tiles ? et : tiles - 1) * steps + s0) * 64 + lane;
+    wp[i] = static_cast<const v8bf*>(a.packed) +
+            (static_cast<int64_t>(et < tiles ? et : tiles - 1) * steps + b0 * 2) * (64 * P) + lane;
   }
   v4f acc[TT][ET] = {};
-  v8bf xb[UX][TT];
-  GateWeights<P> wb[UW][ET];
+  v4i xb[UX][2 * TT];
+  v8bf wb[UW][ET][P];
   auto load_x = [&](int u, int s) {
-    s = s < n ? s : n - 1;  // past the end: loaded again, not used
 #pragma unroll
-    for (int i = 0; i < TT; ++i) xb[u][i] = *reinterpret_cast<const v8bf*>(xp[i] + s * 32);
+    for (int i = 0; i < 2 * TT; ++i) xb[u][i] = *reinterpret_cast<const v4i*>(xp[i] + s * 64);
   };
-  auto load_w = [&](int u, int s) {
-    s = s < n ? s : n - 1;
+  auto load_w = [&](int u, int k) {
 #pragma unroll
-    for (int i = 0; i < ET; ++i) wb[u][i] = wp[i][s * 64];
+    for (int i = 0; i < ET; ++i)
+#pragma unroll
+      for (int p = 0; p < P; ++p) wb[u][i][p] = wp[i][(k * P + p) * 64];
   };
+  unsigned char* const own = reinterpret_cast<unsigned char*>(gate_lds) + wave * (TT * 2048);
+  auto place = [](int r, int c) { return r * 128 + (c ^ ((r >> 1) & 7)) * 16; };
 #pragma unroll
-  for (int u = 0; u < UX; ++u) load_x(u, u);
+  for (int u = 0; u < UX; ++u)
+    if (u < n) load_x(u, u);
 #pragma unroll
-  for (int u = 0; u < UW; ++u) load_w(u, u);
-  compiler_fence();  // the loads stay where they are written, steps ahead of their use
-  for (int s = 0; s < n; s += UX) {
+  for (int u = 0; u < UW; ++u)
+    if (u < 2 * n) load_w(u, u);
+  compiler_fence();  // the loads stay where they are written, ahead of their use
+  for (int s0 = 0; s0 < n; s0 += UN) {
 #pragma unroll
-    for (int u = 0; u < UX; ++u) {
-      if (s + u < n) {
+    for (int v = 0; v < UN; ++v) {
+      const int s = s0 + v;
+      if (s < n) {
 #pragma unroll
-        for (int i = 0; i < ET; ++i) {
-          v8bf w[P];
-          wb[u % UW][i].split(w);
+        for (int i = 0; i < 2 * TT; ++i)
+          *reinterpret_cast<v4i*>(own + place(i * 8 + (lane >> 3), lane & 7)) = xb[v % UX][i];
+        if (s + UX < n) load_x(v % UX, s + UX);
+        wave_sync();
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const int u = (2 * v + h) % UW;
+          v8bf x[TT];
+#pragma unroll
+          for (int j = 0; j < TT; ++j)
+            x[j] = *reinterpret_cast<const v8bf*>(own + place(j * 16 + (lane & 15), h * 4 + (lane >> 4)));
 #pragma unroll
           for (int p = 0; p < P; ++p)
 #pragma unroll
-            for (int j = 0; j < TT; ++j)
-              acc[j][i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(w[p], xb[u][j], acc[j][i], 0, 0, 0);
+            for (int i = 0; i < ET; ++i)
+#pragma unroll
+              for (int j = 0; j < TT; ++j)
+                acc[j][i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wb[u][i][p], x[j], acc[j][i], 0, 0, 0);
+          if (2 * s + h + UW < 2 * n) load_w(u, 2 * s + h + UW);
+          compiler_fence();
         }
-        load_x(u, s + u + UX);
-        load_w(u % UW, s + u + UW);
-        compiler_fence();
+        wave_sync();
       }
     }
   }
+  __syncthreads();
   // [wave][token][expert], padded by a word a row
   constexpr int kRow = 16 * ET + 4;
 #pragma unroll
@@ -544,14 +554,24 @@ __global__ __launch_bounds__(64 * WV) void gate_kernel(GateArgs a, uint32_t cols
       *reinterpret_cast<v4f*>(gate_lds + (wave * 16 * TT + j * 16 + (lane & 15)) * kRow + i * 16 + (lane >> 4) * 4) =
           acc[j][i];
   __syncthreads();
-  for (int o = threadIdx.x; o < kOut; o += 64 * WV) {
-    const int tok = o / (16 * ET), e = o % (16 * ET);
-    float v = gate_lds[tok * kRow + e];
+  const bool vec = (reinterpret_cast<uintptr_t>(a.logits) | (a.ldl * 4)) % 16 == 0;
 #pragma unroll
-    for (int w = 1; w < WV; ++w) v += gate_lds[(w * 16 * TT + tok) * kRow + e];
+  for (int o = threadIdx.x; o < kOut / 4; o += 64 * WV) {
+    const int tok = o / (4 * ET), e = o % (4 * ET) * 4;
+    v4f v = *reinterpret_cast<const v4f*>(gate_lds + tok * kRow + e);
+#pragma unroll
+    for (int w = 1; w < WV; ++w) v += *reinterpret_cast<const v4f*>(gate_lds + (w * 16 * TT + tok) * kRow + e);
     const int64_t t = t0 + tok;
     const int ge = static_cast<int>(col) * 16 * ET + e;
-    if (t < a.B && ge < a.E) a.logits[t * a.ldl + ge] = v;
+    if (t >= a.B) continue;
+    float* out = a.logits + t * a.ldl + ge;
+    if (vec && ge + 4 <= a.E) {
+      *reinterpret_cast<v4f*>(out) = v;
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (ge + i < a.E) out[i] = v[i];
+    }
   }
 }
 
@@ -611,94 +631,102 @@ __device__ __forceinline__ float silu(float g) { return g * __builtin_amdgcn_rcp
 
 // ------------------------------------------------- linear: up to 64 tokens
 // The weight is read once, so its bytes bound the product.  A workgroup takes 16 RT weight rows
-// (SwiGLU: 16 gate rows and their 16 up rows) and all tokens; its WV waves split K, read both
-// operands straight into registers some chunks of 64 bytes ahead, and add their 32-bit sums
-// through LDS.
+// (SwiGLU: 16 gate rows and their 16 up rows) and 16 TT tokens; its WV waves split K in pieces of
+// 128 bytes.  A wave loads a piece's rows eight lanes to a row (lanes that each read a row of
+// their own, as the operand's layout would have it, get a quarter of the L1's rate), some pieces ahead, and
+// turns them into operands through LDS of its own, so that no wave waits for another before
+// the 32-bit sums are added.
 template <int OUT, bool SWIGLU, bool ALIGNED, int RT, int TT, int WV>
 __global__ __launch_bounds__(64 * WV) void linear_stream_kernel(LinearArgs a, uint32_t nx) {
-  extern __shared__ int stream_lds[];
-  constexpr int U = RT + TT >= 5 ? (ALIGNED ? 7 : 4) : ALIGNED ? 8 : 6, COLS = SWIGLU ? 16 : 16 * RT;  // chunks in flight; columns of out
+  extern __shared__ __attribute__((aligned(16))) unsigned char smem[];
+  constexpr int COLS = SWIGLU ? 16 : 16 * RT, NL = 2 * (RT + TT);  // columns of out; loads of a piece
+  constexpr int kRegs = (2048 / WV - 4 * RT * TT - 8 * (RT + TT) - 40) / (NL * (ALIGNED ? 4 : 5));
+  constexpr int U = kRegs > 6 ? 6 : kRegs < 2 ? 2 : kRegs;         // pieces in flight
   static_assert(!SWIGLU || RT == 2, "a gate and an up tile");
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int H = SWIGLU ? a.N / 2 : a.N, n0 = blockIdx.x % nx * COLS, m0 = blockIdx.x / nx * (16 * TT);
-  const int chunks = (a.K + 63) / 64, per = (chunks + WV - 1) / WV, c0 = wave * per;
-  const int n = chunks - c0 < per ? (chunks > c0 ? chunks - c0 : 0) : per;
-  const int r = lane & 15, q = lane >> 4;
-  const int8_t *wp[RT], *ap[TT];
+  const int pieces = (a.K + 127) / 128, per = (pieces + WV - 1) / WV, c0 = wave * per;
+  const int n = pieces - c0 < per ? (pieces > c0 ? pieces - c0 : 0) : per;
+  // load i brings rows 8 i .. 8 i + 7 of the wave's tile: weight rows first, then tokens
+  const int part = lane & 7;
+  const int8_t* rows[NL];
 #pragma unroll
-  for (int i = 0; i < RT; ++i) {
-    const int c = n0 + (SWIGLU ? 0 : i * 16) + r;
-    wp[i] = a.w + ((c < H ? c : H - 1) + (SWIGLU ? static_cast<int64_t>(i) * H : 0)) * a.ldw;
-  }
-#pragma unroll
-  for (int i = 0; i < TT; ++i) ap[i] = a.a + static_cast<int64_t>(m0 + i * 16 + r < a.M ? m0 + i * 16 + r : a.M - 1) * a.lda;
-  using Held = std::conditional_t<ALIGNED, v4i, Words>;
-  v4i acc[RT][TT] = {};
-  Held wb[U][RT], ab[U][TT];
-  // aligned: an operand's 16 bytes lie wholly inside the row or wholly behind it; those behind
-  // are read from the row's last 16 and set to zero when used
-  auto load = [&](int u, int c) {
-    const int k = (c0 + c) * 64 + q * 16;
-    if constexpr (ALIGNED) {
-      const int kc = k < a.K ? k : a.K - 16;
-#pragma unroll
-      for (int i = 0; i < RT; ++i) wb[u][i] = *reinterpret_cast<const v4i*>(wp[i] + kc);
-#pragma unroll
-      for (int i = 0; i < TT; ++i) ab[u][i] = *reinterpret_cast<const v4i*>(ap[i] + kc);
+  for (int i = 0; i < NL; ++i) {
+    const int r = i * 8 + (lane >> 3);
+    if (i < 2 * RT) {
+      const int c = n0 + (SWIGLU ? r & 15 : r);
+      rows[i] = a.w + ((c < H ? c : H - 1) + (SWIGLU ? static_cast<int64_t>(r >> 4) * H : 0)) * a.ldw;
     } else {
-      const bool whole = (c0 + c) * 64 + 64 <= a.K;
+      const int m = m0 + r - 16 * RT;
+      rows[i] = a.a + static_cast<int64_t>(m < a.M ? m : a.M - 1) * a.lda;
+    }
+  }
+  using Held = std::conditional_t<ALIGNED, v4i, Words>;
+  Held held[U][NL];
+  // aligned: 16 bytes lie wholly inside the row or wholly behind it; those behind are read from
+  // the row's last 16 and set to zero when used
+  auto load = [&](int u, int c) {
+    const int k = (c0 + c) * 128 + part * 16;
 #pragma unroll
-      for (int i = 0; i < RT; ++i) wb[u][i] = words16(wp[i] + k, whole, wp[i] + a.K);
-#pragma unroll
-      for (int i = 0; i < TT; ++i) ab[u][i] = words16(ap[i] + k, whole, ap[i] + a.K);
+    for (int i = 0; i < NL; ++i) {
+      if constexpr (ALIGNED) held[u][i] = *reinterpret_cast<const v4i*>(rows[i] + (k < a.K ? k : a.K - 16));
+      else held[u][i] = words16(rows[i] + k, (c0 + c) * 128 + 128 <= a.K, rows[i] + a.K);
     }
   };
-  if (n > 0) {
+  unsigned char* const own = smem + wave * (NL * 1024);
+  auto place = [](int r, int c) { return r * 128 + (c ^ ((r >> 1) & 7)) * 16; };
+  v4i acc[RT][TT] = {};
+#pragma unroll
+  for (int u = 0; u < U; ++u)
+    if (u < n) load(u, u);
+  compiler_fence();
+  for (int c = 0; c < n; c += U) {
 #pragma unroll
     for (int u = 0; u < U; ++u)
-      if (u < n) load(u, u);
-    compiler_fence();
-    for (int c = 0; c < n; c += U) {
+      if (c + u < n) {
+        const int first = (c0 + c + u) * 128, left = first + 128 <= a.K ? 16 : a.K - first - part * 16;
 #pragma unroll
-      for (int u = 0; u < U; ++u)
-        if (c + u < n) {
-          // bytes behind K count as zero; it takes one operand to see to that
-          const int k = (c0 + c + u) * 64 + q * 16;
-          const bool whole = (c0 + c + u) * 64 + 64 <= a.K;
+        for (int i = 0; i < NL; ++i) {  // bytes behind K count as zero; it takes one operand to see to that
+          v4i v;
+          if constexpr (ALIGNED) v = i >= 2 * RT || left > 0 ? held[u][i] : v4i{0, 0, 0, 0};
+          else v = bytes16(held[u][i], skip_of(rows[i]), i < 2 * RT ? left : 16);
+          *reinterpret_cast<v4i*>(own + place(i * 8 + (lane >> 3), part)) = v;
+        }
+        if (c + u + U < n) load(u, c + u + U);
+        wave_sync();
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
           v4i fw[RT], fa[TT];
 #pragma unroll
-          for (int i = 0; i < RT; ++i) {
-            if constexpr (ALIGNED) fw[i] = whole || k < a.K ? wb[u][i] : v4i{0, 0, 0, 0};
-            else fw[i] = bytes16(wb[u][i], skip_of(wp[i]), whole ? 16 : a.K - k);
-          }
+          for (int i = 0; i < RT; ++i)
+            fw[i] = *reinterpret_cast<const v4i*>(own + place(i * 16 + (lane & 15), h * 4 + (lane >> 4)));
 #pragma unroll
-          for (int j = 0; j < TT; ++j) {
-            if constexpr (ALIGNED) fa[j] = ab[u][j];
-            else fa[j] = bytes16(ab[u][j], skip_of(ap[j]), 16);
-          }
+          for (int j = 0; j < TT; ++j)
+            fa[j] = *reinterpret_cast<const v4i*>(own + place((RT + j) * 16 + (lane & 15), h * 4 + (lane >> 4)));
 #pragma unroll
           for (int i = 0; i < RT; ++i)
 #pragma unroll
             for (int j = 0; j < TT; ++j) acc[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(fw[i], fa[j], acc[i][j], 0, 0, 0);
-          if (c + u + U < n) load(u, c + u + U);
-          compiler_fence();
         }
-    }
+        wave_sync();
+      }
   }
   // [wave][token][weight row], padded by four words a row
   constexpr int kRow = 16 * RT + 4, kTile = 16 * TT * kRow;
+  int* const sums = reinterpret_cast<int*>(smem);
+  __syncthreads();
 #pragma unroll
   for (int i = 0; i < RT; ++i)
 #pragma unroll
     for (int j = 0; j < TT; ++j)
-      *reinterpret_cast<v4i*>(stream_lds + wave * kTile + (j * 16 + r) * kRow + i * 16 + q * 4) = acc[i][j];
+      *reinterpret_cast<v4i*>(sums + wave * kTile + (j * 16 + (lane & 15)) * kRow + i * 16 + (lane >> 4) * 4) = acc[i][j];
   __syncthreads();
   using T = typename Elem<OUT>::T;
   for (int o = threadIdx.x; o < COLS * 16 * TT; o += 64 * WV) {
     const int64_t m = m0 + o / COLS;
     const int c = n0 + o % COLS;
     if (m >= a.M || c >= H) continue;
-    const int* p = stream_lds + o / COLS * kRow + o % COLS;
+    const int* p = sums + o / COLS * kRow + o % COLS;
     int sum = 0, sum_up = 0;
 #pragma unroll
     for (int v = 0; v < WV; ++v) {
@@ -1111,7 +1139,7 @@ bool allow_lds(F fn, size_t bytes, std::atomic<uint64_t>& done) {
 template <int P, int TT, int ET, int WV>
 int launch_gate_tile(const GateArgs& a, hipStream_t st) {
   static std::atomic<uint64_t> done{0};
-  constexpr size_t lds = sizeof(float) * WV * 16 * TT * (16 * ET + 4);
+  constexpr size_t lds = WV * std::max(64 * TT * (16 * ET + 4), 2048 * TT);
   static_assert(lds <= 160 * 1024, "gate tile");
   if (!allow_lds(gate_kernel<P, TT, ET, WV>, lds, done)) return MOE_EHIP;
   const uint32_t cols = ((a.E + 15) / 16 + ET - 1) / ET, rows = static_cast<uint32_t>((a.B + 16 * TT - 1) / (16 * TT));
@@ -1122,14 +1150,27 @@ int launch_gate_tile(const GateArgs& a, hipStream_t st) {
 
 template <int P>
 int launch_gate(const GateArgs& a, hipStream_t st) {
-  if (a.B <= 1024) return launch_gate_tile<P, 1, 1, 16>(a, st);
+  // Rounds of tiles over 256 CUs, weighed with a round's time at D = 3584 (in half us, BF16 and
+  // FP32 weight): small tiles fill the CUs, large ones read less.
+  const int64_t tiles = (a.E + 15) / 16;
+  auto cost = [&](int tt, int et, int bf16, int f32) {
+    return ((a.B + 16 * tt - 1) / (16 * tt) * ((tiles + et - 1) / et) + 255) / 256 * (P == 3 ? f32 : bf16);
+  };
+  const int64_t c0 = cost(1, 1, 6, 11), c1 = cost(2, 3, 11, 25), c2 = cost(2, 5, 18, 40), c3 = cost(4, 3, 21, 36),
+                c4 = cost(4, 5, 30, 56);
+  const int64_t best = std::min(std::min(std::min(c0, c1), std::min(c2, c3)), c4);
+  if (best == c0) return launch_gate_tile<P, 1, 1, 8>(a, st);
+  if (best == c1) return launch_gate_tile<P, 2, 3, 8>(a, st);
+  if (best == c2) return launch_gate_tile<P, 2, 5, 8>(a, st);
+  if (best == c3) return launch_gate_tile<P, 4, 3, 8>(a, st);
   return launch_gate_tile<P, 4, 5, 4>(a, st);
 }
 
 template <int OUT, bool SWIGLU, bool ALIGNED, int RT, int TT, int WV>
 int launch_stream(const LinearArgs& a, hipStream_t st) {
   static std::atomic<uint64_t> done{0};
-  constexpr size_t lds = sizeof(int) * WV * 16 * TT * (16 * RT + 4);
+  constexpr size_t lds = WV * std::max(2048 * (RT + TT), 64 * TT * (16 * RT + 4));
+  static_assert(lds <= 160 * 1024, "LDS of a CU");
   if (!allow_lds(linear_stream_kernel<OUT, SWIGLU, ALIGNED, RT, TT, WV>, lds, done)) return MOE_EHIP;
   const int cols = SWIGLU ? a.N / 2 : a.N, per = SWIGLU ? 16 : 16 * RT;
   const uint32_t nx = static_cast<uint32_t>((cols + per - 1) / per), ny = static_cast<uint32_t>((a.M + 16 * TT - 1) / (16 * TT));
@@ -1199,7 +1240,7 @@ extern "C" {
 
 size_t moe_gate_packed_bytes(int32_t E, int32_t D, int32_t wtype) {
   if (!gate_ok(E, D, wtype)) return 0;
-  return static_cast<size_t>((E + 15) / 16) * 16 * D * elem_size(wtype);
+  return static_cast<size_t>((E + 15) / 16) * 16 * D * (wtype == MOE_F32 ? 6 : 2);
 }
 
 int moe_gate_pack(const void* w, int32_t wtype, int32_t E, int32_t D, void* packed, size_t packed_bytes,
@@ -1209,10 +1250,10 @@ int moe_gate_pack(const void* w, int32_t wtype, int32_t E, int32_t D, void* pack
   const int64_t n = static_cast<int64_t>((E + 15) / 16) * (D / 32) * 64;
   const dim3 grid(static_cast<unsigned>((n + 255) / 256));
   if (wtype == MOE_F32)
-    hipLaunchKernelGGL(gate_pack_kernel<float>, grid, dim3(256), 0, as_stream(stream), static_cast<const float*>(w), E, D,
-                       static_cast<float*>(packed));
+    hipLaunchKernelGGL(gate_pack_kernel<MOE_F32>, grid, dim3(256), 0, as_stream(stream),
+                       static_cast<const float*>(w), E, D, static_cast<uint16_t*>(packed));
   else
-    hipLaunchKernelGGL(gate_pack_kernel<uint16_t>, grid, dim3(256), 0, as_stream(stream),
+    hipLaunchKernelGGL(gate_pack_kernel<MOE_BF16>, grid, dim3(256), 0, as_stream(stream),
                        static_cast<const uint16_t*>(w), E, D, static_cast<uint16_t*>(packed));
   return launch_status();
 }

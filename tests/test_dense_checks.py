@@ -14,7 +14,7 @@ BF, F16, F32 = torch.bfloat16, torch.float16, torch.float32
 
 def test_gate_sizes_and_refusals():
     assert m.moe_gate_packed_bytes(160, 3584, BF) == 160 * 3584 * 2
-    assert m.moe_gate_packed_bytes(161, 512, F32) == 176 * 512 * 4
+    assert m.moe_gate_packed_bytes(161, 512, F32) == 176 * 512 * 6
     for e, d, t in ((0, 512, BF), (1025, 512, BF), (8, 500, BF), (8, 0, BF), (8, 16896, BF), (8, 512, F16)):
         assert m.moe_gate_packed_bytes(e, d, t) == 0
     big = 1 << 30
