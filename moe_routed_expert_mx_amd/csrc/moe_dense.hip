@@ -144,20 +144,25 @@ __device__ __forceinline__ double exp_f64(double x) {
   return __builtin_ldexp(p, static_cast<int>(n));
 }
 
-// LPT lanes per token, lane l of them holding experts l, l + LPT, ..., NV of them at most.
-// Each lane sorts its choices (stably, so that equal ones stay in index order) into LDS; then
-// the lanes' heads compete topk times: the largest upper word by rotations among the lanes,
-// and only where several lanes share it the lower word and the index.
+// LPT lanes per token, lane l of them holding experts l, l + LPT, ..., NV of them at most.  Each
+// lane sorts its choices into LDS; then the lanes' heads compete topk times, by rotations among
+// the lanes.
+//
+// First with the choice in FP32, cut to 28 bits, its lane's slot in the other four: sorting takes
+// a maximum and a minimum a pair, a head's contest four rotations.  Whatever lies closer
+// together than that arithmetic can tell apart (two neighbours of the result, or the first left
+// out, or two groups) is noticed, and the wave goes again with the choice in FP64, about three
+// times the work; for random logits that is less than one wave in a hundred.
 template <int LPT, int NV>
 __global__ __launch_bounds__(256) void route_kernel(RouteArgs a) {
   constexpr int TPW = 64 / LPT;
+  static_assert(NV <= 16, "four bits of slot");
   __shared__ uint64_t lds_key[4][NV][64];
   __shared__ uint16_t lds_id[4][NV][64];
   __shared__ uint16_t lds_out[4][TPW][64];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, l = lane % LPT, sub = lane / LPT;
   const int64_t tok = (static_cast<int64_t>(blockIdx.x) * 4 + wave) * TPW + sub, t = tok < a.B ? tok : a.B - 1;
   const float kMasked = -__builtin_huge_valf();
-  const double kNone = -__builtin_huge_val();
   auto logit_at = [&](int e) {
     const int64_t i = t * a.ldl + e;
     float v;
@@ -180,101 +185,190 @@ __global__ __launch_bounds__(256) void route_kernel(RouteArgs a) {
     if (a.sigmoid) return 1.0 / (1.0 + exp_f64(-static_cast<double>(v)));
     return v == m ? 1.0 : exp_f64(static_cast<double>(v) - static_cast<double>(m));
   };
-  // the choice needs no score without a bias, but a sum of two does
-  const bool scored = a.bias || (a.groups && a.sums);
-  double c[NV], inv = 1.0;
-  if (scored) {
-#pragma unroll
-    for (int j = 0; j < NV; ++j) c[j] = score_of(x[j]);
-  }
-  if (!a.sigmoid && (a.bias || !a.renorm)) {
-    double d = 0.0;
-#pragma unroll
-    for (int j = 0; j < NV; ++j) d += scored ? c[j] : score_of(x[j]);
-    d = lanes_sum<LPT>(d);
-    inv = d > 0.0 ? 1.0 / d : 1.0;  // 0: every expert masked
-  }
-  uint64_t key[NV];
-  double* const vals = reinterpret_cast<double*>(lds_key[wave]) + sub * a.E;
-#pragma unroll
-  for (int j = 0; j < NV; ++j) {
-    const int e = l + LPT * j;
-    double v = x[j];
-    if (a.bias) v = c[j] * inv + static_cast<double>(e < a.E ? a.bias[e] : 0.0f);
-    if (x[j] == kMasked || v != v) v = kNone;
-    if (a.groups && e < a.E) vals[e] = scored && !a.bias && v != kNone ? c[j] : v;
-    key[j] = e < a.E ? ordered(v + 0.0) : 0;  // one zero; 0: not there
-  }
-  if (a.groups) {
-    const int size = a.E / a.groups;
+  const bool scored = a.bias || (a.groups && a.sums);  // else the choice is the logit
+  const int size = a.groups ? a.E / a.groups : 1;
+  bool unsure = false;
+
+  // kept groups of this token, by the groups' values vals[0 .. E) in LDS: `near` says whether two
+  // ranks are too close to tell
+  auto keep_groups = [&](auto* vals, auto&& near) -> uint64_t {
+    using F = std::remove_reference_t<decltype(*vals)>;
+    const F none = -static_cast<F>(__builtin_huge_val());
+    F v1 = none, v2 = none;
     wave_sync();
-    double v1 = kNone, v2 = kNone;
     if (l < a.groups)
       for (int i = 0; i < size; ++i) {
-        const double v = vals[l * size + i];
+        const F v = vals[l * size + i];
         v2 = v > v1 ? v1 : v > v2 ? v : v2;
         v1 = v > v1 ? v : v1;
       }
-    const double r = a.sums && v2 != kNone ? v1 + v2 : v1;
+    const F r = a.sums && v2 != none ? v1 + v2 : v1;
     wave_sync();
     if (l < a.groups) vals[l] = r;
     wave_sync();
     int before = 0;
     for (int g = 0; g < a.groups; ++g) {
-      const double o = vals[g];
+      const F o = vals[g];
       before += o > r || (o == r && g < l);
+      unsure |= l < a.groups && g != l && near(o, r);
     }
-    const uint64_t kept = __ballot(l < a.groups && before < a.kept) >> (LPT == 64 ? 0 : sub * LPT);
+    wave_sync();
+    return __ballot(l < a.groups && before < a.kept) >> (LPT == 64 ? 0 : sub * LPT);
+  };
+
+  {  // FP32
+    constexpr float kLog2e = 1.44269504f;
+    uint32_t key[NV];
+    float s32[NV], inv = 1.0f;
+    if (scored) {
+      float d = 0.0f;
+#pragma unroll
+      for (int j = 0; j < NV; ++j) {
+        // (m - m is NaN where m is infinite)
+        if (a.sigmoid) s32[j] = __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-x[j] * kLog2e));
+        else s32[j] = x[j] == m ? 1.0f : __builtin_amdgcn_exp2f((x[j] - m) * kLog2e);
+        d += x[j] == kMasked ? 0.0f : s32[j];
+      }
+      if (!a.sigmoid && a.bias) {
+#pragma unroll
+        for (int k = LPT / 2; k; k >>= 1) d += __shfl_xor(d, k);
+        inv = 1.0f / d;  // masked all: not used
+      }
+    }
+    float* const vals = reinterpret_cast<float*>(lds_key[wave]) + sub * a.E;
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
       const int e = l + LPT * j;
-      if (e < a.E && !((kept >> (e / size)) & 1)) key[j] = 0;
+      float v = x[j];
+      if (a.bias) v = s32[j] * inv + (e < a.E ? a.bias[e] : 0.0f);
+      if (x[j] == kMasked || v != v) v = kMasked;
+      if (a.groups && e < a.E) vals[e] = scored && !a.bias && v != kMasked ? s32[j] : v;
+      key[j] = e < a.E ? (ordered(v + 0.0f) & ~15u) | (15 - j) : 0;  // one zero; 0: not there
+    }
+    if (a.groups) {
+      // scores and their sums are off by less than 2^-20, choices by 2^-22 of themselves more
+      const uint64_t kept = keep_groups(vals, [&](float o, float r) {
+        return scored && __builtin_fabsf(o - r) <= 0x1p-18f + 0x1p-20f * __builtin_fabsf(r);
+      });
+#pragma unroll
+      for (int j = 0; j < NV; ++j) {
+        const int e = l + LPT * j;
+        if (e < a.E && !((kept >> (e / size)) & 1)) key[j] = 0;
+      }
+    }
+#pragma unroll
+    for (int round = 0; round < NV; ++round)
+#pragma unroll
+      for (int j = round & 1; j + 1 < NV; j += 2) {
+        const uint32_t hi = key[j] > key[j + 1] ? key[j] : key[j + 1], lo = key[j] > key[j + 1] ? key[j + 1] : key[j];
+        key[j] = hi;
+        key[j + 1] = lo;
+      }
+    uint32_t* const list = reinterpret_cast<uint32_t*>(lds_key[wave]);
+#pragma unroll
+    for (int j = 1; j < NV; ++j) list[j * 64 + lane] = key[j];
+    uint32_t head = key[0], last = 0;
+    int next = 1;
+    // without a bias only logits that differ in the bits cut off can be mistaken
+    const bool cut = a.type == MOE_F32;
+    for (int k = 0; k <= a.topk; ++k) {
+      const uint32_t top = lanes_max<LPT>(head);
+      if (k > 0 && top != 0) {
+        const uint32_t p = last & ~15u, q = top & ~15u;
+        if (a.bias) {
+          const float fp = unordered(p), fq = unordered(q);
+          unsure |= fp - fq <= 0x1p-18f + 0x1p-17f * fmaxf(__builtin_fabsf(fp), __builtin_fabsf(fq));
+        } else {
+          unsure |= cut && p == q && p != (ordered(kMasked) & ~15u);
+        }
+      }
+      if (k == a.topk) break;
+      last = top;
+      const uint64_t all = __ballot(head == top) >> (LPT == 64 ? 0 : sub * LPT);
+      if (l == __builtin_ctzll(all)) {  // equal: the lowest lane, the slots being equal too
+        lds_out[wave][sub][k] = static_cast<uint16_t>(l + LPT * (15 - (head & 15)));
+        head = next < NV ? list[next * 64 + lane] : 0;
+        ++next;
+      }
     }
     wave_sync();
   }
-  uint32_t id[NV];
+
+  double inv = 1.0;
+  const bool again = __any(unsure);
+  if (!a.sigmoid && (!a.renorm || (again && a.bias))) {
+    double d = 0.0;
 #pragma unroll
-  for (int j = 0; j < NV; ++j) id[j] = l + LPT * j;
-#pragma unroll
-  for (int round = 0; round < NV; ++round)
-#pragma unroll
-    for (int j = round & 1; j + 1 < NV; j += 2) {
-      const bool swap = key[j] < key[j + 1];
-      const uint64_t k0 = key[j], k1 = key[j + 1];
-      const uint32_t i0 = id[j], i1 = id[j + 1];
-      key[j] = swap ? k1 : k0;
-      key[j + 1] = swap ? k0 : k1;
-      id[j] = swap ? i1 : i0;
-      id[j + 1] = swap ? i0 : i1;
-    }
-#pragma unroll
-  for (int j = 1; j < NV; ++j) {
-    lds_key[wave][j][lane] = key[j];
-    lds_id[wave][j][lane] = static_cast<uint16_t>(id[j]);
+    for (int j = 0; j < NV; ++j) d += score_of(x[j]);
+    d = lanes_sum<LPT>(d);
+    inv = d > 0.0 ? 1.0 / d : 1.0;  // 0: every expert masked
   }
-  uint64_t head = key[0];
-  uint32_t head_id = id[0];
-  int next = 1;
-  for (int k = 0; k < a.topk; ++k) {
-    const uint32_t hi = static_cast<uint32_t>(head >> 32), lo = static_cast<uint32_t>(head);
-    bool win = hi == lanes_max<LPT>(hi);
-    // (the maxima are taken by all lanes, outside any condition on `win`)
-    if (__popcll(__ballot(win)) != TPW) {
-      const uint32_t top = lanes_max<LPT>(win ? lo : 0u);
-      win &= lo == top;
-      if (__popcll(__ballot(win)) != TPW) {
-        const uint32_t first = lanes_max<LPT>(win ? ~head_id : 0u);
-        win &= ~head_id == first;
+  if (again) {  // FP64, exact order; equal choices by their index
+    const double kNone = -__builtin_huge_val();
+    uint64_t key[NV];
+    double* const vals = reinterpret_cast<double*>(lds_key[wave]) + sub * a.E;
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      const int e = l + LPT * j;
+      const double s = scored ? score_of(x[j]) : 0.0;
+      double v = x[j];
+      if (a.bias) v = s * inv + static_cast<double>(e < a.E ? a.bias[e] : 0.0f);
+      if (x[j] == kMasked || v != v) v = kNone;
+      if (a.groups && e < a.E) vals[e] = scored && !a.bias && v != kNone ? s : v;
+      key[j] = e < a.E ? ordered(v + 0.0) : 0;
+    }
+    if (a.groups) {
+      const uint64_t kept = keep_groups(vals, [](double, double) { return false; });
+#pragma unroll
+      for (int j = 0; j < NV; ++j) {
+        const int e = l + LPT * j;
+        if (e < a.E && !((kept >> (e / size)) & 1)) key[j] = 0;
       }
     }
-    if (win) {
-      lds_out[wave][sub][k] = static_cast<uint16_t>(head_id);
-      head = next < NV ? lds_key[wave][next][lane] : 0;
-      head_id = next < NV ? lds_id[wave][next][lane] : 0;
-      ++next;
+    uint32_t id[NV];
+#pragma unroll
+    for (int j = 0; j < NV; ++j) id[j] = l + LPT * j;
+#pragma unroll
+    for (int round = 0; round < NV; ++round)
+#pragma unroll
+      for (int j = round & 1; j + 1 < NV; j += 2) {
+        const bool swap = key[j] < key[j + 1];  // neighbours only: equal ones keep their order
+        const uint64_t k0 = key[j], k1 = key[j + 1];
+        const uint32_t i0 = id[j], i1 = id[j + 1];
+        key[j] = swap ? k1 : k0;
+        key[j + 1] = swap ? k0 : k1;
+        id[j] = swap ? i1 : i0;
+        id[j + 1] = swap ? i0 : i1;
+      }
+#pragma unroll
+    for (int j = 1; j < NV; ++j) {
+      lds_key[wave][j][lane] = key[j];
+      lds_id[wave][j][lane] = static_cast<uint16_t>(id[j]);
     }
+    uint64_t head = key[0];
+    uint32_t head_id = id[0];
+    int next = 1;
+    for (int k = 0; k < a.topk; ++k) {
+      const uint32_t hi = static_cast<uint32_t>(head >> 32), lo = static_cast<uint32_t>(head);
+      bool win = hi == lanes_max<LPT>(hi);
+      // (the maxima are taken by all lanes, outside any condition on `win`)
+      if (__popcll(__ballot(win)) != TPW) {
+        const uint32_t top = lanes_max<LPT>(win ? lo : 0u);
+        win &= lo == top;
+        if (__popcll(__ballot(win)) != TPW) {
+          const uint32_t first = lanes_max<LPT>(win ? ~head_id : 0u);
+          win &= ~head_id == first;
+        }
+      }
+      if (win) {
+        lds_out[wave][sub][k] = static_cast<uint16_t>(head_id);
+        head = next < NV ? lds_key[wave][next][lane] : 0;
+        head_id = next < NV ? lds_id[wave][next][lane] : 0;
+        ++next;
+      }
+    }
+    wave_sync();
   }
-  wave_sync();
   constexpr int KP = 64 / LPT;  // selected experts per lane
   double w[KP], total = 0.0;
 #pragma unroll
@@ -300,39 +394,42 @@ __global__ __launch_bounds__(256) void route_kernel(RouteArgs a) {
 }
 
 // --------------------------------------------------------------------- quant
-// code = x * 127 / amax, half to even, exactly.  Both are first scaled by the power of two
-// that brings amax into [1, 2), exactly but for values whose code is 0.  In BF16 and FP16, x * 127 and x * 127 - r * amax
-// are exact in FP32, and a quotient that is no half lies 2^-12 or more away from one, far
-// beyond the guess's error: only exact halves need the remainder.  FP32 goes through FP64.
+// code = x * 127 / amax, half to even, exactly.
+//
+// The quick way adds 1.5 * 2^23 to x * inv in one rounding, inv = 127 / amax rounded up by a step or
+// two: the sum's low byte is the code, unless the exact quotient is (16-bit types) or may be
+// (FP32) a half.
+//   BF16, FP16: a quotient q that is no half lies q 2^-18 or more from one (254 x - (2 k + 1) amax
+// is a whole number of x's last places), inv's error moves it by q 2^-22 at most.  A half, (2 k + 1)
+// amax = 254 x, needs 127 to divide amax's significand, or 2 k + 1 = 127, x = amax / 2, code 64:
+// inv being high, that one comes out right.
+//   FP32: within 2^-14 of a half, the exact way decides.
+// Rows with an amax that 127 divides (16-bit types), or below 2^-100, go the exact way: by the
+// remainder x * 127 - r * amax in FP64, x and amax first scaled by a power of two.
 struct QuantScale {
   int exp;
   float amax, inv;  // scaled; 127 / amax
 };
-template <int TYPE>
-__device__ __forceinline__ int quant_code(float x, const QuantScale& q) {
-  const float xs = __builtin_ldexpf(x, -q.exp);
-  if constexpr (TYPE == MOE_F32) {
-    const double n = static_cast<double>(xs) * 127.0, amax = static_cast<double>(q.amax);
-    const float r0 = __builtin_rintf(xs * q.inv);
-    const double d = 2.0 * __builtin_fma(-static_cast<double>(r0), amax, n);
-    const int r = static_cast<int>(r0);
-    const double far = __builtin_fabs(d);
-    return far > amax || (far == amax && (r & 1)) ? r + (d > 0.0 ? 1 : -1) : r;
-  } else {
-    const float r0 = __builtin_rintf(xs * q.inv);
-    const float d = __builtin_fmaf(-r0, q.amax, xs * 127.0f);
-    const int r = static_cast<int>(r0);
-    return 2.0f * __builtin_fabsf(d) == q.amax && (r & 1) ? r + (d > 0.0f ? 1 : -1) : r;
-  }
+__device__ __forceinline__ int quant_exact(float x, const QuantScale& q) {
+  const float xs = __builtin_ldexpf(x, -q.exp);  // exact but for values whose code is 0
+  const double n = static_cast<double>(xs) * 127.0, amax = static_cast<double>(q.amax);
+  const float r0 = __builtin_rintf(xs * q.inv);
+  const double d = 2.0 * __builtin_fma(-static_cast<double>(r0), amax, n), far = __builtin_fabs(d);
+  const int r = static_cast<int>(r0);
+  return far > amax || (far == amax && (r & 1)) ? r + (d > 0.0 ? 1 : -1) : r;
 }
 
 // W waves per token, which they hold in registers: NV 16-byte pieces a lane (NV 0: any length,
-// the row is read twice).  One pass over the data: bytes bound it.
+// the row is read twice).  One pass over the data: bytes bound it (8192 x 3584 BF16: 88 MB, 17 us
+// at a copy's rate), so an element may cost few instructions: four, with the quick way (15 made
+// it 23.5 us).
 template <int TYPE, int W, int NV>
 __global__ __launch_bounds__(256) void quant_kernel(const void* x, int64_t ldx, int32_t M, int32_t K,
                                                     int8_t* codes, int64_t ldc, float* scales) {
   using T = typename Elem<TYPE>::T;
+  typedef unsigned short u16x2 __attribute__((ext_vector_type(2)));
   constexpr int VE = 16 / sizeof(T), HELD = NV ? NV : 1;
+  constexpr float kMagic = 12582912.0f;
   __shared__ uint32_t part[4];
   const int lane = threadIdx.x % (64 * W), wave = threadIdx.x >> 6;
   const int64_t row = static_cast<int64_t>(blockIdx.x) * (4 / W) + threadIdx.x / (64 * W);
@@ -341,24 +438,39 @@ __global__ __launch_bounds__(256) void quant_kernel(const void* x, int64_t ldx, 
   int8_t* q = codes + row * ldc;
   const int pieces = (K + VE - 1) / VE;
   struct Piece {
-    T v[VE];
+    uint32_t w[4];
+    __device__ __forceinline__ float at(int e) const {
+      if constexpr (TYPE == MOE_F32) return __uint_as_float(w[e]);
+      else return to_f32<TYPE>(static_cast<uint16_t>(e & 1 ? w[e >> 1] >> 16 : w[e >> 1]));
+    }
   };
   auto load = [&](int i) {  // any alignment; zeros behind K
     Piece r;
     if ((i + 1) * VE <= K) {
       __builtin_memcpy(&r, p + i * VE, 16);
     } else {
+      T v[VE];
 #pragma unroll
-      for (int e = 0; e < VE; ++e) r.v[e] = i * VE + e < K ? p[i * VE + e] : T(0);
+      for (int e = 0; e < VE; ++e) v[e] = i * VE + e < K ? p[i * VE + e] : T(0);
+      __builtin_memcpy(&r, v, 16);
     }
     return r;
   };
-  uint32_t top = 0;  // magnitudes order as their bits, infinity and NaN above all
+  // magnitudes order as their bits, infinity and NaN above all
+  uint32_t top = 0;
+  u16x2 top2 = {0, 0};
   auto raise = [&](const Piece& r) {
 #pragma unroll
-    for (int e = 0; e < VE; ++e) {
-      const uint32_t b = __float_as_uint(to_f32<TYPE>(r.v[e])) & 0x7fffffffu;
-      top = b > top ? b : top;
+    for (int i = 0; i < 4; ++i) {
+      if constexpr (TYPE == MOE_F32) {
+        const uint32_t b = r.w[i] & 0x7fffffffu;
+        top = b > top ? b : top;
+      } else {
+        u16x2 b;
+        const uint32_t u = r.w[i] & 0x7fff7fffu;
+        __builtin_memcpy(&b, &u, 4);
+        top2 = __builtin_elementwise_max(top2, b);
+      }
     }
   };
   Piece held[HELD];
@@ -374,6 +486,7 @@ __global__ __launch_bounds__(256) void quant_kernel(const void* x, int64_t ldx, 
   } else {
     for (int i = lane; i < pieces; i += 64 * W) raise(load(i));
   }
+  if constexpr (TYPE != MOE_F32) top = top2[0] > top2[1] ? top2[0] : top2[1];
   top = lanes_max<64>(top);
   if constexpr (W > 1) {
     if ((threadIdx.x & 63) == 0) part[wave] = top;
@@ -381,24 +494,51 @@ __global__ __launch_bounds__(256) void quant_kernel(const void* x, int64_t ldx, 
 #pragma unroll
     for (int i = 0; i < 4; ++i) top = part[i] > top ? part[i] : top;
   }
-  const float amax = __uint_as_float(top);
-  const bool finite = top < 0x7f800000u, some = top != 0 && finite;
+  float amax;
+  if constexpr (TYPE == MOE_F32) amax = __uint_as_float(top);
+  else amax = to_f32<TYPE>(static_cast<uint16_t>(top));
+  const bool finite = (__float_as_uint(amax) & 0x7fffffffu) < 0x7f800000u, some = top != 0 && finite;
+  const uint32_t significand = (__float_as_uint(amax) & 0x7fffffu) | 0x800000u;
+  const bool quick = some && amax >= 0x1p-100f && (TYPE == MOE_F32 || significand % 127 != 0);
   QuantScale s = {0, 1.0f, 0.0f};
-  if (some) {
+  if (some && (!quick || TYPE == MOE_F32)) {
     s.exp = __builtin_amdgcn_frexp_expf(amax) - 1;
     s.amax = __builtin_ldexpf(amax, -s.exp);
     s.inv = 127.0f / s.amax;
   }
+  const float inv = quick ? __uint_as_float(__float_as_uint(127.0f / amax) + 1) : 0.0f;
   auto store = [&](int i, const Piece& r) {
-    int8_t c[VE];
+    uint32_t c[VE / 4] = {};
+    bool redo = some && !quick;
+    if (quick) {
 #pragma unroll
-    for (int e = 0; e < VE; ++e) c[e] = some ? static_cast<int8_t>(quant_code<TYPE>(to_f32<TYPE>(r.v[e]), s)) : 0;
+      for (int g = 0; g < VE / 4; ++g) {
+        uint32_t b[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float v = r.at(4 * g + e), y = __builtin_fmaf(v, inv, kMagic);
+          b[e] = __float_as_uint(y);
+          if constexpr (TYPE == MOE_F32)
+            redo |= __builtin_fabsf(__builtin_fmaf(v, inv, kMagic - y)) >= 0.5f - 0x1p-14f;
+        }
+        const uint32_t lo = __builtin_amdgcn_perm(b[1], b[0], 0x0c0c0400), hi = __builtin_amdgcn_perm(b[3], b[2], 0x0c0c0400);
+        c[g] = lo | hi << 16;
+      }
+    }
+    if (redo) {
+#pragma unroll
+      for (int g = 0; g < VE / 4; ++g) {
+        c[g] = 0;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) c[g] |= static_cast<uint32_t>(quant_exact(r.at(4 * g + e), s) & 255) << (8 * e);
+      }
+    }
     if ((i + 1) * VE <= K) {
       __builtin_memcpy(q + i * VE, c, VE);
     } else {
 #pragma unroll
       for (int e = 0; e < VE; ++e)
-        if (i * VE + e < K) q[i * VE + e] = c[e];
+        if (i * VE + e < K) q[i * VE + e] = static_cast<int8_t>(c[e / 4] >> (8 * (e & 3)));
     }
   };
   if constexpr (NV > 0) {
