@@ -68,7 +68,7 @@ constexpr size_t elem_size(int type) { return type == MOE_F32 ? 4 : 2; }
 struct RouteArgs {
   const void* logits;
   int64_t ldl;
-  int32_t B, E, topk, type, sigmoid, groups, kept, sums, renorm;
+  int32_t B, E, topk, sigmoid, groups, kept, sums, renorm;
   float scale;
   const float* bias;
   int32_t* ids;
@@ -145,30 +145,25 @@ __device__ __forceinline__ double exp_f64(double x) {
 }
 
 // LPT lanes per token, lane l of them holding experts l, l + LPT, ..., NV of them at most.  Each
-// lane sorts its choices into LDS; then the lanes' heads compete topk times, by rotations among
-// the lanes.
-//
-// First with the choice in FP32, cut to 28 bits, its lane's slot in the other four: sorting takes
-// a maximum and a minimum a pair, a head's contest four rotations.  Whatever lies closer
-// together than that arithmetic can tell apart (two neighbours of the result, or the first left
-// out, or two groups) is noticed, and the wave goes again with the choice in FP64, about three
-// times the work; for random logits that is less than one wave in a hundred.
-template <int LPT, int NV>
+// lane sorts its choices (stably, so that equal ones stay in index order) into LDS; then the
+// lanes' heads compete topk times: the largest upper word by rotations among the lanes, and
+// only where several lanes share it the lower word and the index.  Vector instructions bound it (some
+// 350 a token with groups), and the choice in FP64 is a small part of them: a contest in FP32
+// first, FP64 only for waves whose result it cannot tell, was no faster (16384 tokens with bias
+// and groups 23 us against 20.7) and much slower for few tokens, whose slowest wave counts.
+template <int TYPE, int LPT, int NV>
 __global__ __launch_bounds__(256) void route_kernel(RouteArgs a) {
   constexpr int TPW = 64 / LPT;
-  static_assert(NV <= 16, "four bits of slot");
   __shared__ uint64_t lds_key[4][NV][64];
   __shared__ uint16_t lds_id[4][NV][64];
   __shared__ uint16_t lds_out[4][TPW][64];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, l = lane % LPT, sub = lane / LPT;
   const int64_t tok = (static_cast<int64_t>(blockIdx.x) * 4 + wave) * TPW + sub, t = tok < a.B ? tok : a.B - 1;
   const float kMasked = -__builtin_huge_valf();
+  const double kNone = -__builtin_huge_val();
+  const typename Elem<TYPE>::T* const row = static_cast<const typename Elem<TYPE>::T*>(a.logits) + t * a.ldl;
   auto logit_at = [&](int e) {
-    const int64_t i = t * a.ldl + e;
-    float v;
-    if (a.type == MOE_F32) v = static_cast<const float*>(a.logits)[i];
-    else if (a.type == MOE_F16) v = f16_to_f32(static_cast<const uint16_t*>(a.logits)[i]);
-    else v = bf16_to_f32(static_cast<const uint16_t*>(a.logits)[i]);
+    const float v = to_f32<TYPE>(row[e]);
     return v == v ? v : kMasked;
   };
   float x[NV], m = kMasked;
@@ -187,188 +182,107 @@ __global__ __launch_bounds__(256) void route_kernel(RouteArgs a) {
   };
   const bool scored = a.bias || (a.groups && a.sums);  // else the choice is the logit
   const int size = a.groups ? a.E / a.groups : 1;
-  bool unsure = false;
+  const uint32_t per = (1u << 22) / static_cast<uint32_t>(size) + 1;  // e / size = e * per >> 22, as e * size < 2^22
 
-  // kept groups of this token, by the groups' values vals[0 .. E) in LDS: `near` says whether two
-  // ranks are too close to tell
-  auto keep_groups = [&](auto* vals, auto&& near) -> uint64_t {
-    using F = std::remove_reference_t<decltype(*vals)>;
-    const F none = -static_cast<F>(__builtin_huge_val());
-    F v1 = none, v2 = none;
+  // kept groups of this token, from the experts' values vals[0 .. E) in LDS
+  auto keep_groups = [&](double* vals) -> uint64_t {
+    double v1 = kNone, v2 = kNone;
     wave_sync();
     if (l < a.groups)
+#pragma unroll 8
       for (int i = 0; i < size; ++i) {
-        const F v = vals[l * size + i];
+        const double v = vals[l * size + i];
         v2 = v > v1 ? v1 : v > v2 ? v : v2;
         v1 = v > v1 ? v : v1;
       }
-    const F r = a.sums && v2 != none ? v1 + v2 : v1;
+    const double r = a.sums && v2 != kNone ? v1 + v2 : v1;
     wave_sync();
     if (l < a.groups) vals[l] = r;
     wave_sync();
     int before = 0;
+#pragma unroll 4
     for (int g = 0; g < a.groups; ++g) {
-      const F o = vals[g];
+      const double o = vals[g];
       before += o > r || (o == r && g < l);
-      unsure |= l < a.groups && g != l && near(o, r);
     }
     wave_sync();
     return __ballot(l < a.groups && before < a.kept) >> (LPT == 64 ? 0 : sub * LPT);
   };
 
-  {  // FP32
-    constexpr float kLog2e = 1.44269504f;
-    uint32_t key[NV];
-    float s32[NV], inv = 1.0f;
-    if (scored) {
-      float d = 0.0f;
+  double c[NV], inv = 1.0;  // scores
+  if (scored) {
 #pragma unroll
-      for (int j = 0; j < NV; ++j) {
-        // (m - m is NaN where m is infinite)
-        if (a.sigmoid) s32[j] = __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-x[j] * kLog2e));
-        else s32[j] = x[j] == m ? 1.0f : __builtin_amdgcn_exp2f((x[j] - m) * kLog2e);
-        d += x[j] == kMasked ? 0.0f : s32[j];
-      }
-      if (!a.sigmoid && a.bias) {
-#pragma unroll
-        for (int k = LPT / 2; k; k >>= 1) d += __shfl_xor(d, k);
-        inv = 1.0f / d;  // masked all: not used
-      }
-    }
-    float* const vals = reinterpret_cast<float*>(lds_key[wave]) + sub * a.E;
-#pragma unroll
-    for (int j = 0; j < NV; ++j) {
-      const int e = l + LPT * j;
-      float v = x[j];
-      if (a.bias) v = s32[j] * inv + (e < a.E ? a.bias[e] : 0.0f);
-      if (x[j] == kMasked || v != v) v = kMasked;
-      if (a.groups && e < a.E) vals[e] = scored && !a.bias && v != kMasked ? s32[j] : v;
-      key[j] = e < a.E ? (ordered(v + 0.0f) & ~15u) | (15 - j) : 0;  // one zero; 0: not there
-    }
-    if (a.groups) {
-      // scores and their sums are off by less than 2^-20, choices by 2^-22 of themselves more
-      const uint64_t kept = keep_groups(vals, [&](float o, float r) {
-        return scored && __builtin_fabsf(o - r) <= 0x1p-18f + 0x1p-20f * __builtin_fabsf(r);
-      });
-#pragma unroll
-      for (int j = 0; j < NV; ++j) {
-        const int e = l + LPT * j;
-        if (e < a.E && !((kept >> (e / size)) & 1)) key[j] = 0;
-      }
-    }
-#pragma unroll
-    for (int round = 0; round < NV; ++round)
-#pragma unroll
-      for (int j = round & 1; j + 1 < NV; j += 2) {
-        const uint32_t hi = key[j] > key[j + 1] ? key[j] : key[j + 1], lo = key[j] > key[j + 1] ? key[j + 1] : key[j];
-        key[j] = hi;
-        key[j + 1] = lo;
-      }
-    uint32_t* const list = reinterpret_cast<uint32_t*>(lds_key[wave]);
-#pragma unroll
-    for (int j = 1; j < NV; ++j) list[j * 64 + lane] = key[j];
-    uint32_t head = key[0], last = 0;
-    int next = 1;
-    // without a bias only logits that differ in the bits cut off can be mistaken
-    const bool cut = a.type == MOE_F32;
-    for (int k = 0; k <= a.topk; ++k) {
-      const uint32_t top = lanes_max<LPT>(head);
-      if (k > 0 && top != 0) {
-        const uint32_t p = last & ~15u, q = top & ~15u;
-        if (a.bias) {
-          const float fp = unordered(p), fq = unordered(q);
-          unsure |= fp - fq <= 0x1p-18f + 0x1p-17f * fmaxf(__builtin_fabsf(fp), __builtin_fabsf(fq));
-        } else {
-          unsure |= cut && p == q && p != (ordered(kMasked) & ~15u);
-        }
-      }
-      if (k == a.topk) break;
-      last = top;
-      const uint64_t all = __ballot(head == top) >> (LPT == 64 ? 0 : sub * LPT);
-      if (l == __builtin_ctzll(all)) {  // equal: the lowest lane, the slots being equal too
-        lds_out[wave][sub][k] = static_cast<uint16_t>(l + LPT * (15 - (head & 15)));
-        head = next < NV ? list[next * 64 + lane] : 0;
-        ++next;
-      }
-    }
-    wave_sync();
+    for (int j = 0; j < NV; ++j) c[j] = score_of(x[j]);
   }
-
-  double inv = 1.0;
-  const bool again = __any(unsure);
-  if (!a.sigmoid && (!a.renorm || (again && a.bias))) {
+  if (!a.sigmoid && (a.bias || !a.renorm)) {
     double d = 0.0;
 #pragma unroll
-    for (int j = 0; j < NV; ++j) d += score_of(x[j]);
+    for (int j = 0; j < NV; ++j) d += scored ? c[j] : score_of(x[j]);
     d = lanes_sum<LPT>(d);
     inv = d > 0.0 ? 1.0 / d : 1.0;  // 0: every expert masked
   }
-  if (again) {  // FP64, exact order; equal choices by their index
-    const double kNone = -__builtin_huge_val();
-    uint64_t key[NV];
-    double* const vals = reinterpret_cast<double*>(lds_key[wave]) + sub * a.E;
+  uint64_t key[NV];
+  double* const vals = reinterpret_cast<double*>(lds_key[wave]) + sub * a.E;
+#pragma unroll
+  for (int j = 0; j < NV; ++j) {
+    const int e = l + LPT * j;
+    double v = x[j];
+    if (a.bias) v = c[j] * inv + static_cast<double>(e < a.E ? a.bias[e] : 0.0f);
+    if (x[j] == kMasked || v != v) v = kNone;
+    if (a.groups && e < a.E) vals[e] = scored && !a.bias && v != kNone ? c[j] : v;
+    key[j] = e < a.E ? ordered(v + 0.0) : 0;  // one zero; 0: not there
+  }
+  if (a.groups) {
+    const uint64_t kept = keep_groups(vals);
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
       const int e = l + LPT * j;
-      const double s = scored ? score_of(x[j]) : 0.0;
-      double v = x[j];
-      if (a.bias) v = s * inv + static_cast<double>(e < a.E ? a.bias[e] : 0.0f);
-      if (x[j] == kMasked || v != v) v = kNone;
-      if (a.groups && e < a.E) vals[e] = scored && !a.bias && v != kNone ? s : v;
-      key[j] = e < a.E ? ordered(v + 0.0) : 0;
+      if (e < a.E && !((kept >> (static_cast<uint32_t>(e) * per >> 22)) & 1)) key[j] = 0;
     }
-    if (a.groups) {
-      const uint64_t kept = keep_groups(vals, [](double, double) { return false; });
-#pragma unroll
-      for (int j = 0; j < NV; ++j) {
-        const int e = l + LPT * j;
-        if (e < a.E && !((kept >> (e / size)) & 1)) key[j] = 0;
-      }
-    }
-    uint32_t id[NV];
-#pragma unroll
-    for (int j = 0; j < NV; ++j) id[j] = l + LPT * j;
-#pragma unroll
-    for (int round = 0; round < NV; ++round)
-#pragma unroll
-      for (int j = round & 1; j + 1 < NV; j += 2) {
-        const bool swap = key[j] < key[j + 1];  // neighbours only: equal ones keep their order
-        const uint64_t k0 = key[j], k1 = key[j + 1];
-        const uint32_t i0 = id[j], i1 = id[j + 1];
-        key[j] = swap ? k1 : k0;
-        key[j + 1] = swap ? k0 : k1;
-        id[j] = swap ? i1 : i0;
-        id[j + 1] = swap ? i0 : i1;
-      }
-#pragma unroll
-    for (int j = 1; j < NV; ++j) {
-      lds_key[wave][j][lane] = key[j];
-      lds_id[wave][j][lane] = static_cast<uint16_t>(id[j]);
-    }
-    uint64_t head = key[0];
-    uint32_t head_id = id[0];
-    int next = 1;
-    for (int k = 0; k < a.topk; ++k) {
-      const uint32_t hi = static_cast<uint32_t>(head >> 32), lo = static_cast<uint32_t>(head);
-      bool win = hi == lanes_max<LPT>(hi);
-      // (the maxima are taken by all lanes, outside any condition on `win`)
-      if (__popcll(__ballot(win)) != TPW) {
-        const uint32_t top = lanes_max<LPT>(win ? lo : 0u);
-        win &= lo == top;
-        if (__popcll(__ballot(win)) != TPW) {
-          const uint32_t first = lanes_max<LPT>(win ? ~head_id : 0u);
-          win &= ~head_id == first;
-        }
-      }
-      if (win) {
-        lds_out[wave][sub][k] = static_cast<uint16_t>(head_id);
-        head = next < NV ? lds_key[wave][next][lane] : 0;
-        head_id = next < NV ? lds_id[wave][next][lane] : 0;
-        ++next;
-      }
-    }
-    wave_sync();
   }
+  uint32_t id[NV];
+#pragma unroll
+  for (int j = 0; j < NV; ++j) id[j] = l + LPT * j;
+#pragma unroll
+  for (int round = 0; round < NV; ++round)
+#pragma unroll
+    for (int j = round & 1; j + 1 < NV; j += 2) {
+      const bool swap = key[j] < key[j + 1];  // neighbours only: equal ones keep their order
+      const uint64_t k0 = key[j], k1 = key[j + 1];
+      const uint32_t i0 = id[j], i1 = id[j + 1];
+      key[j] = swap ? k1 : k0;
+      key[j + 1] = swap ? k0 : k1;
+      id[j] = swap ? i1 : i0;
+      id[j + 1] = swap ? i0 : i1;
+    }
+#pragma unroll
+  for (int j = 1; j < NV; ++j) {
+    lds_key[wave][j][lane] = key[j];
+    lds_id[wave][j][lane] = static_cast<uint16_t>(id[j]);
+  }
+  uint64_t head = key[0];
+  uint32_t head_id = id[0];
+  int next = 1;
+  for (int k = 0; k < a.topk; ++k) {
+    const uint32_t hi = static_cast<uint32_t>(head >> 32), lo = static_cast<uint32_t>(head);
+    bool win = hi == lanes_max<LPT>(hi);
+    // (the maxima are taken by all lanes, outside any condition on `win`)
+    if (__popcll(__ballot(win)) != TPW) {
+      const uint32_t top = lanes_max<LPT>(win ? lo : 0u);
+      win &= lo == top;
+      if (__popcll(__ballot(win)) != TPW) {
+        const uint32_t first = lanes_max<LPT>(win ? ~head_id : 0u);
+        win &= ~head_id == first;
+      }
+    }
+    if (win) {
+      lds_out[wave][sub][k] = static_cast<uint16_t>(head_id);
+      head = next < NV ? lds_key[wave][next][lane] : 0;
+      head_id = next < NV ? lds_id[wave][next][lane] : 0;
+      ++next;
+    }
+  }
+  wave_sync();
   constexpr int KP = 64 / LPT;  // selected experts per lane
   double w[KP], total = 0.0;
 #pragma unroll
@@ -1229,11 +1143,23 @@ bool gate_ok(int32_t E, int32_t D, int32_t wtype) {
   return E >= 1 && E <= 1024 && D >= 512 && D <= 16384 && D % 512 == 0 && (wtype == MOE_BF16 || wtype == MOE_F32);
 }
 
-template <int LPT, int NV>
+template <int TYPE, int LPT, int NV>
 int launch_route(const RouteArgs& a, hipStream_t st) {
   constexpr int per = 4 * (64 / LPT);
-  hipLaunchKernelGGL((route_kernel<LPT, NV>), dim3(static_cast<unsigned>((a.B + per - 1) / per)), dim3(256), 0, st, a);
+  hipLaunchKernelGGL((route_kernel<TYPE, LPT, NV>), dim3(static_cast<unsigned>((a.B + per - 1) / per)), dim3(256), 0, st, a);
   return launch_status();
+}
+
+template <int TYPE>
+int launch_route(const RouteArgs& a, hipStream_t st) {
+  // 16 lanes a token do less work in all, 64 finish a token sooner (160 experts, top 16, bias: 4096
+  // tokens 9.5 against 9.2 us, 6000 11.2 against 11.4, 16384 16.4 against 23)
+  if (a.B > 4096 && a.E <= 256 && a.groups <= 16) {
+    if (a.E <= 64) return launch_route<TYPE, 16, 4>(a, st);
+    if (a.E <= 160) return launch_route<TYPE, 16, 10>(a, st);
+    return launch_route<TYPE, 16, 16>(a, st);
+  }
+  return a.E <= 256 ? launch_route<TYPE, 64, 4>(a, st) : launch_route<TYPE, 64, 16>(a, st);
 }
 
 template <int TYPE, int W, int NV>
@@ -1419,17 +1345,11 @@ int moe_route(const void* logits, int32_t type, int64_t ldl, int32_t B, int32_t 
                     : E % o.groups || o.topk_groups < 1 || o.topk_groups > o.groups ||
                           topk > o.topk_groups * (E / o.groups))
     return MOE_EINVAL;
-  const RouteArgs a = {logits,   ldl,           B,             E,        topk,
-                       type,     o.score,       o.groups,      o.topk_groups,
-                       o.group_score, o.renorm, o.scale == 0.0f ? 1.0f : o.scale, o.bias_dev, ids, weights};
+  const RouteArgs a = {logits,        ldl,      B,     E, topk, o.score, o.groups, o.topk_groups, o.group_score, o.renorm,
+                       o.scale == 0.0f ? 1.0f : o.scale, o.bias_dev, ids, weights};
   hipStream_t st = as_stream(stream);
-  // 16 lanes a token do less work in all, 64 finish a token sooner
-  if (B >= 2048 && E <= 256 && o.groups <= 16) {
-    if (E <= 64) return launch_route<16, 4>(a, st);
-    if (E <= 160) return launch_route<16, 10>(a, st);
-    return launch_route<16, 16>(a, st);
-  }
-  return E <= 256 ? launch_route<64, 4>(a, st) : launch_route<64, 16>(a, st);
+  if (type == MOE_F32) return launch_route<MOE_F32>(a, st);
+  return type == MOE_F16 ? launch_route<MOE_F16>(a, st) : launch_route<MOE_BF16>(a, st);
 }
 
 int moe_quant_i8(const void* x, int32_t type, int64_t ldx, int32_t M, int32_t K, int8_t* codes, int64_t ldc,

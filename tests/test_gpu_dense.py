@@ -120,6 +120,28 @@ def test_route_masked_infinite_and_tied(m, o):
     _check_route(m, x, 9, **o)
 
 
+def test_route_signed_zeros_are_equal(m):
+    x = torch.zeros(4200, 40)
+    x[:, ::3] = -0.0
+    _check_route(m, x[:5], 7)
+    _check_route(m, x, 7)                               # many tokens: another division of the lanes
+    _check_route(m, x[:5].to(BF), 7, bias=torch.zeros(40))
+
+
+@pytest.mark.parametrize("E,K,o", [(160, 16, dict(score="sigmoid", bias=True, groups=10, topk_groups=5,
+                                                  group_score="top2")), (64, 6, dict()), (200, 33, dict(renorm=False)),
+                                   (256, 8, dict(groups=16, topk_groups=3)), (17, 17, dict(bias=True))])
+def test_route_many_tokens(m, E, K, o):
+    log(f"route 5000x{E} {o}")
+    o, g = dict(o), _gen(E)
+    if o.pop("bias", False):
+        o["bias"] = torch.randn(E, generator=g) * 0.1
+    x = (torch.randn(5001, E, generator=g) * 2).to(F32 if E != 64 else F16)
+    x[::7, ::2] = -float("inf")
+    x[3] = float("nan")
+    _check_route(m, x, K, **o)
+
+
 def test_route_infinite_bias(m):
     b = torch.zeros(20)
     b[7], b[3] = float("inf"), float("inf")
