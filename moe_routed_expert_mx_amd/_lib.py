@@ -281,8 +281,8 @@ def moe_combine(rows, weights, out, stream=None):
 # These entry points check their tensors (the library sees pointers only): types, shapes,
 # unit stride within rows and one GPU for all of them raise ValueError.  They run on that
 # GPU's current stream, whichever GPU is current.  A call takes some microseconds of host
-# time, as long as the smallest kernels run, so the checks are few and plain, and options go
-# as packed bytes.
+# time, as long as the smallest kernels run, so the native binding (csrc/dense_binding.cpp)
+# goes first: it enqueues what is plainly right, and leaves the rest to the code here.
 _MOE_TYPE = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
 _BF16, _F32, _I32, _I8, _U8 = torch.bfloat16, torch.float32, torch.int32, torch.int8, torch.uint8
 _ROUTE_OPTS = struct.Struct("@5ifP2i")   # moe_route_opts_t
@@ -290,6 +290,18 @@ _LINEAR_OPTS = struct.Struct("@2iPPq")   # moe_linear_opts_t
 assert _ROUTE_OPTS.size == ctypes.sizeof(moe_route_opts_t) and _LINEAR_OPTS.size == ctypes.sizeof(moe_linear_opts_t)
 _current_device = torch._C._cuda_getDevice
 _current_stream = torch._C._cuda_getCurrentRawStream
+
+
+def _load_binding():
+    """The native binding, bound to the library; it is built with it."""
+    from . import _dense
+    addresses = [ctypes.cast(getattr(lib, f), ctypes.c_void_p).value
+                 for f in ("moe_gate", "moe_route", "moe_quant_i8", "moe_linear_i8")]
+    _dense.bind(*addresses, _current_stream, _current_device)
+    return _dense
+
+
+_dense = _load_binding()
 
 
 def _refuse(what: str):
@@ -353,7 +365,7 @@ def moe_gate_packed_bytes(E: int, D: int, wdtype=torch.bfloat16) -> int:
 
 def moe_gate_pack(w, packed, stream=None) -> moe_gate_t:
     """Lay a router weight (BF16 or FP32 [E, D], contiguous) out into `packed` (uint8, moe_gate_packed_bytes)
-    and return its handle for moe_gate.  The caller keeps `packed` alive."""
+    and return its handle for moe_gate, which keeps `packed` alive."""
     E, D = _matrix(w, "w")
     if w.dtype not in (_BF16, _F32) or not w.is_contiguous():
         _refuse("w: expected contiguous BF16 or FP32 [E, D]")
@@ -361,11 +373,15 @@ def moe_gate_pack(w, packed, stream=None) -> moe_gate_t:
         _refuse("packed: expected contiguous uint8")
     _enqueue("moe_gate_pack", lib.moe_gate_pack, stream, (w, packed), w.data_ptr(), _MOE_TYPE[w.dtype], E, D,
              packed.data_ptr(), packed.numel())
-    return moe_gate_t(E, D, _MOE_TYPE[w.dtype], packed.data_ptr())
+    gate = moe_gate_t(E, D, _MOE_TYPE[w.dtype], packed.data_ptr())
+    gate.tensor = packed
+    return gate
 
 
 def moe_gate(gate: moe_gate_t, x, logits, stream=None):
     """Router product: x BF16 [B, D] (rows may be strided) -> logits FP32 [B, E]."""
+    if stream is None and _dense.gate(ctypes.addressof(gate), gate.D, gate.E, x, logits) == 0:
+        return
     B = _matrix(x, "x")[0]
     if x.dtype != _BF16 or logits.dtype != _F32:
         _refuse("x: expected BF16, logits: FP32")
@@ -383,9 +399,12 @@ def moe_route(logits, ids, weights, *, score: str = "softmax", bias=None, groups
     the largest choice (score + bias) first, as the expert calls and moe_combine take them.  score "softmax" or
     "sigmoid"; groups experts groups of which topk_groups stay, ranked by group_score "max" or "top2"; renorm
     divides a token's weights by their sum; scale multiplies them."""
+    sc, gs = _SCORES.get(score), _GROUP_SCORES.get(group_score)
+    if stream is None and _dense.route(logits, ids, weights, sc, bias, groups, topk_groups, gs, renorm, scale) == 0:
+        return
     shape = _matrix(logits, "logits")
     B, E = shape
-    kind, sc, gs = _MOE_TYPE.get(logits.dtype), _SCORES.get(score), _GROUP_SCORES.get(group_score)
+    kind = _MOE_TYPE.get(logits.dtype)
     if kind is None or sc is None or gs is None:
         _refuse(f"logits of {logits.dtype}, score {score!r} or group_score {group_score!r} not taken")
     ldl = _rows(logits, "logits", shape)
@@ -407,6 +426,8 @@ def moe_route(logits, ids, weights, *, score: str = "softmax", bias=None, groups
 def moe_quant_i8(x, codes, scales, stream=None):
     """Int8 quantization with one scale for each token: x [M, K] (FP32, BF16 or FP16) -> codes int8 [M, K], scales
     FP32 [M]; code * scale stands for x."""
+    if stream is None and _dense.quant(x, codes, scales) == 0:
+        return
     shape = _matrix(x, "x")
     kind = _MOE_TYPE.get(x.dtype)
     if kind is None or codes.dtype != _I8:
@@ -424,7 +445,10 @@ def moe_linear_i8(a, a_scales, w, w_scales, out, *, act: str = "none", bias=None
     """Int8 product with scales for each token and channel: a int8 [M, K], w int8 [N, K] -> out [M, N] (FP32, BF16 or
     FP16), y = (a . w) * a_scales * w_scales + bias (FP32 [N]); act "swiglu": the first N/2 rows of w are the gate,
     the others up, and out is [M, N/2]; add (as out, may be out itself) is added last."""
-    shape, mode, kind = _matrix(a, "a"), _ACTS.get(act), _MOE_TYPE.get(out.dtype)
+    mode = _ACTS.get(act)
+    if stream is None and _dense.linear(a, a_scales, w, w_scales, out, mode, bias, add) == 0:
+        return
+    shape, kind = _matrix(a, "a"), _MOE_TYPE.get(out.dtype)
     M, K = shape
     N = _matrix(w, "w")[0]
     if mode is None or kind is None or a.dtype != _I8 or w.dtype != _I8:

@@ -1,8 +1,9 @@
-"""Build the HIP library in-tree for gfx950 (hipcc; no JIT cache)."""
+"""Build the HIP library for gfx950 (hipcc) and the native binding of its dense side (g++), in-tree; no JIT cache."""
 from __future__ import annotations
 
 import os
 import subprocess
+import sysconfig
 import tempfile
 from concurrent.futures import ThreadPoolExecutor
 
@@ -10,6 +11,8 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 SOURCES = [os.path.join(HERE, "csrc", name) for name in ("moe_mx.hip", "moe_dense.hip")]
 LIB = os.path.join(HERE, "libmoe_mx.so")
+BINDING_SOURCE = os.path.join(HERE, "csrc", "dense_binding.cpp")
+BINDING = os.path.join(HERE, "_dense.so")
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 FLAGS = [
     "--offload-arch=gfx950", "-O3", "-std=c++17", "-fPIC",
@@ -29,7 +32,7 @@ def _run(cmd, verbose: bool) -> None:
         print(msgs)
 
 
-def build(verbose: bool = False) -> str:
+def build_library(verbose: bool = False) -> str:
     tmp = LIB + ".tmp"
     with tempfile.TemporaryDirectory() as d:
         objs = [os.path.join(d, os.path.basename(src) + ".o") for src in SOURCES]
@@ -39,6 +42,28 @@ def build(verbose: bool = False) -> str:
         _run([HIPCC, "--offload-arch=gfx950", "-shared", *objs, "-o", tmp], verbose)
     os.replace(tmp, LIB)
     return LIB
+
+
+def build_binding(verbose: bool = False) -> str:
+    """Host code only: it reads tensors through torch's headers and calls the library by address."""
+    import torch
+    from torch.utils.cpp_extension import include_paths
+    tmp, libs = BINDING + ".tmp", os.path.join(os.path.dirname(torch.__file__), "lib")
+    includes = [*include_paths(), sysconfig.get_paths()["include"], os.path.join(ROOT, "include")]
+    _run([os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall",
+          f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", *(f"-isystem{i}" for i in includes),
+          BINDING_SOURCE, "-o", tmp, f"-L{libs}", f"-Wl,-rpath,{libs}", "-ltorch_python", "-ltorch", "-ltorch_cpu",
+          "-lc10"], verbose)
+    os.replace(tmp, BINDING)
+    return BINDING
+
+
+def build(verbose: bool = False) -> str:
+    with ThreadPoolExecutor(2) as pool:
+        binding = pool.submit(build_binding, verbose)
+        lib = build_library(verbose)
+        binding.result()
+    return lib
 
 
 if __name__ == "__main__":

@@ -104,8 +104,26 @@ __device__ __forceinline__ uint32_t lanes_max(uint32_t v) {
 }
 template <int LPT>
 __device__ __forceinline__ double lanes_sum(double v) {
+  auto add = [&](auto turn) {
+    const uint64_t u = static_cast<uint64_t>(__double_as_longlong(v));
+    const uint64_t o = static_cast<uint64_t>(turn(static_cast<uint32_t>(u >> 32))) << 32 | turn(static_cast<uint32_t>(u));
+    v += __longlong_as_double(static_cast<int64_t>(o));
+  };
+  add([](uint32_t w) { return rotate_row<8>(w); });
+  add([](uint32_t w) { return rotate_row<4>(w); });
+  add([](uint32_t w) { return rotate_row<2>(w); });
+  add([](uint32_t w) { return rotate_row<1>(w); });
+  if constexpr (LPT == 64) {
+    double r = 0.0;
 #pragma unroll
-  for (int d = LPT / 2; d; d >>= 1) v += __shfl_xor(v, d);
+    for (int i = 0; i < 64; i += 16) {
+      const uint64_t u = static_cast<uint64_t>(__double_as_longlong(v));
+      const uint32_t hi = static_cast<uint32_t>(__builtin_amdgcn_readlane(static_cast<int>(u >> 32), i));
+      const uint32_t lo = static_cast<uint32_t>(__builtin_amdgcn_readlane(static_cast<int>(u), i));
+      r += __longlong_as_double(static_cast<int64_t>(static_cast<uint64_t>(hi) << 32 | lo));
+    }
+    return r;
+  }
   return v;
 }
 // Bits of a number as an unsigned word that orders as the number does.
@@ -166,14 +184,21 @@ __global__ __launch_bounds__(256) void route_kernel(RouteArgs a) {
     const float v = to_f32<TYPE>(row[e]);
     return v == v ? v : kMasked;
   };
-  float x[NV], m = kMasked;
+  // the selected experts' logits: few tokens wait less for LDS, many take less of it
+  constexpr bool kKeep = LPT == 64;
+  __shared__ float lds_logit[kKeep ? 4 : 1][kKeep ? NV : 1][64];
+  float x[NV], bias[NV], m = kMasked;
 #pragma unroll
   for (int j = 0; j < NV; ++j) {
     const int e = l + LPT * j;
     x[j] = e < a.E ? logit_at(e) : kMasked;
+    bias[j] = a.bias && e < a.E ? a.bias[e] : 0.0f;
   }
 #pragma unroll
-  for (int j = 0; j < NV; ++j) m = fmaxf(m, x[j]);
+  for (int j = 0; j < NV; ++j) {
+    if constexpr (kKeep) lds_logit[wave][j][lane] = x[j];
+    m = fmaxf(m, x[j]);
+  }
   m = unordered(lanes_max<LPT>(ordered(m)));
   auto score_of = [&](float v) -> double {  // softmax: without the common denominator
     if (v == kMasked) return 0.0;
@@ -227,7 +252,7 @@ __global__ __launch_bounds__(256) void route_kernel(RouteArgs a) {
   for (int j = 0; j < NV; ++j) {
     const int e = l + LPT * j;
     double v = x[j];
-    if (a.bias) v = c[j] * inv + static_cast<double>(e < a.E ? a.bias[e] : 0.0f);
+    if (a.bias) v = c[j] * inv + static_cast<double>(bias[j]);
     if (x[j] == kMasked || v != v) v = kNone;
     if (a.groups && e < a.E) vals[e] = scored && !a.bias && v != kNone ? c[j] : v;
     key[j] = e < a.E ? ordered(v + 0.0) : 0;  // one zero; 0: not there
@@ -255,10 +280,13 @@ __global__ __launch_bounds__(256) void route_kernel(RouteArgs a) {
       id[j] = swap ? i1 : i0;
       id[j + 1] = swap ? i0 : i1;
     }
+  constexpr bool kShort = NV <= 4;  // stays in registers
+  if constexpr (!kShort) {
 #pragma unroll
-  for (int j = 1; j < NV; ++j) {
-    lds_key[wave][j][lane] = key[j];
-    lds_id[wave][j][lane] = static_cast<uint16_t>(id[j]);
+    for (int j = 1; j < NV; ++j) {
+      lds_key[wave][j][lane] = key[j];
+      lds_id[wave][j][lane] = static_cast<uint16_t>(id[j]);
+    }
   }
   uint64_t head = key[0];
   uint32_t head_id = id[0];
@@ -277,9 +305,19 @@ __global__ __launch_bounds__(256) void route_kernel(RouteArgs a) {
     }
     if (win) {
       lds_out[wave][sub][k] = static_cast<uint16_t>(head_id);
-      head = next < NV ? lds_key[wave][next][lane] : 0;
-      head_id = next < NV ? lds_id[wave][next][lane] : 0;
-      ++next;
+      if constexpr (kShort) {
+        head = key[1];
+        head_id = id[1];
+#pragma unroll
+        for (int j = 1; j < NV; ++j) {
+          key[j] = j + 1 < NV ? key[j + 1] : 0;
+          id[j] = j + 1 < NV ? id[j + 1] : 0;
+        }
+      } else {
+        head = next < NV ? lds_key[wave][next][lane] : 0;
+        head_id = next < NV ? lds_id[wave][next][lane] : 0;
+        ++next;
+      }
     }
   }
   wave_sync();
@@ -291,7 +329,8 @@ __global__ __launch_bounds__(256) void route_kernel(RouteArgs a) {
     w[i] = 0.0;
     if (k < a.topk) {
       const int e = lds_out[wave][sub][k];
-      w[i] = score_of(logit_at(e));
+      if constexpr (kKeep) w[i] = score_of(lds_logit[wave][e / LPT][e % LPT]);
+      else w[i] = score_of(logit_at(e));
       if (tok < a.B) a.ids[t * a.topk + k] = e;
     }
     total += w[i];

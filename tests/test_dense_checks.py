@@ -135,3 +135,18 @@ def test_binding_checks_tensors():
         with pytest.raises(ValueError) as e:
             call()
         assert "must be on a GPU" not in str(e.value), i
+
+
+def test_native_binding_declines():
+    """The native binding enqueues nothing it is not sure of: tensors that are not on a GPU, of another type or
+    shape, no tensors at all, the wrong number of arguments; the caller's own checks follow."""
+    d, no = m._lib._dense, -100
+    x, q, s = _z(4, 512, dtype=BF), _z(4, 512, dtype=torch.int8), _z(4)
+    assert d.quant(x, q, s) == no
+    assert d.quant(x, q, None) == no and d.quant(1, 2, 3) == no and d.quant(x, q) == no
+    assert d.route(_z(4, 16), _z(4, 2, dtype=torch.int32), _z(4, 2), None, None, 0, 0, 0, True, 1.0) == no
+    assert d.route(_z(4, 16), _z(4, 2, dtype=torch.int32), _z(4, 2), 0, None, 0, 0, 0, True, "1") == no
+    assert d.linear(q, s, q, s, _z(4, 4), 0, None, None) == no
+    assert d.gate(0x1000, 512, 16, x, _z(4, 16)) == no
+    meta = torch.empty(4, 512, dtype=BF, device="meta")
+    assert d.quant(meta, q, s) == no

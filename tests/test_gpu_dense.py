@@ -484,6 +484,44 @@ def test_two_streams_at_once(m):
         assert torch.equal(s[4], want)
 
 
+def test_native_binding_and_ctypes_agree(m):
+    """A call without a stream goes through the native binding, one with a stream through ctypes: the same
+    results, and the native binding does take what is right."""
+    g, d, st = _gen(41), m._lib._dense, torch.cuda.current_stream()
+    x = torch.randn(6, 512, generator=g).to(BF).to(DEV)
+    w = torch.randn(40, 512, generator=g).to(DEV)
+    h = m.moe_gate_pack(w, torch.empty(m.moe_gate_packed_bytes(40, 512, F32), dtype=torch.uint8, device=DEV))
+    bias = torch.randn(40, generator=g).to(DEV)
+    wq, ws = _codes((64, 512), g).to(DEV), torch.rand(64, generator=g).to(DEV)
+    b, add = torch.randn(64, generator=g).to(DEV), torch.randn(6, 32, generator=g).to(BF).to(DEV)
+    res = []
+    for s in (None, st):
+        lg, ids, wt = torch.empty(6, 40, device=DEV), torch.empty(6, 5, dtype=torch.int32, device=DEV), \
+            torch.empty(6, 5, device=DEV)
+        q, sc, y = torch.empty(6, 512, dtype=torch.int8, device=DEV), torch.empty(6, device=DEV), \
+            torch.empty(6, 32, dtype=BF, device=DEV)
+        m.moe_gate(h, x, lg, stream=s)
+        m.moe_route(lg, ids, wt, score="sigmoid", bias=bias, groups=5, topk_groups=3, group_score="top2", scale=3,
+                    stream=s)
+        m.moe_quant_i8(x, q, sc, stream=s)
+        m.moe_linear_i8(q, sc, wq, ws, y, act="swiglu", bias=b, add=add, stream=s)
+        torch.cuda.synchronize()
+        res.append((lg, ids, wt, q, sc, y))
+    assert all(torch.equal(p, r) for p, r in zip(*res))
+    lg, ids, wt, q, sc, y = res[0]
+    import ctypes
+    assert d.gate(ctypes.addressof(h), 512, 40, x, lg) == 0
+    assert d.route(lg, ids, wt, 1, bias, 5, 3, 1, True, 3.0) == 0
+    assert d.quant(x, q, sc) == 0
+    assert d.linear(q, sc, wq, ws, y, 1, b, add) == 0
+    assert d.linear(q, sc, wq, ws, y, 0, b, add) == -100        # out has half the columns
+    assert d.quant(x, q.cpu(), sc) == -100
+    with pytest.raises(ValueError, match="one GPU"):
+        m.moe_quant_i8(x, q.cpu(), sc)
+    with pytest.raises(m.MoeError):
+        m.moe_route(lg, ids, wt, groups=7, topk_groups=1)       # 40 experts, 7 groups
+
+
 @pytest.mark.parametrize("B", [1, 8, 40])
 def test_block_end_to_end(m, B):
     """The layer as it is used: router, routed experts, combine, shared expert.  Each stage is
