@@ -1298,16 +1298,18 @@ int launch_dma(const LinearArgs& a, hipStream_t st) {
 
 template <int OUT, bool SWIGLU, bool ALIGNED>
 int launch_linear(const LinearArgs& a, hipStream_t st) {
-  // two row tiles halve the reads of a, where there are workgroups enough without
+  // The streaming kernel's workgroups of 16 columns, 64 tokens a block.  Beyond a round of 256, two
+  // row tiles halve them and the reads of a.  With more than 64 tokens it is taken while it stays
+  // in one round, when tiles would leave most CUs idle (us, it and tiles: 256 x 768 x 3584 7.1 and
+  // 12.5, 512 x 768 x 3584 8.2 and 12.7, 128 x 4096 x 4096 9.3 and 13.9); where tiles cannot use LDS
+  // DMA, two rounds (512 x 768 x 3583 14.9 and 37.7).
   constexpr int R1 = SWIGLU ? 2 : 1;
-  const bool wide = a.N >= 8192;
-  // beyond 64 tokens in blocks of 64, as long as there are few: then tiles leave most CUs idle
-  // (256 x 768 x 3584: 10.6 us against 12.8; 512 x 768: 20.1 against 13.0)
   const int64_t blocks = static_cast<int64_t>((a.M + 63) / 64) * (((SWIGLU ? a.N / 2 : a.N) + 15) / 16);
+  const bool wide = !SWIGLU && blocks > 256;
   if (a.M <= 16) return launch_stream<OUT, SWIGLU, ALIGNED, R1, 1, 16>(a, st);
   if (a.M <= 32)
     return wide ? launch_stream<OUT, SWIGLU, ALIGNED, 2, 2, 8>(a, st) : launch_stream<OUT, SWIGLU, ALIGNED, R1, 2, 8>(a, st);
-  if (a.M <= 64 || blocks <= 256)
+  if (a.M <= 64 || blocks <= (SWIGLU ? 256 : ALIGNED ? 512 : 1024))
     return wide ? launch_stream<OUT, SWIGLU, ALIGNED, 2, 4, 8>(a, st) : launch_stream<OUT, SWIGLU, ALIGNED, R1, 4, 8>(a, st);
   if constexpr (ALIGNED) {
     // Rounds of tiles over 256 CUs, weighed with a round's time at K = 4096 (us, less what every

@@ -362,6 +362,30 @@ def test_linear_sizes(m, M, N, K, act):
                   bias=i % 2 == 0, add=i % 4 < 2)
 
 
+# sizes that take each of the tiles (64 x 128, 128 x 128, 128 x 256, 256 x 256) and the kernel for unaligned rows
+TILES = [(300, 2050, 272), (1000, 3000, 144), (2000, 4000, 80), (4090, 4090, 80), (520, 2050, 273), (700, 2500, 130)]
+
+
+@pytest.mark.parametrize("M,N,K", TILES)
+@pytest.mark.parametrize("act", ["none", "swiglu"])
+def test_linear_tiles(m, M, N, K, act):
+    _check_linear(m, M, N, K, act=act, out=BF, bias=True, add=True, seed=1)
+    pad = 16 if K % 16 == 0 else 1
+    _check_linear(m, M, N, K, act=act, out=F32 if M < 2000 else F16, lda=pad, ldw=2 * pad, ldo=3, offset=pad, seed=2)
+
+
+@pytest.mark.parametrize("M,N", [(300, 2050), (1000, 3000)])
+def test_linear_tiles_longest_rows(m, M, N):
+    K = 131056
+    a = torch.full((M, K), -128, dtype=torch.int8, device=DEV)
+    w = torch.full((N, K), -128, dtype=torch.int8, device=DEV)
+    w[N - 1] = 127
+    out = torch.empty(M, N, device=DEV)
+    m.moe_linear_i8(a, torch.ones(M, device=DEV), w, torch.ones(N, device=DEV), out)
+    assert (out[:, :N - 1] == float(16384 * K)).all()
+    assert (out[:, N - 1] == float(np.float32(-128 * 127 * K))).all()
+
+
 @pytest.mark.parametrize("out", [BF, F16, F32])
 @pytest.mark.parametrize("M", [1, 5, 24, 40, 70, 300])
 def test_linear_epilogues(m, out, M):
@@ -406,9 +430,10 @@ def test_linear_non_finite_scales(m):
     assert torch.equal(bad, want)
 
 
-def test_linear_rows_past_32_bit_offsets(m):
+@pytest.mark.parametrize("N,K", [(32, 64), (2050, 64), (2050, 65)])
+def test_linear_rows_past_32_bit_offsets(m, N, K):
     """A row distance that puts the last rows of a and out beyond 2^32 bytes."""
-    M, K, N, ld = 1100, 64, 32, (1 << 22) - 16
+    M, ld = 1100, (1 << 22) - 16
     store = torch.zeros((M - 1) * ld + K, dtype=torch.int8, device=DEV)
     a = torch.as_strided(store, (M, K), (ld, 1))
     g = _gen(2)
