@@ -371,7 +371,7 @@ typedef struct {
 } moe_gate_t;
 
 /* Router product: logits[t, e] = sum over d of x[t, d] * w[e, d], FP32 sums of exact
- * products, in a fixed order (an FP32 weight counts as the sum of its upper, middle and lower
+ * products, in an order that the sizes alone decide (an FP32 weight counts as the sum of its upper, middle and lower
  * eight significant bits; below 2^-100 in magnitude it loses those under 2^-133).  x_dev BF16 [B, D], ldx >= D and a multiple of 8, x_dev
  * 16-byte aligned; logits_dev FP32 [B, E], ldl >= E.   The logits of a token
  * with an infinite or NaN feature are not finite (with an FP32 weight: NaN).

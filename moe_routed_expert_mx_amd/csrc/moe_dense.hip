@@ -172,13 +172,14 @@ __device__ __forceinline__ double exp_f64(double x) {
 template <int TYPE, int LPT, int NV>
 __global__ __launch_bounds__(256) void route_kernel(RouteArgs a) {
   constexpr int TPW = 64 / LPT;
-  __shared__ uint64_t lds_key[4][NV][64];
-  __shared__ uint16_t lds_id[4][NV][64];
+  __shared__ uint64_t lds_key[4][NV + 1][64];  // behind a lane's last choice, one that never wins
+  __shared__ uint16_t lds_id[4][NV + 1][64];
   __shared__ uint16_t lds_out[4][TPW][64];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, l = lane % LPT, sub = lane / LPT;
   const int64_t tok = (static_cast<int64_t>(blockIdx.x) * 4 + wave) * TPW + sub, t = tok < a.B ? tok : a.B - 1;
   const float kMasked = -__builtin_huge_valf();
-  const double kNone = -__builtin_huge_val();
+  // a masked expert's choice: below every other, FP32 or the sum of two; -inf: not there at all
+  const double kNone = -1e300;
   const typename Elem<TYPE>::T* const row = static_cast<const typename Elem<TYPE>::T*>(a.logits) + t * a.ldl;
   auto logit_at = [&](int e) {
     const float v = to_f32<TYPE>(row[e]);
@@ -246,23 +247,23 @@ __global__ __launch_bounds__(256) void route_kernel(RouteArgs a) {
     d = lanes_sum<LPT>(d);
     inv = d > 0.0 ? 1.0 / d : 1.0;  // 0: every expert masked
   }
-  uint64_t key[NV];
+  double choice[NV];
   double* const vals = reinterpret_cast<double*>(lds_key[wave]) + sub * a.E;
 #pragma unroll
   for (int j = 0; j < NV; ++j) {
     const int e = l + LPT * j;
     double v = x[j];
     if (a.bias) v = c[j] * inv + static_cast<double>(bias[j]);
-    if (x[j] == kMasked || v != v) v = kNone;
+    if (x[j] == kMasked || !(v > kNone)) v = kNone;
     if (a.groups && e < a.E) vals[e] = scored && !a.bias && v != kNone ? c[j] : v;
-    key[j] = e < a.E ? ordered(v + 0.0) : 0;  // one zero; 0: not there
+    choice[j] = e < a.E ? v : -__builtin_huge_val();
   }
   if (a.groups) {
     const uint64_t kept = keep_groups(vals);
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
       const int e = l + LPT * j;
-      if (e < a.E && !((kept >> (static_cast<uint32_t>(e) * per >> 22)) & 1)) key[j] = 0;
+      if (e < a.E && !((kept >> (static_cast<uint32_t>(e) * per >> 22)) & 1)) choice[j] = -__builtin_huge_val();
     }
   }
   uint32_t id[NV];
@@ -272,14 +273,17 @@ __global__ __launch_bounds__(256) void route_kernel(RouteArgs a) {
   for (int round = 0; round < NV; ++round)
 #pragma unroll
     for (int j = round & 1; j + 1 < NV; j += 2) {
-      const bool swap = key[j] < key[j + 1];  // neighbours only: equal ones keep their order
-      const uint64_t k0 = key[j], k1 = key[j + 1];
+      const bool swap = choice[j] < choice[j + 1];  // neighbours only: equal ones keep their order
+      const double c0 = choice[j], c1 = choice[j + 1];
       const uint32_t i0 = id[j], i1 = id[j + 1];
-      key[j] = swap ? k1 : k0;
-      key[j + 1] = swap ? k0 : k1;
+      choice[j] = swap ? c1 : c0;
+      choice[j + 1] = swap ? c0 : c1;
       id[j] = swap ? i1 : i0;
       id[j + 1] = swap ? i0 : i1;
     }
+  uint64_t key[NV];
+#pragma unroll
+  for (int j = 0; j < NV; ++j) key[j] = ordered(choice[j] + 0.0);  // one zero
   constexpr bool kShort = NV <= 4;  // stays in registers
   if constexpr (!kShort) {
 #pragma unroll
@@ -287,6 +291,8 @@ __global__ __launch_bounds__(256) void route_kernel(RouteArgs a) {
       lds_key[wave][j][lane] = key[j];
       lds_id[wave][j][lane] = static_cast<uint16_t>(id[j]);
     }
+    lds_key[wave][NV][lane] = 0;
+    lds_id[wave][NV][lane] = 0;
   }
   uint64_t head = key[0];
   uint32_t head_id = id[0];
@@ -314,8 +320,8 @@ __global__ __launch_bounds__(256) void route_kernel(RouteArgs a) {
           id[j] = j + 1 < NV ? id[j + 1] : 0;
         }
       } else {
-        head = next < NV ? lds_key[wave][next][lane] : 0;
-        head_id = next < NV ? lds_id[wave][next][lane] : 0;
+        head = lds_key[wave][next][lane];
+        head_id = lds_id[wave][next][lane];
         ++next;
       }
     }

@@ -509,6 +509,30 @@ def test_two_streams_at_once(m):
         assert torch.equal(s[4], want)
 
 
+def test_host_threads(m):
+    """Threads that call at once, each on a stream of its own."""
+    import threading
+    g = _gen(25)
+    a, w = _codes((300, 512), g).to(DEV), _codes((2050, 512), g).to(DEV)
+    sa, sw = torch.rand(300, generator=g).to(DEV), torch.rand(2050, generator=g).to(DEV)
+    want = torch.empty(300, 2050, device=DEV)
+    m.moe_linear_i8(a, sa, w, sw, want)
+    outs = [torch.zeros_like(want) for _ in range(4)]
+    torch.cuda.synchronize()
+
+    def work(out):
+        s = torch.cuda.Stream()
+        with torch.cuda.stream(s):
+            for _ in range(20):
+                m.moe_linear_i8(a, sa, w, sw, out)
+        s.synchronize()
+
+    threads = [threading.Thread(target=work, args=(o,)) for o in outs]
+    [t.start() for t in threads]
+    [t.join() for t in threads]
+    assert all(torch.equal(want, o) for o in outs)
+
+
 def test_native_binding_and_ctypes_agree(m):
     """A call without a stream goes through the native binding, one with a stream through ctypes: the same
     results, and the native binding does take what is right."""
