@@ -710,14 +710,15 @@ __device__ __forceinline__ Words words16(const int8_t* p, bool whole, const int8
   }
   return r;
 }
-// The 16 bytes, `skip` bytes into their words; only the first n of them if n < 16.
-__device__ __forceinline__ v4i bytes16(const Words& r, uint32_t skip, int n) {
+// The 16 bytes, `skip` bytes into their words; only the first n of them unless WHOLE.
+template <bool WHOLE>
+__device__ __forceinline__ v4i bytes16(const Words& r, uint32_t skip, int n = 16) {
   v4i o;
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const uint32_t hi = static_cast<uint32_t>(i < 3 ? r.v[i + 1] : r.x);
     uint32_t w = __builtin_amdgcn_alignbyte(hi, static_cast<uint32_t>(r.v[i]), skip);
-    if (n < 16) w &= n >= 4 * i + 4 ? ~0u : n <= 4 * i ? 0u : (1u << (8 * (n - 4 * i))) - 1;
+    if (!WHOLE) w &= n >= 4 * i + 4 ? ~0u : n <= 4 * i ? 0u : (1u << (8 * (n - 4 * i))) - 1;
     o[i] = static_cast<int>(w);
   }
   return o;
@@ -783,14 +784,20 @@ __global__ __launch_bounds__(64 * WV) void linear_stream_kernel(LinearArgs a, ui
 #pragma unroll
     for (int u = 0; u < U; ++u)
       if (c + u < n) {
-        const int first = (c0 + c + u) * 128, left = first + 128 <= a.K ? 16 : a.K - first - part * 16;
+        const int first = (c0 + c + u) * 128, left = a.K - first - part * 16;
+        auto turn = [&](auto whole) {
 #pragma unroll
-        for (int i = 0; i < NL; ++i) {  // bytes behind K count as zero; it takes one operand to see to that
-          v4i v;
-          if constexpr (ALIGNED) v = i >= 2 * RT || left > 0 ? held[u][i] : v4i{0, 0, 0, 0};
-          else v = bytes16(held[u][i], skip_of(rows[i]), i < 2 * RT ? left : 16);
-          *reinterpret_cast<v4i*>(own + place(i * 8 + (lane >> 3), part)) = v;
-        }
+          for (int i = 0; i < NL; ++i) {  // bytes behind K count as zero; it takes one operand to see to that
+            constexpr bool kWhole = decltype(whole)::value;
+            v4i v;
+            if constexpr (ALIGNED) v = kWhole || i >= 2 * RT || left > 0 ? held[u][i] : v4i{0, 0, 0, 0};
+            else if (kWhole || i >= 2 * RT) v = bytes16<true>(held[u][i], skip_of(rows[i]));
+            else v = bytes16<false>(held[u][i], skip_of(rows[i]), left);
+            *reinterpret_cast<v4i*>(own + place(i * 8 + (lane >> 3), part)) = v;
+          }
+        };
+        if (first + 128 <= a.K) turn(std::true_type{});
+        else turn(std::false_type{});
         if (c + u + U < n) load(u, c + u + U);
         wave_sync();
 #pragma unroll
@@ -1141,13 +1148,18 @@ __global__ __launch_bounds__(256, 2) void linear_any_kernel(LinearArgs a, uint32
     }
   };
   auto store = [&](int s, int buf) {
-    const int left = (s + 1) * KB <= a.K ? 16 : a.K - s * KB - part * 16;  // bytes behind K count as zero
+    auto turn = [&](auto whole) {
+      const int left = a.K - s * KB - part * 16;  // bytes behind K count as zero
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int r = r0 + 32 * i;
-      *reinterpret_cast<v4i*>(smem + buf + r * KB + place(r, part) * 16) = bytes16(ga[i], skip_of(pa[i]), 16);
-      *reinterpret_cast<v4i*>(smem + buf + (BM + r) * KB + place(r, part) * 16) = bytes16(gw[i], skip_of(pw[i]), left);
-    }
+      for (int i = 0; i < 4; ++i) {
+        const int r = r0 + 32 * i;
+        *reinterpret_cast<v4i*>(smem + buf + r * KB + place(r, part) * 16) = bytes16<true>(ga[i], skip_of(pa[i]));
+        *reinterpret_cast<v4i*>(smem + buf + (BM + r) * KB + place(r, part) * 16) =
+            bytes16<decltype(whole)::value>(gw[i], skip_of(pw[i]), left);
+      }
+    };
+    if ((s + 1) * KB <= a.K) turn(std::true_type{});
+    else turn(std::false_type{});
   };
   const int wm = (wave & 1) * 64, wn = (wave >> 1) * 64, n = (a.K + KB - 1) / KB;
   v16i acc[TN][TM] = {};
