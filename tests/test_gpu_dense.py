@@ -190,7 +190,10 @@ def _gate(m, x, w, ld=None, out_ld=None):
 
 @pytest.mark.parametrize("B,E,D", [(1, 160, 3584), (8, 160, 3584), (1, 1, 512), (17, 16, 512), (64, 81, 1024),
                                    (65, 200, 512), (129, 15, 1536), (300, 1024, 512), (256, 160, 3584), (31, 96, 512),
-                                   (2, 256, 16384)])
+                                   (2, 256, 16384),
+                                   # one for each further tile: 32 x 16, 32 x 32, 64 x 32, 64 x 48, 64 x 80
+                                   (600, 160, 512), (1300, 161, 512), (2601, 160, 512), (5000, 100, 512),
+                                   (8191, 159, 512), (9000, 250, 512)])
 @pytest.mark.parametrize("wtype", [BF, F32])
 def test_gate_whole_numbers_are_exact(m, B, E, D, wtype):
     """Whole numbers whose sums stay below 2^24: every order of summation gives the same."""
