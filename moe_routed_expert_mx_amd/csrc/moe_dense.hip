@@ -1340,8 +1340,12 @@ int launch_linear(const LinearArgs& a, hipStream_t st) {
       const int64_t b = SWIGLU ? bn / 2 : bn;
       return (((a.M + bm - 1) / bm) * ((cols + b - 1) / b) + 255) / 256 * us;
     };
-    const int64_t c0 = cost(64, 128, 22), c1 = cost(128, 128, 35), c2 = cost(128, 256, 64), c3 = cost(256, 256, 124);
+    // (Timed over 32 to 6400 tokens, 256 to 8192 columns, K from 256 to 8192.)
+    const int64_t c0 = cost(64, 128, 22), c1 = cost(128, 128, 37), c2 = cost(128, 256, 64), c3 = cost(256, 256, 124);
     const int64_t best = std::min(std::min(c0, c1), std::min(c2, c3));
+    if constexpr (!SWIGLU) {  // (a wave's 32 rows hold no gate and up pair)
+      if (cost(64, 64, 17) < best) return launch_dma<64, 64, 2, 2, 128, 4, OUT, SWIGLU>(a, st);
+    }
     if (best == c3) return launch_dma<256, 256, 2, 4, 128, 2, OUT, SWIGLU>(a, st);
     if (best == c2) return launch_dma<128, 256, 2, 4, 128, 3, OUT, SWIGLU>(a, st);
     if (best == c1) return launch_dma<128, 128, 4, 2, 128, 4, OUT, SWIGLU>(a, st);

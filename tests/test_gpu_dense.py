@@ -365,8 +365,9 @@ def test_linear_sizes(m, M, N, K, act):
                   bias=i % 2 == 0, add=i % 4 < 2)
 
 
-# sizes that take each of the tiles (64 x 128, 128 x 128, 128 x 256, 256 x 256) and the kernel for unaligned rows
-TILES = [(300, 2050, 272), (1000, 3000, 144), (2000, 4000, 80), (4090, 4090, 80), (520, 2050, 273), (700, 2500, 130)]
+# sizes that take each of the tiles (64 x 64, 64 x 128, 128 x 128, 128 x 256, 256 x 256) and the kernel for unaligned
+# rows
+TILES = [(300, 2050, 272), (500, 3000, 272), (1000, 3000, 144), (2000, 4000, 80), (4090, 4090, 80), (520, 2050, 273), (700, 2500, 130)]
 
 
 @pytest.mark.parametrize("M,N,K", TILES)
