@@ -294,7 +294,11 @@ _current_stream = torch._C._cuda_getCurrentRawStream
 
 def _load_binding():
     """The native binding, bound to the library; it is built with it."""
-    from . import _dense
+    try:
+        from . import _dense
+    except ImportError as e:
+        raise ImportError(f"the native binding is not built ({e}): run `python moe_routed_expert_mx_amd/build.py` "
+                          "(or __graft_entry__.build()) first") from e
     addresses = [ctypes.cast(getattr(lib, f), ctypes.c_void_p).value
                  for f in ("moe_gate", "moe_route", "moe_quant_i8", "moe_linear_i8")]
     _dense.bind(*addresses, _current_stream, _current_device)

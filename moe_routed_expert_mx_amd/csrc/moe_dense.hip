@@ -1327,7 +1327,8 @@ int launch_linear(const LinearArgs& a, hipStream_t st) {
   constexpr int R1 = SWIGLU ? 2 : 1;
   const int64_t blocks = static_cast<int64_t>((a.M + 63) / 64) * (((SWIGLU ? a.N / 2 : a.N) + 15) / 16);
   const bool wide = !SWIGLU && blocks > 256;
-  if (a.M <= 16) return launch_stream<OUT, SWIGLU, ALIGNED, R1, 1, 16>(a, st);
+  // (unaligned gate and up rows take more registers than sixteen waves leave)
+  if (a.M <= 16) return launch_stream<OUT, SWIGLU, ALIGNED, R1, 1, SWIGLU && !ALIGNED ? 8 : 16>(a, st);
   if (a.M <= 32)
     return wide ? launch_stream<OUT, SWIGLU, ALIGNED, 2, 2, 8>(a, st) : launch_stream<OUT, SWIGLU, ALIGNED, R1, 2, 8>(a, st);
   if (a.M <= 64 || blocks <= (SWIGLU ? 256 : ALIGNED ? 512 : 1024))
