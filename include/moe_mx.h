@@ -434,7 +434,7 @@ typedef struct {
  * The sum is exact (32-bit integers), the rest is FP32.  a_dev int8 [M, K] (lda >= K), w_dev
  * int8 [N, K] (ldw >= K), out_dev [M, N or N/2] of out_type (ldo).  All 256 codes are taken
  * at their value.  Rows whose start is 16-byte aligned with K % 16 == 0 (a_dev, w_dev,
- * lda, ldw) are read the fast way.  1 <= N <= 2^20, M * N <= 2^34, 1 <= K <=
+ * lda, ldw) are read the fast way; others as the aligned 4-byte words that hold their bytes.  1 <= N <= 2^20, M * N <= 2^34, 1 <= K <=
  * 131071 (the sum's range), lda and ldw < 2^22; MOE_EINVAL otherwise. */
 int moe_linear_i8(const int8_t* a_dev, int64_t lda, const float* a_scales_dev, const int8_t* w_dev,
                   int64_t ldw, const float* w_scales_dev, int32_t M, int32_t N, int32_t K,
