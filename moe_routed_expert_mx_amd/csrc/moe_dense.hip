@@ -997,14 +997,17 @@ __global__ __launch_bounds__(64 * WM * WN, (BM + BN) * KB * NS > 78 * 1024 ? 1 :
   }
   constexpr int kIssue = RA + RW;
   // DMA d of this wave for stage s into the LDS at buf; parts behind K, and whole stages behind
-  // it, are zeros
+  // it, are zeros.  The bounds check holds a lane's offset against the extent less the scalar offset, so a
+  // stage behind K has none: with few rows in the tile it could exceed the extent, and nothing says that
+  // the difference does not wrap.
   auto issue = [&](int s, int buf, int d) {
     const int k0 = s * KB;
+    const uint32_t soff = k0 < a.K ? k0 : 0;
     if (d < RA) {
-      dma16(ra, k0 + ka[d] < a.K ? va[d] : kOutside, k0, lds0 + buf + (wave * RA + d) * 1024);
+      dma16(ra, k0 + ka[d] < a.K ? va[d] : kOutside, soff, lds0 + buf + (wave * RA + d) * 1024);
     } else {
       d -= RA;
-      dma16(rw[d], k0 + kw[d] < a.K ? vw[d] : kOutside, k0, lds0 + buf + BM * KB + (wave * RW + d) * 1024);
+      dma16(rw[d], k0 + kw[d] < a.K ? vw[d] : kOutside, soff, lds0 + buf + BM * KB + (wave * RW + d) * 1024);
     }
   };
 

@@ -378,6 +378,16 @@ def test_linear_tiles(m, M, N, K, act):
     _check_linear(m, M, N, K, act=act, out=F32 if M < 2000 else F16, lda=pad, ldw=2 * pad, ldo=3, offset=pad, seed=2)
 
 
+# a single row in the last tile of each size, plain (64 x 64, 64 x 128, 128 x 128, 128 x 256, 256 x 256) and SwiGLU
+@pytest.mark.parametrize("M,N,act", [(257, 1793, "none"), (257, 3329, "none"), (513, 3585, "none"), (3585, 1025, "none"),
+                                     (3073, 3841, "none"), (513, 1026, "swiglu"), (257, 6658, "swiglu"),
+                                     (513, 7170, "swiglu"), (2305, 5122, "swiglu")])
+def test_linear_last_tile_of_one_row(m, M, N, act):
+    """Its extent is one row of K bytes, and the stages issued ahead lie behind that."""
+    _check_linear(m, M, N, 16, act=act, out=F32, seed=3)
+    _check_linear(m, M, N, 144, act=act, bias=True, lda=16, ldw=32, seed=4)
+
+
 @pytest.mark.parametrize("M,N", [(300, 2050), (1000, 3000)])
 def test_linear_tiles_longest_rows(m, M, N):
     K = 131056
