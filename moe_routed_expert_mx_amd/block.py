@@ -5,14 +5,43 @@
 moe_linear_i8), and ``MoeBlock`` runs them around a ``MoeLayer``: router, routed experts,
 weighted combine, shared expert added last.  Each owns its device buffers for up to B_max
 tokens and reuses them from call to call, so calls of one object must be ordered (one
-stream, or ordered streams).  torch only allocates memory and supplies the stream.
+stream, or ordered streams), and follow its construction, which enqueues on the current stream.
+torch only allocates memory and supplies the stream.
+
+A call runs on the current stream, or on `stream` (a torch stream or a raw handle): there it
+allocates too, as it would under torch.cuda.stream(stream), so that no buffer it drops is
+handed on before the stream is done with it.  What it returns is recorded on the caller's current
+stream: after the usual wait for `stream` it may be read there and dropped at any time.
 """
 from __future__ import annotations
+
+import contextlib
 
 import torch
 
 from . import _lib
 from .layer import MoeLayer
+
+
+@contextlib.contextmanager
+def _on(stream, device):
+    """Work and allocate on `stream` of `device` (None: its current one); yields a function that hands tensors on to
+    the caller's stream."""
+    if stream is None:
+        yield lambda t: t
+        return
+    caller = torch.cuda.current_stream(device)
+    if not hasattr(stream, "cuda_stream"):
+        stream = torch.cuda.ExternalStream(int(stream), device=device)
+    elif stream.device_index != device.index:
+        raise ValueError("the stream belongs to another GPU than the tensors")
+
+    def give(t):
+        t.record_stream(caller)
+        return t
+
+    with torch.cuda.stream(stream):
+        yield give
 
 
 class Router:
@@ -38,12 +67,13 @@ class Router:
         B = x.shape[0]
         if B > self.B_max:
             raise ValueError("batch larger than B_max")
-        ids = torch.empty(B, self.topk, dtype=torch.int32, device=self.device)
-        weights = torch.empty(B, self.topk, device=self.device)
-        logits = self.logits[:B]
-        _lib.moe_gate(self.gate, x, logits, stream=stream)
-        _lib.moe_route(logits, ids, weights, bias=self.bias, stream=stream, **self.opts)
-        return ids, weights
+        with _on(stream, x.device) as give:
+            ids = torch.empty(B, self.topk, dtype=torch.int32, device=self.device)
+            weights = torch.empty(B, self.topk, device=self.device)
+            logits = self.logits[:B]
+            _lib.moe_gate(self.gate, x, logits)
+            _lib.moe_route(logits, ids, weights, bias=self.bias, **self.opts)
+            return give(ids), give(weights)
 
 
 class SharedExpertI8:
@@ -79,17 +109,18 @@ class SharedExpertI8:
         B = x.shape[0]
         if B > self.B_max:
             raise ValueError("batch larger than B_max")
-        if out is None:
-            out = torch.empty(B, self.D, dtype=torch.bfloat16, device=self.device)
-        # rows of the code buffers are packed for each product, so that they stay 16-byte aligned
-        flat = self.codes.view(-1)
-        scales, hidden = self.scales[:B], self.hidden[:B]
-        q = flat[:B * self.D].view(B, self.D)
-        _lib.moe_quant_i8(x, q, scales, stream=stream)
-        _lib.moe_linear_i8(q, scales, self.w13, self.s13, hidden, act="swiglu", stream=stream)
-        q = flat[:B * self.I].view(B, self.I)
-        _lib.moe_quant_i8(hidden, q, scales, stream=stream)
-        _lib.moe_linear_i8(q, scales, self.w2, self.s2, out, add=add, stream=stream)
+        with _on(stream, x.device) as give:
+            if out is None:
+                out = give(torch.empty(B, self.D, dtype=torch.bfloat16, device=self.device))
+            # rows of the code buffers are packed for each product, so that they stay 16-byte aligned
+            flat = self.codes.view(-1)
+            scales, hidden = self.scales[:B], self.hidden[:B]
+            q = flat[:B * self.D].view(B, self.D)
+            _lib.moe_quant_i8(x, q, scales)
+            _lib.moe_linear_i8(q, scales, self.w13, self.s13, hidden, act="swiglu")
+            q = flat[:B * self.I].view(B, self.I)
+            _lib.moe_quant_i8(hidden, q, scales)
+            _lib.moe_linear_i8(q, scales, self.w2, self.s2, out, add=add)
         return out
 
 
@@ -106,13 +137,13 @@ class MoeBlock:
         rows, rounded to BF16, plus the shared expert's."""
         if x.dtype != torch.bfloat16 or not x.is_contiguous():
             raise ValueError("x: expected contiguous BF16 [B, D]")
-        with torch.cuda.device(x.device):
-            return self._forward(x, stream, path)
+        with torch.cuda.device(x.device), _on(stream, x.device) as give:
+            return give(self._forward(x, path))
 
-    def _forward(self, x, stream, path):
-        ids, weights = self.router.forward(x, stream=stream)
-        rows = self.layer.forward(x, ids, stream=stream, path=path)
-        y = self.layer.combine(rows, weights, stream=stream)
+    def _forward(self, x, path):
+        ids, weights = self.router.forward(x)
+        rows = self.layer.forward(x, ids, path=path)
+        y = self.layer.combine(rows, weights)
         if self.shared is not None:
-            self.shared.forward(x, add=y, out=y, stream=stream)
+            self.shared.forward(x, add=y, out=y)
         return y

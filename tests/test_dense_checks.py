@@ -150,3 +150,73 @@ def test_native_binding_declines():
     assert d.gate(0x1000, 512, 16, x, _z(4, 16)) == no
     meta = torch.empty(4, 512, dtype=BF, device="meta")
     assert d.quant(meta, q, s) == no
+
+
+def test_layer_objects_allocate_on_the_stream_they_run_on(monkeypatch):
+    """Buffers of a call with a stream come from that stream's pool: one that is dropped at return, with the kernels still
+    to run, must not be handed to work on another stream.  (Stand-ins for the library and the streams: no GPU needed.)"""
+    import contextlib
+    import types
+
+    from moe_routed_expert_mx_amd import block
+
+    here, side = types.SimpleNamespace(name="here"), types.SimpleNamespace(name="side", cuda_stream=7,
+                                                                            device_index=None)
+    state = types.SimpleNamespace(current=here, allocated=[], calls=[], recorded=[])
+
+    @contextlib.contextmanager
+    def entered(s):
+        before, state.current = state.current, s
+        yield
+        state.current = before
+
+    class Tensors(torch.Tensor):
+        def record_stream(self, s):
+            state.recorded.append(s)
+
+    empty = torch.empty
+
+    def recording(*a, **k):
+        state.allocated.append(state.current)
+        return empty(*a, **k).as_subclass(Tensors)
+
+    def called(*a, stream=None, **k):
+        state.calls.append(state.current if stream is None else stream)
+
+    class Layer:
+        E, D, topk = 16, 512, 2
+
+        def forward(self, x, ids, *, stream=None, path="auto"):
+            called(stream=stream)
+            return torch.empty(len(ids) * 2, 512, dtype=BF)
+
+        def combine(self, rows, weights, *, stream=None):
+            called(stream=stream)
+            return torch.empty(len(weights), 512, dtype=BF)
+
+    fake = types.SimpleNamespace(moe_gate_packed_bytes=lambda *a: 64, moe_gate_pack=lambda w, p: p, moe_gate=called,
+                                 moe_route=called, moe_quant_i8=called, moe_linear_i8=called)
+    monkeypatch.setattr(block, "_lib", fake)
+    monkeypatch.setattr(torch, "empty", recording)
+    monkeypatch.setattr(torch.cuda, "stream", entered)
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda *a: state.current)
+    monkeypatch.setattr(torch.cuda, "device", lambda d: contextlib.nullcontext())
+    monkeypatch.setattr(torch.cuda, "ExternalStream", lambda h, device=None: side if h == 7 else None)
+    router = block.Router(_z(16, 512, dtype=BF), topk=2, B_max=4, device="cpu")
+    i8 = torch.int8
+    shared = block.SharedExpertI8(_z(64, 512, dtype=i8), _z(64), _z(512, 32, dtype=i8), _z(512), B_max=4, device="cpu")
+    x = _z(3, 512, dtype=BF)
+    for stream in (side, 7):
+        for obj, calls, made, returned in ((router, 2, 2, 2), (shared, 4, 1, 1),
+                                           (block.MoeBlock(router, Layer(), shared), 8, 4, 1)):
+            for record in (state.allocated, state.calls, state.recorded):
+                record.clear()
+            obj.forward(x, stream=stream)
+            assert state.allocated == [side] * made
+            assert len(state.calls) == calls and all(c in (side, 7) for c in state.calls)
+            assert state.recorded.count(here) == returned and state.current is here
+    with pytest.raises(ValueError, match="another GPU"):
+        router.forward(x, stream=types.SimpleNamespace(cuda_stream=9, device_index=3))
+    state.allocated.clear()
+    router.forward(x)
+    assert state.allocated == [here] * 2

@@ -638,3 +638,46 @@ def test_shared_expert_twice_with_other_batches(m):
         assert torch.equal(sh.forward(x), want)
     with pytest.raises(ValueError):
         sh.forward(torch.zeros(101, 512, dtype=BF, device=DEV))
+
+
+@pytest.mark.parametrize("raw", [False, True])
+@pytest.mark.parametrize("B", [3, 40])
+def test_block_on_a_side_stream(m, B, raw):
+    """The layer on a stream that lags behind: what the current stream allocates and fills right after the call
+    must not be what the call still uses."""
+    import workloads
+    from moe_routed_expert_mx_amd.block import MoeBlock, Router, SharedExpertI8
+    from moe_routed_expert_mx_amd.layer import MoeLayer
+    log(f"block on a side stream B={B} raw={raw}")
+    d = workloads.generate(workloads.custom(B=B, E=24, K=4, D=512, I=64, seed=B + 5))
+    g = _gen(B)
+    x = torch.from_numpy(d["x"]).view(BF).to(DEV)
+    router = Router(torch.randn(24, 512, generator=g) / 22, topk=4, B_max=48)
+    layer = MoeLayer(d["w13"], d["s13"], d["w2"], d["s2"], B_max=48, topk=4, device=DEV)
+    shared = SharedExpertI8.quantize(torch.randn(2 * 96, 512, generator=g) / 22, torch.randn(512, 96, generator=g) / 10,
+                                     B_max=48)
+    block = MoeBlock(router, layer, shared)
+    calls = [block.forward, shared.forward, lambda x, stream=None: router.forward(x, stream=stream)[1]]
+    want = [c(x).clone() for c in calls]
+    big = torch.randn(4096, 4096, device=DEV)
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    for call, w in zip(calls, want):
+        for _ in range(3):
+            with torch.cuda.stream(s):
+                for _ in range(8):
+                    torch.mm(big, big)
+            y = call(x, stream=s.cuda_stream if raw else s)
+            junk = []
+            for _ in range(4):
+                junk += [torch.zeros(B, 4, dtype=torch.int32, device=DEV), torch.zeros(B, 4, device=DEV),
+                         torch.zeros(B * 4, 512, dtype=BF, device=DEV), torch.zeros(B, 512, dtype=BF, device=DEV)]
+            torch.cuda.current_stream().wait_stream(s)
+            got = y.clone()
+            torch.cuda.synchronize()
+            assert torch.equal(got, w)
+            assert not any(j.any() for j in junk)
+    y = block.forward(x, stream=torch.cuda.default_stream().cuda_stream if raw else torch.cuda.default_stream())
+    torch.cuda.synchronize()
+    assert torch.equal(y, want[0])
