@@ -282,7 +282,9 @@ def moe_combine(rows, weights, out, stream=None):
 # unit stride within rows and one GPU for all of them raise ValueError.  They run on that
 # GPU's current stream, whichever GPU is current.  A call takes some microseconds of host
 # time, as long as the smallest kernels run, so the native binding (csrc/dense_binding.cpp)
-# goes first: it enqueues what is plainly right, and leaves the rest to the code here.
+# goes first: it enqueues what is plainly right, and leaves the rest to the code here.  Only what it
+# did not take (_NOT_TAKEN) is tried here: another status is the library's own, and a call that it
+# may have enqueued is not made a second time (the product of moe_linear_i8 would be added twice).
 _MOE_TYPE = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
 _BF16, _F32, _I32, _I8, _U8 = torch.bfloat16, torch.float32, torch.int32, torch.int8, torch.uint8
 _ROUTE_OPTS = struct.Struct("@5ifP2i")   # moe_route_opts_t
@@ -306,6 +308,7 @@ def _load_binding():
 
 
 _dense = _load_binding()
+_NOT_TAKEN = -100
 
 
 def _refuse(what: str):
@@ -384,8 +387,10 @@ def moe_gate_pack(w, packed, stream=None) -> moe_gate_t:
 
 def moe_gate(gate: moe_gate_t, x, logits, stream=None):
     """Router product: x BF16 [B, D] (rows may be strided) -> logits FP32 [B, E]."""
-    if stream is None and _dense.gate(ctypes.addressof(gate), gate.D, gate.E, x, logits) == 0:
-        return
+    if stream is None:
+        status = _dense.gate(ctypes.addressof(gate), gate.D, gate.E, x, logits)
+        if status != _NOT_TAKEN:
+            return _check("moe_gate", status)
     B = _matrix(x, "x")[0]
     if x.dtype != _BF16 or logits.dtype != _F32:
         _refuse("x: expected BF16, logits: FP32")
@@ -404,8 +409,10 @@ def moe_route(logits, ids, weights, *, score: str = "softmax", bias=None, groups
     "sigmoid"; groups experts groups of which topk_groups stay, ranked by group_score "max" or "top2"; renorm
     divides a token's weights by their sum; scale multiplies them."""
     sc, gs = _SCORES.get(score), _GROUP_SCORES.get(group_score)
-    if stream is None and _dense.route(logits, ids, weights, sc, bias, groups, topk_groups, gs, renorm, scale) == 0:
-        return
+    if stream is None:
+        status = _dense.route(logits, ids, weights, sc, bias, groups, topk_groups, gs, renorm, scale)
+        if status != _NOT_TAKEN:
+            return _check("moe_route", status)
     shape = _matrix(logits, "logits")
     B, E = shape
     kind = _MOE_TYPE.get(logits.dtype)
@@ -430,8 +437,10 @@ def moe_route(logits, ids, weights, *, score: str = "softmax", bias=None, groups
 def moe_quant_i8(x, codes, scales, stream=None):
     """Int8 quantization with one scale for each token: x [M, K] (FP32, BF16 or FP16) -> codes int8 [M, K], scales
     FP32 [M]; code * scale stands for x."""
-    if stream is None and _dense.quant(x, codes, scales) == 0:
-        return
+    if stream is None:
+        status = _dense.quant(x, codes, scales)
+        if status != _NOT_TAKEN:
+            return _check("moe_quant_i8", status)
     shape = _matrix(x, "x")
     kind = _MOE_TYPE.get(x.dtype)
     if kind is None or codes.dtype != _I8:
@@ -450,8 +459,10 @@ def moe_linear_i8(a, a_scales, w, w_scales, out, *, act: str = "none", bias=None
     FP16), y = (a . w) * a_scales * w_scales + bias (FP32 [N]); act "swiglu": the first N/2 rows of w are the gate,
     the others up, and out is [M, N/2]; add (as out, may be out itself) is added last."""
     mode = _ACTS.get(act)
-    if stream is None and _dense.linear(a, a_scales, w, w_scales, out, mode, bias, add) == 0:
-        return
+    if stream is None:
+        status = _dense.linear(a, a_scales, w, w_scales, out, mode, bias, add)
+        if status != _NOT_TAKEN:
+            return _check("moe_linear_i8", status)
     shape, kind = _matrix(a, "a"), _MOE_TYPE.get(out.dtype)
     M, K = shape
     N = _matrix(w, "w")[0]

@@ -3,9 +3,9 @@
 // A decode step's kernels take 3 to 6 us, and so do the checks and argument conversions of a
 // ctypes call.  Each function here takes what its namesake in _lib.py takes (options as plain
 // numbers), checks it the same way and calls the library on the current stream of the tensors'
-// GPU.  It returns 0 when the call was enqueued; anything else -- a tensor it does not like, another
-// GPU than the current one, a refusal -- is left to _lib.py, which checks again and says what
-// is wrong.  No function of the library is linked: their addresses come through bind().
+// GPU.  It returns the library's status, or kNotTaken if it did not call it -- a tensor it does not
+// like, another GPU than the current one --: those are left to _lib.py, which checks again and says
+// what is wrong.  No function of the library is linked: their addresses come through bind().
 #include <torch/csrc/autograd/python_variable.h>
 
 #include "moe_mx.h"
@@ -59,8 +59,10 @@ struct Call {
     return nullptr;
   }
   void need(bool b) { ok = ok && b; }
-  void* stream() {  // of the tensors' GPU, which must be the current one
-    if (!ok) return nullptr;
+  // The stream of the tensors' GPU, which must be the current one.  The last step before the library's call: an
+  // argument or an answer that was no number clears `ok` here.
+  void* stream() {
+    if (!ok || PyErr_Occurred()) return fail();
     PyObject* d = PyObject_CallNoArgs(g_device);
     const long current = d ? PyLong_AsLong(d) : -1;
     Py_XDECREF(d);
@@ -71,7 +73,7 @@ struct Call {
     if (!s) return fail();
     void* raw = PyLong_AsVoidPtr(s);
     Py_DECREF(s);
-    return raw;
+    return PyErr_Occurred() ? fail() : raw;
   }
 };
 
@@ -113,7 +115,7 @@ long route(PyObject* const* v) {
              ranked = PyLong_AsLong(v[7]);
   const int renorm = PyObject_IsTrue(v[8]);
   const double scale = PyFloat_AsDouble(v[9]);
-  c.need(!PyErr_Occurred() && renorm >= 0 && scale != 0.0 && groups >= 0 && groups <= 64 && kept >= 0 && kept <= 64);
+  c.need(renorm >= 0 && scale != 0.0 && groups >= 0 && groups <= 64 && kept >= 0 && kept <= 64);
   void* st = c.stream();
   if (!c.ok) return kNotTaken;
   const moe_route_opts_t o = {static_cast<int32_t>(score),  static_cast<int32_t>(groups), static_cast<int32_t>(kept),
@@ -161,7 +163,8 @@ long linear(PyObject* const* v) {
                   static_cast<int32_t>(N), static_cast<int32_t>(K), &o, out, type_of(v[4]), ldo, st);
 }
 
-// No exception leaves: a tensor without storage, say, is one that _lib.py has to explain.
+// No exception leaves: a tensor without storage, say, is one that _lib.py has to explain.  (The library throws none,
+// so one means that it was not called.)
 template <long (*F)(PyObject* const*), int ARGS>
 PyObject* entry(PyObject*, PyObject* const* args, Py_ssize_t n) {
   long r = kNotTaken;
@@ -170,10 +173,7 @@ PyObject* entry(PyObject*, PyObject* const* args, Py_ssize_t n) {
   } catch (...) {
     r = kNotTaken;
   }
-  if (PyErr_Occurred()) {
-    PyErr_Clear();
-    r = kNotTaken;
-  }
+  PyErr_Clear();
   return PyLong_FromLong(r);
 }
 

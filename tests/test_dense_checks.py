@@ -220,3 +220,21 @@ def test_layer_objects_allocate_on_the_stream_they_run_on(monkeypatch):
     state.allocated.clear()
     router.forward(x)
     assert state.allocated == [here] * 2
+
+
+@pytest.mark.parametrize("status", [m._lib.MOE_EHIP, EINVAL])
+def test_a_status_of_the_library_is_raised_not_retried(monkeypatch, status):
+    """A call that the native binding made may be enqueued whatever its status: made again, moe_linear_i8 with add = out
+    would add its product twice."""
+    made = []
+    for name in ("gate", "route", "quant", "linear"):
+        monkeypatch.setattr(m._lib._dense, name, lambda *a: status)
+    monkeypatch.setattr(m._lib, "_enqueue", lambda name, *a: made.append(name))
+    x, q, s = _z(4, 512, dtype=BF), _z(4, 512, dtype=torch.int8), _z(4)
+    out = _z(4, 4)
+    for call in (lambda: m.moe_gate(m.moe_gate_t(16, 512, 0, 0x1000), x, _z(4, 16)),
+                 lambda: m.moe_route(_z(4, 16), _z(4, 2, dtype=torch.int32), _z(4, 2)),
+                 lambda: m.moe_quant_i8(x, q, s), lambda: m.moe_linear_i8(q, s, q, s, out, add=out)):
+        with pytest.raises(m.MoeError) as e:
+            call()
+        assert e.value.status == status and made == []

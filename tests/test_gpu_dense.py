@@ -585,6 +585,37 @@ def test_native_binding_and_ctypes_agree(m):
         m.moe_route(lg, ids, wt, groups=7, topk_groups=1)       # 40 experts, 7 groups
 
 
+def test_native_binding_calls_once_or_not_at_all(m):
+    """The library's status comes back as it is, after one call; a stream that is no handle means no call.  (The
+    library's function is a stand-in that launches nothing.)"""
+    import ctypes
+    calls, status = [], [0]
+
+    @ctypes.CFUNCTYPE(ctypes.c_int, *[ctypes.c_void_p] * 14)
+    def linear(*a):
+        calls.append(a)
+        return status[0]
+
+    lib, d = m._lib, m._lib._dense
+    names = ("moe_gate", "moe_route", "moe_quant_i8", "moe_linear_i8")
+    own = [ctypes.cast(getattr(lib.lib, n), ctypes.c_void_p).value for n in names]
+    stub = own[:3] + [ctypes.cast(linear, ctypes.c_void_p).value]
+    q, s, out = torch.zeros(4, 16, dtype=torch.int8, device=DEV), torch.zeros(4, device=DEV), torch.zeros(4, 4, device=DEV)
+    try:
+        d.bind(*stub, lib._current_stream, lib._current_device)
+        for status[0] in (0, lib.MOE_EHIP, lib.MOE_EINVAL):
+            assert d.linear(q, s, q, s, out, 0, None, out) == status[0]
+        assert len(calls) == 3
+        for st in ("stream", None, 1 << 70):
+            d.bind(*stub, lambda dev: st, lib._current_device)
+            assert d.linear(q, s, q, s, out, 0, None, out) == -100
+        d.bind(*stub, lib._current_stream, lambda: "device")
+        assert d.linear(q, s, q, s, out, 0, None, out) == -100
+        assert len(calls) == 3
+    finally:
+        d.bind(*own, lib._current_stream, lib._current_device)
+
+
 @pytest.mark.parametrize("B", [1, 8, 40])
 def test_block_end_to_end(m, B):
     """The layer as it is used: router, routed experts, combine, shared expert.  Each stage is
