@@ -1196,7 +1196,22 @@ __global__ __launch_bounds__(256, 2) void linear_any_kernel(LinearArgs a, uint32
 
 // ---------------------------------------------------------------------- host
 hipStream_t as_stream(void* s) { return reinterpret_cast<hipStream_t>(s); }
-int launch_status() { return hipGetLastError() == hipSuccess ? MOE_OK : MOE_EHIP; }
+int hip_failed() {
+  (void)hipGetLastError();  // reported here, and not again by the thread's next caller
+  return MOE_EHIP;
+}
+// Enqueue a kernel.  The status is this launch's own: the thread's last error may be an earlier call's, and would
+// make a call that was enqueued look like one that was not.
+template <typename T>
+struct Same {
+  using type = T;
+};
+template <typename... P>
+int launch(void (*kernel)(P...), uint32_t grid, uint32_t block, size_t lds, hipStream_t st, typename Same<P>::type... p) {
+  void* args[] = {const_cast<void*>(static_cast<const void*>(&p))...};
+  const hipError_t e = hipLaunchKernel(reinterpret_cast<const void*>(kernel), dim3(grid), dim3(block), args, lds, st);
+  return e == hipSuccess ? MOE_OK : hip_failed();
+}
 constexpr int32_t kMaxRows = 1 << 22;  // tokens of one call: its grids stay within the launch limits
 bool type_ok(int32_t t) { return t == MOE_BF16 || t == MOE_F16 || t == MOE_F32; }
 bool gate_ok(int32_t E, int32_t D, int32_t wtype) {
@@ -1206,8 +1221,7 @@ bool gate_ok(int32_t E, int32_t D, int32_t wtype) {
 template <int TYPE, int LPT, int NV>
 int launch_route(const RouteArgs& a, hipStream_t st) {
   constexpr int per = 4 * (64 / LPT);
-  hipLaunchKernelGGL((route_kernel<TYPE, LPT, NV>), dim3(static_cast<unsigned>((a.B + per - 1) / per)), dim3(256), 0, st, a);
-  return launch_status();
+  return launch(route_kernel<TYPE, LPT, NV>, (a.B + per - 1) / per, 256, 0, st, a);
 }
 
 template <int TYPE>
@@ -1226,9 +1240,7 @@ template <int TYPE, int W, int NV>
 int launch_quant(const void* x, int64_t ldx, int32_t M, int32_t K, int8_t* codes, int64_t ldc, float* scales,
                  hipStream_t st) {
   constexpr int per = 4 / W;
-  hipLaunchKernelGGL((quant_kernel<TYPE, W, NV>), dim3(static_cast<unsigned>((M + per - 1) / per)), dim3(256), 0, st, x,
-                     ldx, M, K, codes, ldc, scales);
-  return launch_status();
+  return launch(quant_kernel<TYPE, W, NV>, (M + per - 1) / per, 256, 0, st, x, ldx, M, K, codes, ldc, scales);
 }
 
 template <int TYPE>
@@ -1267,11 +1279,9 @@ int launch_gate_tile(const GateArgs& a, hipStream_t st) {
   static std::atomic<uint64_t> done{0};
   constexpr size_t lds = WV * std::max(64 * TT * (16 * ET + 4), 2048 * TT);
   static_assert(lds <= 160 * 1024, "gate tile");
-  if (!allow_lds(gate_kernel<P, TT, ET, WV>, lds, done)) return MOE_EHIP;
+  if (!allow_lds(gate_kernel<P, TT, ET, WV>, lds, done)) return hip_failed();
   const uint32_t cols = ((a.E + 15) / 16 + ET - 1) / ET, rows = static_cast<uint32_t>((a.B + 16 * TT - 1) / (16 * TT));
-  hipLaunchKernelGGL((gate_kernel<P, TT, ET, WV>), dim3((rows + 7) / 8 * 8 * cols), dim3(64 * WV), lds, st, a, cols,
-                     rows);
-  return launch_status();
+  return launch(gate_kernel<P, TT, ET, WV>, (rows + 7) / 8 * 8 * cols, 64 * WV, lds, st, a, cols, rows);
 }
 
 template <int P>
@@ -1300,12 +1310,10 @@ int launch_stream(const LinearArgs& a, hipStream_t st) {
   static std::atomic<uint64_t> done{0};
   constexpr size_t lds = WV * std::max(2048 * (RT + TT), 64 * TT * (16 * RT + 4));
   static_assert(lds <= 160 * 1024, "LDS of a CU");
-  if (!allow_lds(linear_stream_kernel<OUT, SWIGLU, ALIGNED, RT, TT, WV>, lds, done)) return MOE_EHIP;
+  if (!allow_lds(linear_stream_kernel<OUT, SWIGLU, ALIGNED, RT, TT, WV>, lds, done)) return hip_failed();
   const int cols = SWIGLU ? a.N / 2 : a.N, per = SWIGLU ? 16 : 16 * RT;
   const uint32_t nx = static_cast<uint32_t>((cols + per - 1) / per), ny = static_cast<uint32_t>((a.M + 16 * TT - 1) / (16 * TT));
-  hipLaunchKernelGGL((linear_stream_kernel<OUT, SWIGLU, ALIGNED, RT, TT, WV>), dim3(nx * ny), dim3(64 * WV), lds, st, a,
-                     nx);
-  return launch_status();
+  return launch(linear_stream_kernel<OUT, SWIGLU, ALIGNED, RT, TT, WV>, nx * ny, 64 * WV, lds, st, a, nx);
 }
 
 template <int BM, int BN, int WM, int WN, int KB, int NS, int OUT, bool SWIGLU>
@@ -1313,11 +1321,10 @@ int launch_dma(const LinearArgs& a, hipStream_t st) {
   static std::atomic<uint64_t> done{0};
   constexpr size_t lds = NS * (BM + BN) * KB + 4 * (BM + 2 * BN);
   static_assert(lds <= 160 * 1024, "LDS of a CU");
-  if (!allow_lds(linear_dma_kernel<BM, BN, WM, WN, KB, NS, OUT, SWIGLU>, lds, done)) return MOE_EHIP;
+  if (!allow_lds(linear_dma_kernel<BM, BN, WM, WN, KB, NS, OUT, SWIGLU>, lds, done)) return hip_failed();
   const uint32_t nm = static_cast<uint32_t>((a.M + BM - 1) / BM), bn = SWIGLU ? BN / 2 : BN,
                  nn = static_cast<uint32_t>(((SWIGLU ? a.N / 2 : a.N) + bn - 1) / bn), per = (nm * nn + 7) / 8;
-  hipLaunchKernelGGL((linear_dma_kernel<BM, BN, WM, WN, KB, NS, OUT, SWIGLU>), dim3(per * 8), dim3(64 * WM * WN), lds, st, a, nm, nn, per);
-  return launch_status();
+  return launch(linear_dma_kernel<BM, BN, WM, WN, KB, NS, OUT, SWIGLU>, per * 8, 64 * WM * WN, lds, st, a, nm, nn, per);
 }
 
 template <int OUT, bool SWIGLU, bool ALIGNED>
@@ -1357,11 +1364,10 @@ int launch_linear(const LinearArgs& a, hipStream_t st) {
   }
   static std::atomic<uint64_t> done{0};
   constexpr size_t lds = 2 * 256 * 128 + 4 * (128 + 2 * 128);
-  if (!allow_lds(linear_any_kernel<OUT, SWIGLU>, lds, done)) return MOE_EHIP;
+  if (!allow_lds(linear_any_kernel<OUT, SWIGLU>, lds, done)) return hip_failed();
   const uint32_t ny = static_cast<uint32_t>((a.M + 127) / 128);
   const uint32_t nx = static_cast<uint32_t>(SWIGLU ? (a.N / 2 + 63) / 64 : (a.N + 127) / 128);
-  hipLaunchKernelGGL((linear_any_kernel<OUT, SWIGLU>), dim3(nx * ny), dim3(256), lds, st, a, nx);
-  return launch_status();
+  return launch(linear_any_kernel<OUT, SWIGLU>, nx * ny, 256, lds, st, a, nx);
 }
 
 template <int OUT>
@@ -1384,14 +1390,12 @@ int moe_gate_pack(const void* w, int32_t wtype, int32_t E, int32_t D, void* pack
   if (!w || !packed || !gate_ok(E, D, wtype)) return MOE_EINVAL;
   if (packed_bytes < moe_gate_packed_bytes(E, D, wtype)) return MOE_ENOSPACE;
   const int64_t n = static_cast<int64_t>((E + 15) / 16) * (D / 32) * 64;
-  const dim3 grid(static_cast<unsigned>((n + 255) / 256));
+  const uint32_t grid = static_cast<uint32_t>((n + 255) / 256);
   if (wtype == MOE_F32)
-    hipLaunchKernelGGL(gate_pack_kernel<MOE_F32>, grid, dim3(256), 0, as_stream(stream),
-                       static_cast<const float*>(w), E, D, static_cast<uint16_t*>(packed));
-  else
-    hipLaunchKernelGGL(gate_pack_kernel<MOE_BF16>, grid, dim3(256), 0, as_stream(stream),
-                       static_cast<const uint16_t*>(w), E, D, static_cast<uint16_t*>(packed));
-  return launch_status();
+    return launch(gate_pack_kernel<MOE_F32>, grid, 256, 0, as_stream(stream), static_cast<const float*>(w), E, D,
+                  static_cast<uint16_t*>(packed));
+  return launch(gate_pack_kernel<MOE_BF16>, grid, 256, 0, as_stream(stream), static_cast<const uint16_t*>(w), E, D,
+                static_cast<uint16_t*>(packed));
 }
 
 int moe_gate(const moe_gate_t* g, const void* x, int64_t ldx, int32_t B, float* logits, int64_t ldl, void* stream) {

@@ -616,6 +616,36 @@ def test_native_binding_calls_once_or_not_at_all(m):
         d.bind(*own, lib._current_stream, lib._current_device)
 
 
+@pytest.mark.parametrize("through", ["binding", "ctypes"])
+def test_an_earlier_error_is_not_this_calls(m, through):
+    """An error that another call left on the thread (no such device: the runtime refuses that) neither fails the
+    calls here nor makes them run twice."""
+    st = None if through == "binding" else torch.cuda.current_stream()
+    g, hip = _gen(51), m._lib.lib
+    a, w = _codes((3, 64), g).to(DEV), _codes((32, 64), g).to(DEV)
+    sa, sw, out = torch.ones(3, device=DEV), torch.ones(32, device=DEV), torch.zeros(3, 32, device=DEV)
+    x, gw = torch.ones(3, 512, dtype=BF, device=DEV), torch.ones(16, 512, dtype=BF, device=DEV)
+    packed = torch.zeros(m.moe_gate_packed_bytes(16, 512, BF), dtype=torch.uint8, device=DEV)
+    lg, ids, wt = torch.zeros(3, 16, device=DEV), torch.zeros(3, 2, dtype=torch.int32, device=DEV), torch.zeros(3, 2, device=DEV)
+    q, s = torch.zeros(3, 512, dtype=torch.int8, device=DEV), torch.zeros(3, device=DEV)
+    want = a.cpu().double() @ w.cpu().double().T
+    torch.cuda.synchronize()
+    gate = []
+    try:
+        for call in (lambda: m.moe_linear_i8(a, sa, w, sw, out, add=out, stream=st),
+                     lambda: gate.append(m.moe_gate_pack(gw, packed, stream=st)),
+                     lambda: m.moe_gate(gate[0], x, lg, stream=st), lambda: m.moe_route(lg, ids, wt, stream=st),
+                     lambda: m.moe_quant_i8(x, q, s, stream=st)):
+            assert hip.hipSetDevice(100000) != 0
+            call()
+    finally:
+        hip.hipGetLastError()
+    torch.cuda.synchronize()
+    assert torch.equal(out.cpu().double(), want)
+    assert (lg == 512).all() and (ids == torch.tensor([0, 1], device=DEV)).all() and (wt == 0.5).all()
+    assert (q == 127).all()
+
+
 @pytest.mark.parametrize("B", [1, 8, 40])
 def test_block_end_to_end(m, B):
     """The layer as it is used: router, routed experts, combine, shared expert.  Each stage is
