@@ -424,8 +424,8 @@ def moe_route(logits, ids, weights, *, score: str = "softmax", bias=None, groups
         _refuse(f"ids: expected contiguous int32 [{B}, topk]")
     if weights.shape != out or weights.dtype != _F32 or not weights.is_contiguous():
         _refuse(f"weights: expected contiguous FP32 {list(out)}")
-    if scale == 0.0:
-        _refuse("scale must not be 0")
+    if not 0.0 < abs(ctypes.c_float(scale).value) < float("inf"):  # (the library reads 0 as 1)
+        _refuse(f"scale {scale!r}: expected a finite FP32 number other than 0")
     tensors, pb = (logits, ids, weights), 0
     if bias is not None:
         tensors, pb = (logits, ids, weights, bias), _vector(bias, "bias", E)

@@ -8,6 +8,8 @@
 // what is wrong.  No function of the library is linked: their addresses come through bind().
 #include <torch/csrc/autograd/python_variable.h>
 
+#include <cmath>
+
 #include "moe_mx.h"
 
 namespace {
@@ -114,12 +116,13 @@ long route(PyObject* const* v) {
   const long score = PyLong_AsLong(v[3]), groups = PyLong_AsLong(v[5]), kept = PyLong_AsLong(v[6]),
              ranked = PyLong_AsLong(v[7]);
   const int renorm = PyObject_IsTrue(v[8]);
-  const double scale = PyFloat_AsDouble(v[9]);
-  c.need(renorm >= 0 && scale != 0.0 && groups >= 0 && groups <= 64 && kept >= 0 && kept <= 64);
+  const float scale = static_cast<float>(PyFloat_AsDouble(v[9]));
+  // (the library reads a scale of 0 as 1)
+  c.need(renorm >= 0 && scale != 0.0f && std::isfinite(scale) && groups >= 0 && groups <= 64 && kept >= 0 && kept <= 64);
   void* st = c.stream();
   if (!c.ok) return kNotTaken;
   const moe_route_opts_t o = {static_cast<int32_t>(score),  static_cast<int32_t>(groups), static_cast<int32_t>(kept),
-                              static_cast<int32_t>(ranked), renorm, static_cast<float>(scale), bias, {0, 0}};
+                              static_cast<int32_t>(ranked), renorm, scale, bias, {0, 0}};
   return g_route(logits, type_of(v[0]), ldl, static_cast<int32_t>(B), static_cast<int32_t>(E), static_cast<int32_t>(K), &o,
                  static_cast<int32_t*>(ids), static_cast<float*>(weights), st);
 }

@@ -222,6 +222,15 @@ def test_layer_objects_allocate_on_the_stream_they_run_on(monkeypatch):
     assert state.allocated == [here] * 2
 
 
+@pytest.mark.parametrize("scale", [0, -0.0, 1e-46, -7e-46, 1e39, float("inf"), float("nan")])
+def test_route_scale_is_taken_in_fp32(scale):
+    """A scale that FP32 holds as 0 is none the library could tell from its default, 1."""
+    with pytest.raises(ValueError, match="scale"):
+        m.moe_route(_z(4, 16), _z(4, 2, dtype=torch.int32), _z(4, 2), scale=scale)
+    with pytest.raises(ValueError, match="must be on a GPU"):
+        m.moe_route(_z(4, 16), _z(4, 2, dtype=torch.int32), _z(4, 2), scale=1e-45)
+
+
 @pytest.mark.parametrize("status", [m._lib.MOE_EHIP, EINVAL])
 def test_a_status_of_the_library_is_raised_not_retried(monkeypatch, status):
     """A call that the native binding made may be enqueued whatever its status: made again, moe_linear_i8 with add = out

@@ -149,6 +149,18 @@ def test_route_infinite_bias(m):
     _check_route(m, torch.randn(5, 20, generator=_gen(1)), 4, bias=b, groups=5, topk_groups=2, group_score="top2")
 
 
+@pytest.mark.parametrize("through", ["binding", "ctypes"])
+def test_route_scales_near_the_ends_of_fp32(m, through):
+    st = None if through == "binding" else torch.cuda.current_stream()
+    x = torch.zeros(3, 16)
+    for scale in (2.0 ** -149, -2.0 ** -126, 2.0 ** 127, 1e-45, True):
+        _, w = _route(m, x, 4, stream=st, scale=scale)
+        assert np.array_equal(w, np.full((3, 4), float(np.float32(np.float64(np.float32(scale)) / 4)), np.float32))
+    for scale in (1e-46, 0.0, float("inf"), 1e39):
+        with pytest.raises(ValueError, match="scale"):
+            _route(m, x, 4, stream=st, scale=scale)
+
+
 def test_route_strided_rows_and_streams(m):
     big = torch.randn(50, 200, generator=_gen(9)).to(DEV)
     view = big[:, 13:13 + 96]
