@@ -386,16 +386,19 @@ def moe_gate_pack(w, packed, stream=None) -> moe_gate_t:
 
 
 def moe_gate(gate: moe_gate_t, x, logits, stream=None):
-    """Router product: x BF16 [B, D] (rows may be strided) -> logits FP32 [B, E]."""
+    """Router product: x BF16 [B, D] (rows may be strided) -> logits FP32 [B, E].  gate: from moe_gate_pack; of a
+    moe_gate_t filled by hand, the caller sees to it that `packed` is on the GPU of x and stays alive."""
+    packed = getattr(gate, "tensor", None)
     if stream is None:
-        status = _dense.gate(ctypes.addressof(gate), gate.D, gate.E, x, logits)
+        status = _dense.gate(ctypes.addressof(gate), gate.D, gate.E, x, logits, packed)
         if status != _NOT_TAKEN:
             return _check("moe_gate", status)
     B = _matrix(x, "x")[0]
     if x.dtype != _BF16 or logits.dtype != _F32:
         _refuse("x: expected BF16, logits: FP32")
     ldx, ldl = _rows(x, "x", (B, gate.D)), _rows(logits, "logits", (B, gate.E))
-    _enqueue("moe_gate", lib.moe_gate, stream, (x, logits), gate, x.data_ptr(), ldx, B, logits.data_ptr(), ldl)
+    tensors = (x, logits) if packed is None else (x, logits, packed)
+    _enqueue("moe_gate", lib.moe_gate, stream, tensors, gate, x.data_ptr(), ldx, B, logits.data_ptr(), ldl)
 
 
 _SCORES = {"softmax": 0, "sigmoid": 1}

@@ -89,21 +89,22 @@ int type_of(PyObject* o) {
 }
 bool is(PyObject* o, at::ScalarType t) { return THPVariable_Unpack(o).scalar_type() == t; }
 
-// gate(handle address, D, E, x, logits)
-long gate(PyObject* const* v) {
+// gate(handle address, D, E, x, logits[, the tensor that holds the packed weight, or None])
+long gate(PyObject* const* v, Py_ssize_t n) {
   Call c;
   const void* h = PyLong_AsVoidPtr(v[0]);
   int64_t B = -1, D = PyLong_AsLongLong(v[1]), E = PyLong_AsLongLong(v[2]), ldx = 0, ldl = 0;
   void* x = c.matrix(v[3], B, D, ldx);
   void* out = c.matrix(v[4], B, E, ldl);
   c.need(c.ok && is(v[3], at::kBFloat16) && is(v[4], at::kFloat));
+  if (n > 5 && v[5] != Py_None) c.tensor(v[5]);
   void* st = c.stream();
   if (!c.ok) return kNotTaken;
   return g_gate(static_cast<const moe_gate_t*>(h), x, ldx, static_cast<int32_t>(B), static_cast<float*>(out), ldl, st);
 }
 
 // route(logits, ids, weights, score, bias, groups, topk_groups, group_score, renorm, scale)
-long route(PyObject* const* v) {
+long route(PyObject* const* v, Py_ssize_t) {
   Call c;
   int64_t B = -1, E = -1, K = -1, ldl = 0, ld = 0;
   void* logits = c.matrix(v[0], B, E, ldl);
@@ -128,7 +129,7 @@ long route(PyObject* const* v) {
 }
 
 // quant(x, codes, scales)
-long quant(PyObject* const* v) {
+long quant(PyObject* const* v, Py_ssize_t) {
   Call c;
   int64_t M = -1, K = -1, ldx = 0, ldc = 0;
   void* x = c.matrix(v[0], M, K, ldx);
@@ -142,7 +143,7 @@ long quant(PyObject* const* v) {
 }
 
 // linear(a, a_scales, w, w_scales, out, act, bias, add)
-long linear(PyObject* const* v) {
+long linear(PyObject* const* v, Py_ssize_t) {
   Call c;
   int64_t M = -1, K = -1, N = -1, lda = 0, ldw = 0, ldo = 0;
   const long act = PyLong_AsLong(v[5]);
@@ -168,11 +169,11 @@ long linear(PyObject* const* v) {
 
 // No exception leaves: a tensor without storage, say, is one that _lib.py has to explain.  (The library throws none,
 // so one means that it was not called.)
-template <long (*F)(PyObject* const*), int ARGS>
+template <long (*F)(PyObject* const*, Py_ssize_t), int ARGS, int MORE = 0>
 PyObject* entry(PyObject*, PyObject* const* args, Py_ssize_t n) {
   long r = kNotTaken;
   try {
-    if (n == ARGS && g_linear) r = F(args);
+    if (n >= ARGS && n <= ARGS + MORE && g_linear) r = F(args, n);
   } catch (...) {
     r = kNotTaken;
   }
@@ -197,7 +198,7 @@ PyObject* bind(PyObject*, PyObject* args) {
 }
 
 #define FAST(F) reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(F)), METH_FASTCALL, nullptr
-PyMethodDef methods[] = {{"gate", FAST((entry<gate, 5>))},
+PyMethodDef methods[] = {{"gate", FAST((entry<gate, 5, 1>))},
                          {"route", FAST((entry<route, 10>))},
                          {"quant", FAST((entry<quant, 3>))},
                          {"linear", FAST((entry<linear, 8>))},

@@ -222,6 +222,17 @@ def test_layer_objects_allocate_on_the_stream_they_run_on(monkeypatch):
     assert state.allocated == [here] * 2
 
 
+def test_gate_weight_on_another_gpu():
+    """The packed weight has to be where x and the logits are (here: on no GPU)."""
+    import types
+    g = m.moe_gate_t(16, 512, 0, 0x1000)
+    with pytest.raises(ValueError, match="must be on a GPU"):
+        m.moe_gate(g, _z(4, 512, dtype=BF), _z(4, 16))
+    g.tensor = types.SimpleNamespace(get_device=lambda: 1)
+    with pytest.raises(ValueError, match="must be on one GPU"):
+        m.moe_gate(g, _z(4, 512, dtype=BF), _z(4, 16))
+
+
 @pytest.mark.parametrize("scale", [0, -0.0, 1e-46, -7e-46, 1e39, float("inf"), float("nan")])
 def test_route_scale_is_taken_in_fp32(scale):
     """A scale that FP32 holds as 0 is none the library could tell from its default, 1."""

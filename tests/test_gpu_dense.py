@@ -254,6 +254,27 @@ def test_gate_rows_do_not_meet(m):
     assert not got[bad].isfinite().any() and torch.equal(got[~bad], want[~bad])
 
 
+@pytest.mark.parametrize("through", ["binding", "ctypes"])
+def test_gate_weight_elsewhere_is_refused(m, through):
+    """The packed weight is held to the GPU of x, on both ways into the library."""
+    import ctypes
+    st = None if through == "binding" else torch.cuda.current_stream()
+    h = m.moe_gate_pack(torch.ones(16, 512, device=DEV),
+                        torch.empty(m.moe_gate_packed_bytes(16, 512, F32), dtype=torch.uint8, device=DEV))
+    x, lg = torch.ones(4, 512, dtype=BF, device=DEV), torch.zeros(4, 16, device=DEV)
+    m.moe_gate(h, x, lg, stream=st)
+    assert (lg == 512).all()
+    lg.zero_()
+    packed, h.tensor = h.tensor, h.tensor.cpu()
+    assert m._lib._dense.gate(ctypes.addressof(h), 512, 16, x, lg, h.tensor) == -100
+    with pytest.raises(ValueError, match="one GPU"):
+        m.moe_gate(h, x, lg, stream=st)
+    assert not lg.any()
+    h.tensor = packed
+    assert m._lib._dense.gate(ctypes.addressof(h), 512, 16, x, lg, packed) == 0
+    assert (lg == 512).all()
+
+
 # --------------------------------------------------------------------- quant
 def _check_quant(m, x, ldx=0, ldc=0):
     M, K = x.shape
