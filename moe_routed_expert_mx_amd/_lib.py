@@ -10,6 +10,7 @@ from __future__ import annotations
 import ctypes
 import os
 import struct
+import warnings
 
 # PyTorch first: the library runs on torch's streams and memory, so it must bind to the
 # HIP runtime torch has loaded.  Loaded the other way round, the process holds two HIP
@@ -294,13 +295,28 @@ _current_device = torch._C._cuda_getDevice
 _current_stream = torch._C._cuda_getCurrentRawStream
 
 
+_NOT_TAKEN = -100
+
+
+class _NoBinding:
+    """In the native binding's place where that is not built: takes no call, so that each goes through ctypes."""
+
+    @staticmethod
+    def gate(*args) -> int:
+        return _NOT_TAKEN
+
+    route = quant = linear = gate
+
+
 def _load_binding():
-    """The native binding, bound to the library; it is built with it."""
+    """The native binding, bound to the library.  It makes calls shorter, no more: without it (a build of the HIP
+    library alone, or for another PyTorch) the package works, with a warning."""
     try:
         from . import _dense
     except ImportError as e:
-        raise ImportError(f"the native binding is not built ({e}): run `python moe_routed_expert_mx_amd/build.py` "
-                          "(or __graft_entry__.build()) first") from e
+        warnings.warn(f"the native binding is not built ({e}): calls of the dense side take some 5 us longer; "
+                      "`python moe_routed_expert_mx_amd/build.py` builds it", RuntimeWarning, stacklevel=2)
+        return _NoBinding
     addresses = [ctypes.cast(getattr(lib, f), ctypes.c_void_p).value
                  for f in ("moe_gate", "moe_route", "moe_quant_i8", "moe_linear_i8")]
     _dense.bind(*addresses, _current_stream, _current_device)
@@ -308,7 +324,6 @@ def _load_binding():
 
 
 _dense = _load_binding()
-_NOT_TAKEN = -100
 
 
 def _refuse(what: str):

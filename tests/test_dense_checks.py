@@ -222,6 +222,50 @@ def test_layer_objects_allocate_on_the_stream_they_run_on(monkeypatch):
     assert state.allocated == [here] * 2
 
 
+def test_package_works_without_the_native_binding(tmp_path):
+    """A tree with the HIP library alone imports, with a warning, and its calls go through ctypes."""
+    import os
+    import shutil
+    import subprocess
+    import sys
+    shutil.copytree(m._lib.HERE, tmp_path / "moe_routed_expert_mx_amd",
+                    ignore=shutil.ignore_patterns("_dense*", "__pycache__", "csrc", "*.tmp*"))
+    code = """if True:
+        import warnings
+        with warnings.catch_warnings(record=True) as seen:
+            warnings.simplefilter("always")
+            import moe_routed_expert_mx_amd as m
+        assert any("native binding" in str(w.message) for w in seen), seen
+        import torch
+        assert m.moe_plan_bytes(1, 512) > 0 and "site-packages" not in m.__file__
+        x = torch.zeros(4, 32)
+        try:
+            m.moe_quant_i8(x, x.to(torch.int8), x[:, 0].contiguous())
+        except ValueError as e:
+            assert "must be on a GPU" in str(e)
+            print("fine", m.__file__)
+    """
+    r = subprocess.run([sys.executable, "-c", code], cwd=tmp_path, env={**os.environ, "PYTHONPATH": str(tmp_path)},
+                       capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and f"fine {tmp_path}" in r.stdout, r.stderr
+
+
+def test_build_goes_on_without_the_native_binding(tmp_path, monkeypatch, capsys):
+    """... and leaves no binding of an older source behind."""
+    import importlib.util
+    import os
+    spec = importlib.util.spec_from_file_location("builder", os.path.join(m._lib.HERE, "build.py"))
+    b = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(b)
+    stale = tmp_path / "_dense.so"
+    stale.write_bytes(b"old")
+    monkeypatch.setattr(b, "BINDING", str(stale))
+    monkeypatch.setattr(b, "build_library", lambda verbose: "library")
+    monkeypatch.setenv("CXX", str(tmp_path / "no-such-compiler"))
+    assert b.build() == "library"
+    assert not stale.exists() and "native binding not built" in capsys.readouterr().err
+
+
 def test_gate_weight_on_another_gpu():
     """The packed weight has to be where x and the logits are (here: on no GPU)."""
     import types

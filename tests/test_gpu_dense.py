@@ -618,6 +618,28 @@ def test_native_binding_and_ctypes_agree(m):
         m.moe_route(lg, ids, wt, groups=7, topk_groups=1)       # 40 experts, 7 groups
 
 
+def test_without_the_native_binding(m, monkeypatch):
+    """Where the binding is not built, the same calls go through ctypes and give the same."""
+    g = _gen(43)
+    x, w = torch.randn(6, 512, generator=g).to(BF).to(DEV), torch.randn(40, 512, generator=g).to(DEV)
+    h = m.moe_gate_pack(w, torch.empty(m.moe_gate_packed_bytes(40, 512, F32), dtype=torch.uint8, device=DEV))
+    wq, ws = _codes((64, 512), g).to(DEV), torch.rand(64, generator=g).to(DEV)
+    res = []
+    for binding in (m._lib._dense, m._lib._NoBinding):
+        monkeypatch.setattr(m._lib, "_dense", binding)
+        lg, ids, wt = torch.empty(6, 40, device=DEV), torch.empty(6, 5, dtype=torch.int32, device=DEV), \
+            torch.empty(6, 5, device=DEV)
+        q, s, y = torch.empty(6, 512, dtype=torch.int8, device=DEV), torch.empty(6, device=DEV), \
+            torch.empty(6, 32, dtype=BF, device=DEV)
+        m.moe_gate(h, x, lg)
+        m.moe_route(lg, ids, wt)
+        m.moe_quant_i8(x, q, s)
+        m.moe_linear_i8(q, s, wq, ws, y, act="swiglu")
+        torch.cuda.synchronize()
+        res.append((lg, ids, wt, q, s, y))
+    assert all(torch.equal(p, r) for p, r in zip(*res))
+
+
 def test_native_binding_calls_once_or_not_at_all(m):
     """The library's status comes back as it is, after one call; a stream that is no handle means no call.  (The
     library's function is a stand-in that launches nothing.)"""
