@@ -398,11 +398,15 @@ typedef struct {
  *   with it); with groups, only the topk_groups best groups take part (group_score 1
  *   without a bias sums scores); ids = the topk largest choices, largest first;
  *   weight = score (renorm: / sum of the selected scores, 0 where that is 0) * scale.
- * Choices are compared in FP64 and ties go to the lowest index (of groups too), so ids do
- * not depend on rounding.  ids are always valid and distinct within a token: a logit of
- * -inf or NaN masks its expert (score 0, choice -inf; it is selected, lowest index first,
- * only when the others run out, with weight 0), and so does a NaN choice; logits of +inf
- * share a softmax's weight equally.  Weights are computed in FP64 and rounded once.
+ * Scores and choices are FP64, and ties go to the lowest index (of groups too).  Without a
+ * bias and summed groups ids depend on no rounding; with them, choices that lie closer than
+ * FP64 rounds them may stand either way.  ids are always valid and distinct within a token:
+ * a logit of -inf or NaN masks its expert (score 0, choice -inf), which is selected, lowest
+ * index first, only when the others run out, with weight 0.  A choice that the bias makes NaN
+ * or -inf comes last in the same way and adds nothing to its group; but the score stays what
+ * the logit makes it, so that such an expert, where it is selected, has its weight and counts
+ * in the sum.  Logits of +inf share a softmax's weight equally.  Weights are computed in FP64
+ * and rounded once.
  * 1 <= E <= 1024, 1 <= topk <= 64, topk <= E (with groups: <= topk_groups * E / groups),
  * MOE_EINVAL otherwise. */
 int moe_route(const void* logits_dev, int32_t type, int64_t ldl, int32_t B, int32_t E, int32_t topk,

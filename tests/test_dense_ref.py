@@ -33,6 +33,13 @@ def test_route_masked():
     assert w.tolist() == [[1, 0, 0], [0, 0, 0], [0.5, 0.5, 0]]
 
 
+def test_route_nan_or_infinite_bias_decides_but_does_not_weigh():
+    """The bias puts an expert last; its score stays, in its own weight and in the sum."""
+    for b in (np.nan, -np.inf):
+        ids, w = ref.route(np.zeros((1, 3)), 3, score="sigmoid", bias=[b, 0.0, 0.0])
+        assert ids.tolist() == [[1, 2, 0]] and np.allclose(w, 1 / 3, rtol=1e-15)
+
+
 def test_quant_worked_example():
     q, s = ref.quant(np.array([[0.0, 0.0, 0.0], [127.0, 0.5, -1.5], [254.0, 1.0, 3.0], [np.inf, 1.0, 0.0]]))
     assert q.tolist() == [[0, 0, 0], [127, 0, -2], [127, 0, 2], [0, 0, 0]]   # halves go to even

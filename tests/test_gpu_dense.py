@@ -149,6 +149,23 @@ def test_route_infinite_bias(m):
     _check_route(m, torch.randn(5, 20, generator=_gen(1)), 4, bias=b, groups=5, topk_groups=2, group_score="top2")
 
 
+@pytest.mark.parametrize("B", [5, 4500])
+@pytest.mark.parametrize("o", [dict(), dict(renorm=False), dict(score="sigmoid"),
+                               dict(score="sigmoid", groups=4, topk_groups=4, group_score="top2"),
+                               dict(groups=4, topk_groups=3)])
+def test_route_selects_experts_whose_bias_is_not_finite(m, B, o):
+    """Experts with a bias of NaN or -inf come last, among them the masked ones, by index; selected, they keep the weight
+    that their score gives them."""
+    log(f"route nan bias B={B} {o}")
+    E = 16
+    g = _gen(B)
+    b = torch.randn(E, generator=g) * 0.1
+    b[1], b[6], b[15] = float("nan"), -float("inf"), float("nan")
+    x = torch.randn(B, E, generator=g)
+    x[1, 3], x[2, 6], x[3, ::2] = -float("inf"), float("nan"), -float("inf")
+    _check_route(m, x, 12 if o.get("topk_groups") == 3 else E, bias=b, **o)
+
+
 @pytest.mark.parametrize("through", ["binding", "ctypes"])
 def test_route_scales_near_the_ends_of_fp32(m, through):
     st = None if through == "binding" else torch.cuda.current_stream()
