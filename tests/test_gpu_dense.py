@@ -142,6 +142,21 @@ def test_route_many_tokens(m, E, K, o):
     _check_route(m, x, K, **o)
 
 
+@pytest.mark.parametrize("E,K,o", [(48, 8, dict(groups=6, topk_groups=2)), (160, 16, dict(bias=True)), (250, 64, dict()),
+                                   (170, 5, dict(groups=17, topk_groups=3, bias=True)), (300, 7, dict(score="sigmoid")),
+                                   (1023, 20, dict(groups=33, topk_groups=4, group_score="top2"))])
+@pytest.mark.parametrize("dtype", [BF, F16, F32])
+def test_route_many_tokens_each_type(m, E, K, o, dtype):
+    """Beyond 4096 tokens: 16 lanes a token in their three sizes, and 64 for more experts or groups than those take."""
+    log(f"route 4111x{E} {o} {dtype}")
+    o, g = dict(o), _gen(E)
+    if o.pop("bias", False):
+        o["bias"] = torch.randn(E, generator=g) * 0.1
+    x = (torch.randn(4111, E, generator=g) * 2).to(dtype)
+    x[::9, ::2] = -float("inf")
+    _check_route(m, x, K, **o)
+
+
 def test_route_infinite_bias(m):
     b = torch.zeros(20)
     b[7], b[3] = float("inf"), float("inf")
@@ -234,6 +249,18 @@ def test_gate_whole_numbers_are_exact(m, B, E, D, wtype):
     assert torch.equal(_gate(m, x, w, ld=D + 64, out_ld=E + 3), want)
 
 
+@pytest.mark.parametrize("B,E", [(600, 160), (1300, 161), (2601, 160), (5000, 100), (8191, 159)])
+@pytest.mark.parametrize("D", [1536, 3584])
+@pytest.mark.parametrize("wtype", [BF, F32])
+def test_gate_tiles_with_long_rows(m, B, E, D, wtype):
+    """Each larger tile with more features to a wave than it has in flight, and with unequal shares."""
+    log(f"gate long rows {B}x{E}x{D} {wtype}")
+    g = _gen(B + E + D)
+    x = torch.randint(-8, 9, (B, D), generator=g).to(BF)
+    w = torch.randint(-100, 101, (E, D), generator=g).to(wtype)
+    assert torch.equal(_gate(m, x, w, out_ld=E + 1), x.double() @ w.double().T)
+
+
 def test_gate_fp32_weight_keeps_all_its_bits(m):
     """One feature a token: the logits are the FP32 weights themselves times a power of two."""
     g = _gen(3)
@@ -316,6 +343,15 @@ def test_quant_sizes(m, M, K, ldx, ldc, dtype):
     g = _gen(M + K)
     _check_quant(m, (torch.randn(M, K, generator=g) * torch.exp2(torch.randint(-6, 7, (M, 1), generator=g))).to(dtype),
                  ldx, ldc)
+
+
+@pytest.mark.parametrize("K,ldx,ldc", [(250, 0, 0), (257, 0, 3), (1021, 3, 0), (1032, 0, 0), (2040, 8, 8), (2050, 0, 0),
+                                       (4090, 0, 0), (4097, 1, 1)])
+@pytest.mark.parametrize("dtype", [BF, F16, F32])
+def test_quant_many_tokens(m, K, ldx, ldc, dtype):
+    """A wave a token, 1 to 8 pieces a lane, and rows too long for that."""
+    log(f"quant 1027x{K}+{ldx} {dtype}")
+    _check_quant(m, torch.randn(1027, K, generator=_gen(K)).to(dtype), ldx, ldc)
 
 
 @pytest.mark.parametrize("dtype", [BF, F16, F32])
@@ -426,6 +462,22 @@ def test_linear_tiles(m, M, N, K, act):
     _check_linear(m, M, N, K, act=act, out=BF, bias=True, add=True, seed=1)
     pad = 16 if K % 16 == 0 else 1
     _check_linear(m, M, N, K, act=act, out=F32 if M < 2000 else F16, lda=pad, ldw=2 * pad, ldo=3, offset=pad, seed=2)
+
+
+# The streaming kernel's variants by the launch rule: 16, 32 and 64 tokens a block; one row tile (up to 256 blocks,
+# the first size of a pair) and two; aligned and unaligned rows (K or K + 1), with more than 64 tokens too.  M, N and
+# K leave a remainder in each; K = 9008 gives each wave more pieces than it has in flight, 272 leaves most waves none.
+STREAM = [(11, 100), (11, 4114), (24, 100), (24, 4114), (50, 100), (50, 4130), (70, 258), (500, 770), (130, 2070)]
+
+
+@pytest.mark.parametrize("M,N", STREAM)
+@pytest.mark.parametrize("K", [272, 273, 9008, 9009])
+@pytest.mark.parametrize("act", ["none", "swiglu"])
+def test_linear_streaming_variants(m, M, N, K, act):
+    if M > 100 and K > 1000:
+        K -= 7008
+    _check_linear(m, M, N, K, act=act, out=(BF, F32)[K % 2], bias=K % 2 == 0, add=True, seed=5)
+    _check_linear(m, M, N, K, act=act, out=F16, bias=K % 2 == 1, lda=16, ldw=32, offset=16, ldo=1, seed=6)
 
 
 # a single row in the last tile of each size, plain (64 x 64, 64 x 128, 128 x 128, 128 x 256, 256 x 256) and SwiGLU
