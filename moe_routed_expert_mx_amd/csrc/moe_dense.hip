@@ -358,10 +358,11 @@ __global__ __launch_bounds__(256) void route_kernel(RouteArgs a) {
 // The quick way adds 1.5 * 2^23 to x * inv in one rounding, inv = 127 / amax rounded up by a step or
 // two: the sum's low byte is the code, unless the exact quotient is (16-bit types) or may be
 // (FP32) a half.
-//   BF16, FP16: a quotient q that is no half lies q 2^-18 or more from one (254 x - (2 k + 1) amax
-// is a whole number of x's last places), inv's error moves it by q 2^-22 at most.  A half, (2 k + 1)
-// amax = 254 x, needs 127 to divide amax's significand, or 2 k + 1 = 127, x = amax / 2, code 64:
-// inv being high, that one comes out right.
+//   BF16, FP16: with significands of at most 11 bits, X and A, x / amax = X / (A 2^j).  A quotient q that
+// is no half lies |254 X - (2 k + 1) A 2^j| / (A 2^(j + 1)) from k + 1/2, the numerator being 1 or
+// more: q / (254 X), above q 2^-19 (closest: A = 2033, X = 2025, j = 0).  inv's error moves q by
+// q 2^-22 at most.  A half, (2 k + 1) amax = 254 x, needs 127 to divide amax's significand, or
+// 2 k + 1 = 127, x = amax / 2, code 64: inv being high, that one comes out right.
 //   FP32: within 2^-14 of a half, the exact way decides.
 // Rows with an amax that 127 divides (16-bit types), or below 2^-100, go the exact way: by the
 // remainder x * 127 - r * amax in FP64, x and amax first scaled by a power of two.

@@ -395,6 +395,19 @@ def test_quant_every_mantissa(m, dtype):
     _check_quant(m, x)
 
 
+@pytest.mark.parametrize("dtype", [BF, F16])
+def test_quant_every_pair_of_significands(m, dtype):
+    """amax of every significand, x of every one up to it and in the binade below: among them the quotient nearest
+    to a half, FP16's 2025 * 127 / 2033, off it by 2^-18.97 of itself."""
+    n = 2 ** (7 if dtype == BF else 10)
+    sig = torch.arange(n, 2 * n)
+    same = torch.where(sig[None, :] <= sig[:, None], sig[None, :], 0)
+    x = torch.cat([sig[:, None], same, -(sig / 2).expand(n, -1)], dim=1)
+    assert dtype == BF or x[2033 - n, 1 + 2025 - n] == 2025
+    _check_quant(m, x.to(dtype))
+    _check_quant(m, (x / n).to(dtype)[:1000])          # few tokens: four waves each
+
+
 # -------------------------------------------------------------------- linear
 def _codes(shape, g):
     return torch.randint(-128, 128, shape, generator=g).to(torch.int8)
