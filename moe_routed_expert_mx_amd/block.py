@@ -55,6 +55,7 @@ class Router:
         n = _lib.moe_gate_packed_bytes(self.E, self.D, w.dtype)
         if n == 0:
             raise ValueError("unsupported shape or type of the router's weight")
+        self.device = w.device  # with its index: "cuda" would mean another GPU where another is current
         self.packed = torch.empty(n, dtype=torch.uint8, device=self.device)
         self.gate = _lib.moe_gate_pack(w, self.packed)
         self.bias = None if bias is None else torch.as_tensor(bias).to(self.device, torch.float32).contiguous()
@@ -82,6 +83,7 @@ class SharedExpertI8:
         self.device, self.B_max = torch.device(device), int(B_max)
         self.w13, self.w2 = (torch.as_tensor(t).to(self.device, torch.int8).contiguous() for t in (w13, w2))
         self.s13, self.s2 = (torch.as_tensor(t).to(self.device, torch.float32).contiguous() for t in (s13, s2))
+        self.device = self.w2.device  # with its index: "cuda" would mean another GPU where another is current
         self.D, self.I = map(int, self.w2.shape)
         if self.w13.shape != (2 * self.I, self.D) or self.s13.shape != (2 * self.I,) or self.s2.shape != (self.D,):
             raise ValueError("shared expert: weights or scales of the wrong shape")

@@ -838,6 +838,18 @@ def test_shared_expert_twice_with_other_batches(m):
         sh.forward(torch.zeros(101, 512, dtype=BF, device=DEV))
 
 
+def test_objects_keep_the_gpu_they_were_made_on(m):
+    """... by its index, so that a call allocates there whichever GPU is current by then."""
+    from moe_routed_expert_mx_amd.block import Router, SharedExpertI8
+    here = torch.device("cuda", torch.cuda.current_device())
+    router = Router(torch.ones(16, 512), topk=2, B_max=4)
+    shared = SharedExpertI8(torch.ones(64, 512, dtype=torch.int8), torch.ones(64), torch.ones(512, 32, dtype=torch.int8),
+                            torch.ones(512), B_max=4)
+    assert router.device == here and shared.device == here
+    x = torch.zeros(4, 512, dtype=BF, device=DEV)
+    assert [t.device for t in (*router.forward(x), shared.forward(x))] == [here] * 3
+
+
 @pytest.mark.parametrize("raw", [False, True])
 @pytest.mark.parametrize("B", [3, 40])
 def test_block_on_a_side_stream(m, B, raw):
