@@ -79,9 +79,10 @@ class Router:
 
 class SharedExpertI8:
     def __init__(self, w13, s13, w2, s2, *, B_max: int, device="cuda"):
-        """w13 int8 [2I, D] (gate rows, then up rows) with FP32 scales [2I], w2 int8 [D, I] with scales [D]."""
+        """w13 int8 [2I, D] (gate rows, then up rows) with FP32 scales [2I], w2 int8 [D, I] with scales [D].  Codes of
+        another type are taken where int8 holds them; quantize() takes weights that are not codes yet."""
         self.device, self.B_max = torch.device(device), int(B_max)
-        self.w13, self.w2 = (torch.as_tensor(t).to(self.device, torch.int8).contiguous() for t in (w13, w2))
+        self.w13, self.w2 = (self._codes(t).to(self.device).contiguous() for t in (w13, w2))
         self.s13, self.s2 = (torch.as_tensor(t).to(self.device, torch.float32).contiguous() for t in (s13, s2))
         self.device = self.w2.device  # with its index: "cuda" would mean another GPU where another is current
         self.D, self.I = map(int, self.w2.shape)
@@ -91,6 +92,16 @@ class SharedExpertI8:
         self.codes = torch.empty(B, max(self.D, self.I), dtype=torch.int8, device=self.device)
         self.scales = torch.empty(B, device=self.device)
         self.hidden = torch.empty(B, self.I, dtype=torch.bfloat16, device=self.device)
+
+    @staticmethod
+    def _codes(t) -> torch.Tensor:
+        t = torch.as_tensor(t)
+        if t.dtype == torch.int8:
+            return t
+        codes = t.to(torch.int8)
+        if not ((t >= -128) & (t <= 127) & (codes.to(t.dtype) == t)).all():
+            raise ValueError(f"shared expert: weights of {t.dtype} that are no int8 codes (see quantize)")
+        return codes
 
     @classmethod
     def quantize(cls, w13, w2, *, B_max: int, device="cuda") -> "SharedExpertI8":

@@ -266,6 +266,25 @@ def test_build_goes_on_without_the_native_binding(tmp_path, monkeypatch, capsys)
     assert not stale.exists() and "native binding not built" in capsys.readouterr().err
 
 
+def test_shared_expert_takes_codes_only():
+    """Weights that int8 does not hold are refused, not cut to it."""
+    from moe_routed_expert_mx_amd.block import SharedExpertI8
+    g = torch.Generator().manual_seed(0)
+    w13, w2 = (torch.randint(-128, 128, s, generator=g) for s in ((64, 512), (512, 32)))
+
+    def make(a, b):
+        return SharedExpertI8(a, torch.ones(64), b, torch.ones(512), B_max=4, device="cpu")
+
+    for t in (torch.int8, torch.int32, F32):
+        e = make(w13.to(t), w2.to(t).numpy())
+        assert e.w13.dtype == torch.int8 and torch.equal(e.w13.long(), w13) and torch.equal(e.w2.long(), w2)
+    for bad in (w13 + 0.25, w13 * 1000, w13 * float("nan"), torch.full((64, 512), 128), w13.to(torch.int8).view(torch.uint8)):
+        with pytest.raises(ValueError, match="int8"):
+            make(bad, w2)
+    with pytest.raises(ValueError, match="int8"):
+        make(w13, w2 * 0.01)
+
+
 def test_gate_weight_on_another_gpu():
     """The packed weight has to be where x and the logits are (here: on no GPU)."""
     import types
