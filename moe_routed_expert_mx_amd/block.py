@@ -99,7 +99,7 @@ class SharedExpertI8:
         if t.dtype == torch.int8:
             return t
         codes = t.to(torch.int8)
-        if not ((t >= -128) & (t <= 127) & (codes.to(t.dtype) == t)).all():
+        if not torch.equal(codes.double(), t.double()):
             raise ValueError(f"shared expert: weights of {t.dtype} that are no int8 codes (see quantize)")
         return codes
 

@@ -278,6 +278,8 @@ def test_shared_expert_takes_codes_only():
     for t in (torch.int8, torch.int32, F32):
         e = make(w13.to(t), w2.to(t).numpy())
         assert e.w13.dtype == torch.int8 and torch.equal(e.w13.long(), w13) and torch.equal(e.w2.long(), w2)
+    half = w13.abs().clamp_max(127).to(torch.uint8)
+    assert torch.equal(make(half, w2).w13.long(), half.long())
     for bad in (w13 + 0.25, w13 * 1000, w13 * float("nan"), torch.full((64, 512), 128), w13.to(torch.int8).view(torch.uint8)):
         with pytest.raises(ValueError, match="int8"):
             make(bad, w2)
