@@ -857,13 +857,13 @@ __device__ __forceinline__ void dma16(v4i rsrc, uint32_t voff, uint32_t soff, ui
   asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds"
                :
                : "s"(lds), "v"(voff), "s"(rsrc), "s"(soff)
-               : "memory");
+               : "m0", "memory");
 }
 __device__ __forceinline__ void dma4(v4i rsrc, uint32_t voff, uint32_t lds) {  // 4 bytes a lane
   asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dword %1, %2, 0 offen lds"
                :
                : "s"(lds), "v"(voff), "s"(rsrc)
-               : "memory");
+               : "m0", "memory");
 }
 __device__ __forceinline__ v4i make_rsrc(const void* base, uint32_t bytes) {
   const uint64_t b = reinterpret_cast<uint64_t>(base);
