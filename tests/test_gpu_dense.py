@@ -891,3 +891,34 @@ def test_block_on_a_side_stream(m, B, raw):
     y = block.forward(x, stream=torch.cuda.default_stream().cuda_stream if raw else torch.cuda.default_stream())
     torch.cuda.synchronize()
     assert torch.equal(y, want[0])
+
+
+@pytest.mark.parametrize("B", [3, 40])
+def test_block_captured_and_replayed(m, B):
+    """The whole layer in a graph, by the current stream and by the capturing stream's name; replays with new inputs
+    and eager calls of the same object between them."""
+    import workloads
+    from moe_routed_expert_mx_amd.block import MoeBlock, Router, SharedExpertI8
+    from moe_routed_expert_mx_amd.layer import MoeLayer
+    log(f"block captured B={B}")
+    d = workloads.generate(workloads.custom(B=B, E=24, K=4, D=512, I=64, seed=B + 9))
+    g = _gen(B)
+    router = Router(torch.randn(24, 512, generator=g) / 22, topk=4, B_max=48)
+    layer = MoeLayer(d["w13"], d["s13"], d["w2"], d["s2"], B_max=48, topk=4, device=DEV)
+    shared = SharedExpertI8.quantize(torch.randn(2 * 96, 512, generator=g) / 22, torch.randn(512, 96, generator=g) / 10,
+                                     B_max=48)
+    block = MoeBlock(router, layer, shared)
+    x = torch.randn(B, 512, generator=g).to(BF).to(DEV)
+    block.forward(x)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        y1 = block.forward(x)
+        y2 = block.forward(x, stream=torch.cuda.current_stream())
+    for _ in range(4):
+        x.copy_(torch.randn(B, 512, generator=g).to(BF))
+        want = block.forward(x)
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(y1, want) and torch.equal(y2, want)
