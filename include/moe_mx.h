@@ -354,8 +354,8 @@ enum moe_dtype { MOE_BF16 = 0, MOE_F16 = 1, MOE_F32 = 2 };
 
 /* Bytes of the router weight [E, D] laid out by moe_gate_pack, E padded to a multiple of 16:
  * wtype MOE_BF16 as it is, MOE_F32 in three BF16 planes, the upper, middle and lower eight
- * significant bits of a weight.  0 on invalid sizes (1 <= E <=
- * 1024, 512 <= D <= 16384 with D % 512 == 0, as the experts). */
+ * significant bits of a weight.  0 on invalid sizes (1 <= E <= 1024, 512 <= D <= 16384 with
+ * D % 512 == 0, as the experts). */
 size_t moe_gate_packed_bytes(int32_t E, int32_t D, int32_t wtype);
 
 /* One-time re-layout of a router weight, row-major [E, D] of wtype, into the order
@@ -371,10 +371,11 @@ typedef struct {
 } moe_gate_t;
 
 /* Router product: logits[t, e] = sum over d of x[t, d] * w[e, d], FP32 sums of exact
- * products, in an order that the sizes alone decide (an FP32 weight counts as the sum of its upper, middle and lower
- * eight significant bits; below 2^-100 in magnitude it loses those under 2^-133).  x_dev BF16 [B, D], ldx >= D and a multiple of 8, x_dev
- * 16-byte aligned; logits_dev FP32 [B, E], ldl >= E.   The logits of a token
- * with an infinite or NaN feature are not finite (with an FP32 weight: NaN).
+ * products, in an order that the sizes alone decide (an FP32 weight counts as the sum of its
+ * upper, middle and lower eight significant bits; below 2^-100 in magnitude it loses those
+ * under 2^-133).  x_dev BF16 [B, D], ldx >= D and a multiple of 8, x_dev 16-byte aligned;
+ * logits_dev FP32 [B, E], ldl >= E.  The logits of a token with an infinite or NaN feature
+ * are not finite (with an FP32 weight: NaN).
  * MOE_EINVAL for a null pointer, size, stride or alignment outside these. */
 int moe_gate(const moe_gate_t* gate, const void* x_dev, int64_t ldx, int32_t B, float* logits_dev,
              int64_t ldl, void* stream);
@@ -437,9 +438,10 @@ typedef struct {
  *   act 1: y[m, n] = silu(y[m, n]) * y[m, N/2 + n];   out = y + add, rounded once
  * The sum is exact (32-bit integers), the rest is FP32.  a_dev int8 [M, K] (lda >= K), w_dev
  * int8 [N, K] (ldw >= K), out_dev [M, N or N/2] of out_type (ldo).  All 256 codes are taken
- * at their value.  Rows whose start is 16-byte aligned with K % 16 == 0 (a_dev, w_dev,
- * lda, ldw) are read the fast way; others as the aligned 4-byte words that hold their bytes.  1 <= N <= 2^20, M * N <= 2^34, 1 <= K <=
- * 131071 (the sum's range), lda and ldw < 2^22; MOE_EINVAL otherwise. */
+ * at their value.  Rows whose start is 16-byte aligned with K % 16 == 0 (a_dev, w_dev, lda,
+ * ldw) are read the fast way; others as the aligned 4-byte words that hold their bytes.
+ * 1 <= N <= 2^20, M * N <= 2^34, 1 <= K <= 131071 (the sum's range), lda and ldw < 2^22;
+ * MOE_EINVAL otherwise. */
 int moe_linear_i8(const int8_t* a_dev, int64_t lda, const float* a_scales_dev, const int8_t* w_dev,
                   int64_t ldw, const float* w_scales_dev, int32_t M, int32_t N, int32_t K,
                   const moe_linear_opts_t* opts, void* out_dev, int32_t out_type, int64_t ldo,

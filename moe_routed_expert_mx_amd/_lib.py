@@ -314,7 +314,7 @@ def _load_binding():
     try:
         from . import _dense
     except ImportError as e:
-        warnings.warn(f"the native binding is not built ({e}): calls of the dense side take some 5 us longer; "
+        warnings.warn(f"the native binding is not built ({e}): calls of the dense side take 5 to 8 us instead of 3; "
                       "`python moe_routed_expert_mx_amd/build.py` builds it", RuntimeWarning, stacklevel=2)
         return _NoBinding
     addresses = [ctypes.cast(getattr(lib, f), ctypes.c_void_p).value

@@ -165,10 +165,13 @@ __device__ __forceinline__ double exp_f64(double x) {
 // LPT lanes per token, lane l of them holding experts l, l + LPT, ..., NV of them at most.  Each
 // lane sorts its choices (stably, so that equal ones stay in index order) into LDS; then the
 // lanes' heads compete topk times: the largest upper word by rotations among the lanes, and
-// only where several lanes share it the lower word and the index.  Vector instructions bound it (some
-// 350 a token with groups), and the choice in FP64 is a small part of them: a contest in FP32
-// first, FP64 only for waves whose result it cannot tell, was no faster (16384 tokens with bias
-// and groups 23 us against 20.7) and much slower for few tokens, whose slowest wave counts.
+// only where several lanes share it the lower word and the index.  For many tokens vector
+// instructions bound it (463 a token with 160 experts in 10 groups, top 16: 20.4 us for 16384
+// tokens), and in part LDS: the ranking of groups reads runs of experts that lie on the same banks
+// (69 % of the LDS cycles are conflicts).  The choice in FP64 is a small part of the instructions: a
+// contest in FP32 first, FP64 only for waves whose result it cannot tell, was no faster (16384
+// tokens with bias and groups 23 us against 20.7) and much slower for few tokens, whose slowest
+// wave counts.
 template <int TYPE, int LPT, int NV>
 __global__ __launch_bounds__(256) void route_kernel(RouteArgs a) {
   constexpr int TPW = 64 / LPT;
@@ -1228,7 +1231,9 @@ int launch_route(const RouteArgs& a, hipStream_t st) {
 template <int TYPE>
 int launch_route(const RouteArgs& a, hipStream_t st) {
   // 16 lanes a token do less work in all, 64 finish a token sooner (160 experts, top 16, bias: 4096
-  // tokens 9.5 against 9.2 us, 6000 11.2 against 11.4, 16384 16.4 against 23)
+  // tokens 9.5 against 9.2 us, 6000 11.2 against 11.4, 16384 16.4 against 23).  A lane's list is sorted in a number of
+  // steps that grows with the square of its room, hence three sizes of it (16384 tokens, top 8, bias: 64 experts
+  // with room for 4 a lane 7.6 us; for 10 and for 16: 72 experts 11.4 and 18.3, 128 13.1 and 20.2, 160 14.3 and 21.7)
   if (a.B > 4096 && a.E <= 256 && a.groups <= 16) {
     if (a.E <= 64) return launch_route<TYPE, 16, 4>(a, st);
     if (a.E <= 160) return launch_route<TYPE, 16, 10>(a, st);
@@ -1290,7 +1295,7 @@ int launch_gate(const GateArgs& a, hipStream_t st) {
   // Rounds of tiles over 256 CUs, weighed with a tile's time (BF16 and FP32 weight): small tiles
   // fill the CUs, large ones read less.  The weights are fitted to 1 to 8192 tokens, 32 to 250
   // experts, 1024 to 5120 features, where the tile chosen is on average 4 % (BF16) and 2 % (FP32)
-  // slower than the best of thirteen.
+  // slower than the best of thirteen (at worst by a third: 2600 tokens with 250 experts).
   const int64_t tiles = (a.E + 15) / 16;
   auto cost = [&](int tt, int et, int bf16, int f32) {
     return ((a.B + 16 * tt - 1) / (16 * tt) * ((tiles + et - 1) / et) + 255) / 256 * (P == 3 ? f32 : bf16);
