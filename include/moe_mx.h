@@ -447,6 +447,105 @@ int moe_linear_i8(const int8_t* a_dev, int64_t lda, const float* a_scales_dev, c
                   const moe_linear_opts_t* opts, void* out_dev, int32_t out_type, int64_t ldo,
                   void* stream);
 
+/* ------------------------------------------------- block-scaled FP8 ---- */
+/* The layer in 8-bit floating point: e4m3 codes (OCP; largest 448) with an FP32 scale for each
+ * block of 128 consecutive k of a row (the last block of a row may be shorter; KB = ceil(K / 128)),
+ * weights with one for each 128 rows of such a block.  A code times its scale stands for a value.
+ * Conventions as the dense side's: no state, 64-bit offsets, outputs must not overlap inputs
+ * unless said otherwise. */
+
+/* Quantization into blocks: x [M, K] (moe_dtype, ldx >= K) -> codes_dev [M, K] (ldc >= K),
+ * scales_dev FP32 [M, KB] (lds >= KB).  scale = 2^e, e the smallest integer >= -126 with amax *
+ * 2^-e <= 448 (as the MXFP8 plan's); code = e4m3 of x * 2^-e, which is exact, half to even.  A
+ * block of zeros has scale 0; one with an infinity or NaN scale NaN and codes 0, so that
+ * what is computed from it is NaN.  Bytes of codes_dev between K and ldc are left as they were.
+ * 1 <= K <= 131072. */
+int moe_quant_f8(const void* x_dev, int32_t type, int64_t ldx, int32_t M, int32_t K, uint8_t* codes_dev,
+                 int64_t ldc, float* scales_dev, int64_t lds, void* stream);
+
+/* Codes that moe_rms_norm writes. */
+enum moe_codes { MOE_CODES_NONE = 0, MOE_CODES_I8 = 1, MOE_CODES_E4M3 = 2 };
+
+/* Options of moe_rms_norm (zero-initialise for the defaults). */
+typedef struct {
+  double eps;
+  const void* residual_dev; /* optional [M, K] of x's type (ldr): added to x */
+  int64_t ldr;
+  void* total_dev;          /* optional [M, K] of x's type (ldt): x + residual; may be residual_dev or x_dev
+                               itself with the same row distance */
+  int64_t ldt;
+  void* out_dev;            /* optional [M, K] of x's type (ldo): the norm; may be x_dev or residual_dev
+                               itself with the same row distance (but not total_dev) */
+  int64_t ldo;
+  int32_t codes;            /* moe_codes */
+  int32_t reserved;
+  void* codes_dev;          /* [M, K] bytes (ldc) */
+  int64_t ldc;
+  float* scales_dev;        /* MOE_CODES_I8: [M]; MOE_CODES_E4M3: [M, KB] (lds) */
+  int64_t lds;
+} moe_norm_opts_t;
+
+/* Root-mean-square norm, with the residual's addition before it and codes in 8 bits after it:
+ *   h = x + residual, rounded to x's type (total);
+ *   r = 1 / sqrt(sum over k of h[k]^2 / K + eps), in FP64, rounded to FP32 once;
+ *   y = (h * r) * weight, in FP32;   out = y rounded to x's type;
+ *   codes and scales of y: as moe_quant_i8 makes them of an FP32 row, or as moe_quant_f8 does.
+ * x_dev [M, K] (moe_dtype, ldx >= K); weight_dev [K] of wtype, MOE_F32 or x's type.  One of out
+ * and codes at least.  1 <= K <= 16384, eps >= 0 and finite; MOE_EINVAL otherwise. */
+int moe_rms_norm(const void* x_dev, int32_t type, int64_t ldx, int32_t M, int32_t K, const void* weight_dev,
+                 int32_t wtype, const moe_norm_opts_t* opts, void* stream);
+
+/* Product of block-scaled e4m3 matrices:
+ *   y[m, n] = sum over blocks b of a_scales[m, b] * w_scales[n / 128, b] * (sum over k in b of
+ *             a[m, k] * w[n, k]) + bias[n];   act 1: y[m, n] = silu(y[m, n]) * y[m, N/2 + n];
+ *   out = y + add, rounded once;   sums and scales in FP32, in an order that the sizes decide.
+ * Products of codes are exact; for outputs in 16 bits the matrix cores then cut each at 2^-13 of the
+ * largest of its eight neighbours along k (some 1.5e-5 of a sum), for FP32 outputs they do not.
+ * a_dev [M, K] (lda), a_scales_dev FP32 [M, KB] (ldsa >= KB); w_dev [N, K] (ldw), w_scales_dev FP32
+ * [NB, KB], contiguous: NB = ceil(N / 128), with act 1 NB = 2 ceil(N/2 / 128), as the gate rows (0 ..
+ * N/2 - 1) and the up rows have blocks of their own.  out_dev [M, N or N/2] of out_type (ldo).
+ * opts as moe_linear_i8's.  16-byte alignment of a_dev, w_dev, lda and ldw, K % 16 == 0.
+ * 1 <= N <= 2^20, M * N <= 2^34, 16 <= K <= 65536, lda, ldw and ldsa < 2^22; MOE_EINVAL otherwise. */
+int moe_linear_f8(const uint8_t* a_dev, int64_t lda, const float* a_scales_dev, int64_t ldsa, const uint8_t* w_dev,
+                  int64_t ldw, const float* w_scales_dev, int32_t M, int32_t N, int32_t K,
+                  const moe_linear_opts_t* opts, void* out_dev, int32_t out_type, int64_t ldo, void* stream);
+
+/* Bytes of the workspace of moe_lists for R = B * topk routes over E experts: 0 where it needs none
+ * (up to 8192 routes), and on invalid sizes. */
+size_t moe_lists_ws_bytes(int64_t R, int32_t E);
+
+/* Routes sorted by expert: ids i32 [R] (routes t * topk + s in their order) -> offsets_dev i32
+ * [E + 1], where each expert's routes begin, and pairs_dev i32 [R]: the routes, ascending
+ * within an expert.  Ids outside [0, E) are left out (experts that another rank holds);
+ * pairs behind offsets[E] are -1.  An id may repeat within a token.  1 <= R <= 2^26, 1 <= E <= 1024.
+ * Calls that share a workspace must be ordered. */
+int moe_lists(const int32_t* ids_dev, int64_t R, int32_t E, int32_t* offsets_dev, int32_t* pairs_dev, void* ws_dev,
+              size_t ws_bytes, void* stream);
+
+/* Options of moe_grouped_f8 (zero-initialise for the defaults). */
+typedef struct {
+  int32_t act;              /* as moe_linear_opts_t */
+  int32_t gather;           /* 0: row i is a[i]; g > 0: a[pairs[i] / g] */
+  int32_t scatter;          /* 0: its result is out[i]; 1: out[pairs[i]] */
+  int32_t reserved;
+  const int32_t* pairs_dev; /* i32 [R], from moe_lists; NULL without gather and scatter */
+} moe_grouped_opts_t;
+
+/* Products grouped by expert: rows i = offsets[e] .. offsets[e + 1] - 1 are multiplied with expert
+ * e's weight, as moe_linear_f8 does.
+ *   a_dev [a_rows, K], a_scales_dev FP32 [a_rows, KB] (lda, ldsa); w_dev [E, N, K] (ldw between
+ *   rows, ldwe between experts), w_scales_dev FP32 [E, NB, KB], contiguous; offsets_dev i32 [E + 1],
+ *   ascending; R the most rows that they may hold; out_dev [out_rows, N or N/2] (ldo).
+ * Without gather a_rows >= R, without scatter out_rows >= R.  Rows behind offsets[E], and those whose
+ * pair names no row of a or out, are left as they were; offsets outside 0 .. R are cut to it.
+ * With gather a_rows * lda < 2^31.  1 <= E <= 1024, 1 <= R <= 2^26, R * N <= 2^40; other limits as
+ * moe_linear_f8's. */
+int moe_grouped_f8(const uint8_t* a_dev, int64_t lda, const float* a_scales_dev, int64_t ldsa, int64_t a_rows,
+                   const uint8_t* w_dev, int64_t ldw, int64_t ldwe, const float* w_scales_dev,
+                   const int32_t* offsets_dev, int64_t R, int32_t E, int32_t N, int32_t K,
+                   const moe_grouped_opts_t* opts, void* out_dev, int32_t out_type, int64_t ldo, int64_t out_rows,
+                   void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -59,6 +59,19 @@ class moe_linear_opts_t(ctypes.Structure):
                 ("add_dev", ctypes.c_void_p), ("ldadd", ctypes.c_int64)]
 
 
+class moe_norm_opts_t(ctypes.Structure):
+    _fields_ = [("eps", ctypes.c_double), ("residual_dev", ctypes.c_void_p), ("ldr", ctypes.c_int64),
+                ("total_dev", ctypes.c_void_p), ("ldt", ctypes.c_int64), ("out_dev", ctypes.c_void_p),
+                ("ldo", ctypes.c_int64), ("codes", ctypes.c_int32), ("reserved", ctypes.c_int32),
+                ("codes_dev", ctypes.c_void_p), ("ldc", ctypes.c_int64), ("scales_dev", ctypes.c_void_p),
+                ("lds", ctypes.c_int64)]
+
+
+class moe_grouped_opts_t(ctypes.Structure):
+    _fields_ = [("act", ctypes.c_int32), ("gather", ctypes.c_int32), ("scatter", ctypes.c_int32),
+                ("reserved", ctypes.c_int32), ("pairs_dev", ctypes.c_void_p)]
+
+
 class moe_prefetch_row_t(ctypes.Structure):
     _fields_ = [("addr", ctypes.c_void_p), ("bytes", ctypes.c_uint64)]
 
@@ -109,6 +122,14 @@ def _load():
         "moe_quant_i8": (c.c_int, [P, c.c_int32, c.c_int64, c.c_int32, c.c_int32, P, c.c_int64, P, P]),
         "moe_linear_i8": (c.c_int, [P, c.c_int64, P, P, c.c_int64, P, c.c_int32, c.c_int32, c.c_int32, P, P, c.c_int32,
                                     c.c_int64, P]),
+        "moe_quant_f8": (c.c_int, [P, c.c_int32, c.c_int64, c.c_int32, c.c_int32, P, c.c_int64, P, c.c_int64, P]),
+        "moe_rms_norm": (c.c_int, [P, c.c_int32, c.c_int64, c.c_int32, c.c_int32, P, c.c_int32, P, P]),
+        "moe_linear_f8": (c.c_int, [P, c.c_int64, P, c.c_int64, P, c.c_int64, P, c.c_int32, c.c_int32, c.c_int32, P, P,
+                                    c.c_int32, c.c_int64, P]),
+        "moe_lists_ws_bytes": (c.c_size_t, [c.c_int64, c.c_int32]),
+        "moe_lists": (c.c_int, [P, c.c_int64, c.c_int32, P, P, P, c.c_size_t, P]),
+        "moe_grouped_f8": (c.c_int, [P, c.c_int64, P, c.c_int64, c.c_int64, P, c.c_int64, c.c_int64, P, P, c.c_int64,
+                                     c.c_int32, c.c_int32, c.c_int32, P, P, c.c_int32, c.c_int64, c.c_int64, P]),
         "moe_work_split": (c.c_int, [c.c_int32] * 6 + [P, P]),
         "moe_grouped_runs": (c.c_int, [c.c_int32, P, c.c_int32, c.c_int32, c.c_int32, P]),
     }
@@ -123,7 +144,8 @@ EXPORTED = ("moe_status_string", "moe_plan_bytes", "moe_units_bytes", "moe_works
             "moe_pack_weights", "moe_workspace_init", "moe_plan", "moe_group", "moe_plan_group", "moe_units_export",
             "moe_experts_run", "moe_decode_run", "moe_decode_run_noalloc", "moe_combine", "moe_work_split",
             "moe_grouped_runs", "moe_gate_packed_bytes", "moe_gate_pack", "moe_gate", "moe_route", "moe_quant_i8",
-            "moe_linear_i8")
+            "moe_linear_i8", "moe_quant_f8", "moe_rms_norm", "moe_linear_f8", "moe_lists_ws_bytes", "moe_lists",
+            "moe_grouped_f8")
 
 
 def status_string(status: int) -> str:
@@ -290,7 +312,10 @@ _MOE_TYPE = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
 _BF16, _F32, _I32, _I8, _U8 = torch.bfloat16, torch.float32, torch.int32, torch.int8, torch.uint8
 _ROUTE_OPTS = struct.Struct("@5ifP2i")   # moe_route_opts_t
 _LINEAR_OPTS = struct.Struct("@2iPPq")   # moe_linear_opts_t
+_NORM_OPTS = struct.Struct("@dPqPqPq2iPqPq")  # moe_norm_opts_t
+_GROUPED_OPTS = struct.Struct("@4iP")    # moe_grouped_opts_t
 assert _ROUTE_OPTS.size == ctypes.sizeof(moe_route_opts_t) and _LINEAR_OPTS.size == ctypes.sizeof(moe_linear_opts_t)
+assert _NORM_OPTS.size == ctypes.sizeof(moe_norm_opts_t) and _GROUPED_OPTS.size == ctypes.sizeof(moe_grouped_opts_t)
 _current_device = torch._C._cuda_getDevice
 _current_stream = torch._C._cuda_getCurrentRawStream
 
@@ -306,6 +331,7 @@ class _NoBinding:
         return _NOT_TAKEN
 
     route = quant = linear = gate
+    norm = quant_f8 = linear_f8 = lists = grouped_f8 = gate
 
 
 def _load_binding():
@@ -320,6 +346,8 @@ def _load_binding():
     addresses = [ctypes.cast(getattr(lib, f), ctypes.c_void_p).value
                  for f in ("moe_gate", "moe_route", "moe_quant_i8", "moe_linear_i8")]
     _dense.bind(*addresses, _current_stream, _current_device)
+    _dense.bind_f8(*(ctypes.cast(getattr(lib, f), ctypes.c_void_p).value
+                     for f in ("moe_rms_norm", "moe_quant_f8", "moe_linear_f8", "moe_lists", "moe_grouped_f8")))
     return _dense
 
 
@@ -504,3 +532,204 @@ def moe_linear_i8(a, a_scales, w, w_scales, out, *, act: str = "none", bias=None
         tensors += (add,)
     _enqueue("moe_linear_i8", lib.moe_linear_i8, stream, tensors, a.data_ptr(), lda, psa, w.data_ptr(), ldw, psw, M, N,
              K, _LINEAR_OPTS.pack(mode, 0, pb, pd, ldd), out.data_ptr(), kind, ldo)
+
+
+# ------------------------------------------------------------ block-scaled FP8
+# e4m3 codes are torch.float8_e4m3fn tensors, their scales FP32 with one column for each 128 of a row.
+_F8 = torch.float8_e4m3fn
+
+
+def _kb(K: int) -> int:
+    return (K + 127) // 128
+
+
+def _blocks_of(t, name: str, shape: tuple):
+    """Scales of weight blocks: contiguous FP32."""
+    if t.dtype != _F32 or t.shape != shape or not t.is_contiguous():
+        _refuse(f"{name}: expected contiguous FP32 {list(shape)}")
+    return t.data_ptr()
+
+
+def _row_scales(t, name: str, shape: tuple) -> int:
+    if t.dtype != _F32 or t.dim() != 2:
+        _refuse(f"{name}: expected FP32 {list(shape)}")
+    return _rows(t, name, shape)
+
+
+def moe_quant_f8(x, codes, scales, stream=None):
+    """Quantization into blocks of 128: x [M, K] (FP32, BF16 or FP16) -> codes float8_e4m3fn [M, K], scales FP32
+    [M, ceil(K / 128)], powers of two."""
+    if stream is None:
+        status = _dense.quant_f8(x, codes, scales)
+        if status != _NOT_TAKEN:
+            return _check("moe_quant_f8", status)
+    shape = _matrix(x, "x")
+    kind = _MOE_TYPE.get(x.dtype)
+    if kind is None or codes.dtype != _F8:
+        _refuse(f"x of {x.dtype} or codes of {codes.dtype} not taken")
+    M, K = shape
+    ldx, ldc, lds = _rows(x, "x", shape), _rows(codes, "codes", shape), _row_scales(scales, "scales", (M, _kb(K)))
+    _enqueue("moe_quant_f8", lib.moe_quant_f8, stream, (x, codes, scales), x.data_ptr(), kind, ldx, M, K,
+             codes.data_ptr(), ldc, scales.data_ptr(), lds)
+
+
+def moe_rms_norm(x, weight, *, out=None, residual=None, total=None, codes=None, scales=None, eps: float = 1e-6,
+                 stream=None):
+    """Root-mean-square norm of h = x + residual (h = x without one), x [M, K] (FP32, BF16 or FP16), weight [K] (FP32
+    or as x).  Outputs, each optional: total [M, K], h itself (may be residual or x); out [M, K], the norm, as x (may
+    be x or residual); codes of it in 8 bits, int8 with scales FP32 [M] as moe_quant_i8's, or float8_e4m3fn with
+    scales FP32 [M, ceil(K / 128)] as moe_quant_f8's.  One of out and codes at least."""
+    if stream is None:
+        status = _dense.norm(x, weight, out, residual, total, codes, scales, eps)
+        if status != _NOT_TAKEN:
+            return _check("moe_rms_norm", status)
+    shape = _matrix(x, "x")
+    M, K = shape
+    kind = _MOE_TYPE.get(x.dtype)
+    if kind is None or weight.dtype not in (_F32, x.dtype) or weight.shape != (K,) or (K != 1 and weight.stride(0) != 1):
+        _refuse(f"x of {x.dtype} not taken, or weight: expected contiguous FP32 or {x.dtype} [{K}]")
+    tensors, at = [x, weight], []
+    for t, name in ((residual, "residual"), (total, "total"), (out, "out")):
+        if t is None:
+            at += [0, 0]
+            continue
+        if t.dtype != x.dtype:
+            _refuse(f"{name}: expected {x.dtype}")
+        _matrix(t, name)
+        at += [t.data_ptr(), _rows(t, name, shape)]
+        tensors.append(t)
+    form, pc, ldc, ps, lds = 0, 0, 0, 0, 0
+    if codes is not None:
+        form = 1 if codes.dtype == _I8 else 2 if codes.dtype == _F8 else _refuse(f"codes of {codes.dtype} not taken")
+        if scales is None:
+            _refuse("codes without scales")
+        _matrix(codes, "codes")
+        pc, ldc, ps = codes.data_ptr(), _rows(codes, "codes", shape), scales.data_ptr()
+        lds = _row_scales(scales, "scales", (M, _kb(K))) if form == 2 else (_vector(scales, "scales", M), 0)[1]
+        tensors += [codes, scales]
+    elif scales is not None:
+        _refuse("scales without codes")
+    if out is None and codes is None:
+        _refuse("neither out nor codes")
+    if not 0.0 <= eps < float("inf"):
+        _refuse(f"eps {eps!r}: expected a finite number, 0 or more")
+    _enqueue("moe_rms_norm", lib.moe_rms_norm, stream, tuple(tensors), x.data_ptr(), kind, _rows(x, "x", shape), M, K,
+             weight.data_ptr(), _MOE_TYPE[weight.dtype], _NORM_OPTS.pack(eps, *at, form, 0, pc, ldc, ps, lds))
+
+
+def _f8_weight_blocks(N: int, K: int, mode: int) -> tuple:
+    return (2 * ((N // 2 + 127) // 128) if mode else (N + 127) // 128, _kb(K))
+
+
+def moe_linear_f8(a, a_scales, w, w_scales, out, *, act: str = "none", bias=None, add=None, stream=None):
+    """Product of block-scaled e4m3 matrices: a float8_e4m3fn [M, K] with scales FP32 [M, ceil(K / 128)], w
+    float8_e4m3fn [N, K] with scales FP32 [ceil(N / 128), ceil(K / 128)] -> out [M, N] (FP32, BF16 or FP16), plus bias
+    (FP32 [N]); act "swiglu": the first N/2 rows of w are the gate, the others up, each half with scale blocks of its
+    own ([2 ceil(N/2 / 128), ..]), and out is [M, N/2]; add (as out, may be out itself) is added last.  K a multiple
+    of 16, rows 16-byte aligned."""
+    mode = _ACTS.get(act)
+    if stream is None:
+        status = _dense.linear_f8(a, a_scales, w, w_scales, out, mode, bias, add)
+        if status != _NOT_TAKEN:
+            return _check("moe_linear_f8", status)
+    shape, kind = _matrix(a, "a"), _MOE_TYPE.get(out.dtype)
+    M, K = shape
+    N = _matrix(w, "w")[0]
+    if mode is None or kind is None or a.dtype != _F8 or w.dtype != _F8:
+        _refuse(f"act {act!r}, a of {a.dtype}, w of {w.dtype} or out of {out.dtype} not taken")
+    if mode and N % 2:
+        _refuse("w: SwiGLU needs an even number of rows")
+    cols = N // 2 if mode else N
+    _matrix(out, "out")
+    lda, ldw, ldo = _rows(a, "a", shape), _rows(w, "w", (N, K)), _rows(out, "out", (M, cols))
+    ldsa = _row_scales(a_scales, "a_scales", (M, _kb(K)))
+    psw = _blocks_of(w_scales, "w_scales", _f8_weight_blocks(N, K, mode))
+    tensors, pb, pd, ldd = (a, a_scales, w, w_scales, out), 0, 0, 0
+    if bias is not None:
+        pb = _vector(bias, "bias", N)
+        tensors += (bias,)
+    if add is not None:
+        if add.dtype != out.dtype:
+            _refuse(f"add: expected {out.dtype}")
+        _matrix(add, "add")
+        ldd, pd = _rows(add, "add", (M, cols)), add.data_ptr()
+        tensors += (add,)
+    _enqueue("moe_linear_f8", lib.moe_linear_f8, stream, tensors, a.data_ptr(), lda, a_scales.data_ptr(), ldsa,
+             w.data_ptr(), ldw, psw, M, N, K, _LINEAR_OPTS.pack(mode, 0, pb, pd, ldd), out.data_ptr(), kind, ldo)
+
+
+def moe_lists_ws_bytes(R: int, E: int) -> int:
+    """Bytes of moe_lists' workspace for R = B * topk routes over E experts; 0: it needs none."""
+    return lib.moe_lists_ws_bytes(R, E)
+
+
+def _list_tensor(t, name: str, n: int) -> int:
+    if t.dtype != _I32 or t.shape != (n,) or not t.is_contiguous():
+        _refuse(f"{name}: expected contiguous int32 [{n}]")
+    return t.data_ptr()
+
+
+def moe_lists(ids, offsets, pairs, *, ws=None, stream=None):
+    """Routes sorted by expert: ids int32 [B, topk] -> offsets int32 [E + 1], where each expert's routes begin, and
+    pairs int32 [B * topk], the routes t * topk + s, ascending within an expert.  Ids outside [0, E) are left out;
+    pairs behind offsets[E] are -1.  ws: uint8, moe_lists_ws_bytes(B * topk, E) of them (None where that is 0)."""
+    if stream is None:
+        status = _dense.lists(ids, offsets, pairs, ws)
+        if status != _NOT_TAKEN:
+            return _check("moe_lists", status)
+    B, K = _matrix(ids, "ids")
+    if ids.dtype != _I32 or not ids.is_contiguous():
+        _refuse("ids: expected contiguous int32 [B, topk]")
+    if offsets.dim() != 1 or offsets.shape[0] < 2:
+        _refuse("offsets: expected contiguous int32 [E + 1]")
+    E = offsets.shape[0] - 1
+    tensors, pw, nw = (ids, offsets, pairs), 0, 0
+    po, pp = _list_tensor(offsets, "offsets", E + 1), _list_tensor(pairs, "pairs", B * K)
+    if ws is not None and ws.numel():
+        if not ws.is_contiguous():
+            _refuse("ws: expected contiguous memory")
+        pw, nw = ws.data_ptr(), _nbytes(ws)
+        tensors += (ws,)
+    _enqueue("moe_lists", lib.moe_lists, stream, tensors, ids.data_ptr(), B * K, E, po, pp, pw, nw)
+
+
+def moe_grouped_f8(a, a_scales, w, w_scales, offsets, out, *, act: str = "none", pairs=None, gather: int = 0,
+                   scatter: bool = False, stream=None):
+    """Products grouped by expert: rows offsets[e] .. offsets[e + 1] - 1 with w[e], w float8_e4m3fn [E, N, K] with
+    scales FP32 [E, blocks of rows, ceil(K / 128)], otherwise as moe_linear_f8.  Row i is a[i], or with gather = g
+    a[pairs[i] / g] (g = topk: the tokens' rows); its result is out[i], or with scatter out[pairs[i]].  offsets and
+    pairs from moe_lists.  Without pairs a and out have a row for each place of the lists."""
+    mode = _ACTS.get(act)
+    if stream is None:
+        status = _dense.grouped_f8(a, a_scales, w, w_scales, offsets, out, mode, pairs, gather, scatter)
+        if status != _NOT_TAKEN:
+            return _check("moe_grouped_f8", status)
+    kind = _MOE_TYPE.get(out.dtype)
+    if w.dim() != 3:
+        _refuse(f"w: expected three dimensions, got {w.dim()}")
+    E, N, K = w.shape
+    shape, rows_out = _matrix(a, "a"), _matrix(out, "out")[0]
+    if mode is None or kind is None or a.dtype != _F8 or w.dtype != _F8:
+        _refuse(f"act {act!r}, a of {a.dtype}, w of {w.dtype} or out of {out.dtype} not taken")
+    if mode and N % 2:
+        _refuse("w: SwiGLU needs an even number of rows")
+    lda, ldo = _rows(a, "a", (shape[0], K)), _rows(out, "out", (rows_out, N // 2 if mode else N))
+    ldw = _rows(w[0], "w", (N, K))
+    ldwe = w.stride(0) if E > 1 else (N - 1) * ldw + K + 15 & ~15
+    if ldwe < (N - 1) * ldw + K:
+        _refuse("w: experts overlap")
+    ldsa = _row_scales(a_scales, "a_scales", (shape[0], _kb(K)))
+    psw = _blocks_of(w_scales, "w_scales", (E, *_f8_weight_blocks(N, K, mode)))
+    po = _list_tensor(offsets, "offsets", E + 1)
+    tensors, pp, R = (a, a_scales, w, w_scales, offsets, out), 0, min(shape[0], rows_out)
+    if gather or scatter:
+        if pairs is None:
+            _refuse("gather or scatter without pairs")
+        R = pairs.numel()
+        pp = _list_tensor(pairs, "pairs", R)
+        tensors += (pairs,)
+    elif pairs is not None:
+        _refuse("pairs without gather or scatter")
+    _enqueue("moe_grouped_f8", lib.moe_grouped_f8, stream, tensors, a.data_ptr(), lda, a_scales.data_ptr(), ldsa, shape[0],
+             w.data_ptr(), ldw, ldwe, psw, po, R, E, N, K, _GROUPED_OPTS.pack(mode, gather, 1 if scatter else 0, 0, pp),
+             out.data_ptr(), kind, ldo, rows_out)

@@ -3,7 +3,9 @@
 ``Router`` turns tokens into expert ids and weights (moe_gate, moe_route),
 ``SharedExpertI8`` is a SwiGLU MLP on every token in 8-bit integers (moe_quant_i8,
 moe_linear_i8), and ``MoeBlock`` runs them around a ``MoeLayer``: router, routed experts,
-weighted combine, shared expert added last.  Each owns its device buffers for up to B_max
+weighted combine, shared expert added last.  ``ExpertsF8`` and ``SharedExpertF8`` are the routed
+experts (moe_lists, moe_grouped_f8) and the shared one (moe_linear_f8) in block-scaled FP8, for
+batches from one token to prompts, and ``Norm`` (moe_rms_norm) stands in front of the layer.  Each owns its device buffers for up to B_max
 tokens and reuses them from call to call, so calls of one object must be ordered (one
 stream, or ordered streams), and follow its construction, which enqueues on the current stream.
 torch only allocates memory and supplies the stream.
@@ -21,6 +23,8 @@ import torch
 
 from . import _lib
 from .layer import MoeLayer
+
+_F8 = torch.float8_e4m3fn
 
 
 @contextlib.contextmanager
@@ -137,26 +141,204 @@ class SharedExpertI8:
         return out
 
 
+def f8_weight_blocks(w, *, halves: bool = False):
+    """Weights [.., N, K] of a float type -> (codes float8_e4m3fn [.., N, K], scales FP32 [.., row blocks, K blocks])
+    with scale = amax / 448 for each 128 x 128; halves: gate and up rows, each half with blocks of its own (the
+    first product's weight).  For loading, in torch."""
+    w = torch.as_tensor(w)
+    if halves:
+        if w.shape[-2] % 2:
+            raise ValueError("gate and up rows: expected an even number of rows")
+        parts = [f8_weight_blocks(p) for p in w.chunk(2, dim=-2)]
+        return torch.cat([p[0].view(torch.uint8) for p in parts], -2).view(_F8), torch.cat([p[1] for p in parts], -2)
+    *lead, N, K = w.shape
+    nb, kb = (N + 127) // 128, (K + 127) // 128
+    v = torch.nn.functional.pad(w.float(), (0, kb * 128 - K, 0, nb * 128 - N)).view(*lead, nb, 128, kb, 128)
+    scales = v.abs().amax((-3, -1)) / 448
+    v = v / torch.where(scales > 0, scales, 1.0)[..., :, None, :, None]
+    return v.view(*lead, nb * 128, kb * 128)[..., :N, :K].to(_F8).contiguous(), scales.contiguous()
+
+
+def _f8_weight(w, s, device, shape, name):
+    """Codes and scales of a block-scaled weight, on the device."""
+    w, s = torch.as_tensor(w), torch.as_tensor(s)
+    if w.dtype != _F8 or w.shape != shape[0] or s.shape != shape[1]:
+        raise ValueError(f"{name}: expected float8_e4m3fn {list(shape[0])} with scales {list(shape[1])} (see "
+                         f"f8_weight_blocks), got {w.dtype} {list(w.shape)} with {list(s.shape)}")
+    return w.to(device).contiguous(), s.to(device, torch.float32).contiguous()
+
+
+class _CodesF8:
+    """Codes and scales of up to `rows` rows of `cols` features."""
+
+    def __init__(self, rows: int, cols: int, device):
+        self.codes = torch.empty(rows, cols, dtype=_F8, device=device)
+        self.scales = torch.empty(rows, (cols + 127) // 128, device=device)
+
+    def of(self, x):
+        codes, scales = self.codes[:x.shape[0]], self.scales[:x.shape[0]]
+        _lib.moe_quant_f8(x, codes, scales)
+        return codes, scales
+
+
+class ExpertsF8:
+    """Routed experts in block-scaled FP8, for batches from one token to prompts; in MoeLayer's place in a MoeBlock."""
+
+    def __init__(self, w13, s13, w2, s2, *, topk: int, B_max: int, device="cuda"):
+        """w13 float8_e4m3fn [E, 2I, D] (gate rows, then up rows) with FP32 scales [E, 2 ceil(I / 128), ceil(D / 128)],
+        w2 [E, D, I] with [E, ceil(D / 128), ceil(I / 128)]; D and I multiples of 16.  f8_weight_blocks makes them of
+        other weights."""
+        w2 = torch.as_tensor(w2)
+        if w2.dim() != 3:
+            raise ValueError("experts: w2: expected [E, D, I]")
+        self.E, self.D, self.I = map(int, w2.shape)
+        self.B_max, self.topk = int(B_max), int(topk)
+        if self.D % 16 or self.I % 16 or not 1 <= self.E <= 1024 or self.topk < 1 or self.B_max < 1:
+            raise ValueError("experts: D and I must be multiples of 16, E at most 1024")
+        E, D, I, b = self.E, self.D, self.I, lambda n: (n + 127) // 128
+        self.w13, self.s13 = _f8_weight(w13, s13, device, ((E, 2 * I, D), (E, 2 * b(I), b(D))), "experts: w13")
+        self.w2, self.s2 = _f8_weight(w2, s2, device, ((E, D, I), (E, b(D), b(I))), "experts: w2")
+        self.device = self.w2.device  # with its index: "cuda" would mean another GPU where another is current
+        R = self.B_max * self.topk
+        self.x = _CodesF8(self.B_max, D, self.device)
+        self.hidden = torch.empty(R, I, dtype=torch.bfloat16, device=self.device)
+        self.h = _CodesF8(R, I, self.device)
+        self.offsets = torch.empty(E + 1, dtype=torch.int32, device=self.device)
+        self.pairs = torch.empty(R, dtype=torch.int32, device=self.device)
+        self.ws = torch.empty(_lib.moe_lists_ws_bytes(R, E), dtype=torch.uint8, device=self.device)
+
+    def out_buffer(self, B: int) -> torch.Tensor:
+        return torch.empty(B * self.topk, self.D, dtype=torch.bfloat16, device=self.device)
+
+    def forward(self, x, ids: torch.Tensor, out: torch.Tensor | None = None, *, stream=None,
+                path: str = "auto") -> torch.Tensor:
+        """x: BF16 [B, D], or its codes and scales (as moe_quant_f8 or moe_rms_norm made them); ids: int32 [B, topk]
+        -> rows BF16 [B * topk, D] in the order of the ids, no routing weight applied.  Ids outside [0, E) have no
+        expert here, their rows of `out` are left as they were.  The hidden is rounded to BF16 between the products.
+        path: "auto" (there is one)."""
+        given = isinstance(x, (tuple, list))
+        B = (x[0] if given else x).shape[0]
+        if B > self.B_max or ids.shape != (B, self.topk):
+            raise ValueError("batch larger than B_max or ids of the wrong shape")
+        if path != "auto":
+            raise ValueError(f"unknown path {path!r}")
+        R = B * self.topk
+        with _on(stream, self.device) as give:
+            if out is None:
+                out = give(self.out_buffer(B))
+            pairs, hidden = self.pairs[:R], self.hidden[:R]
+            codes, scales = x if given else self.x.of(x)
+            _lib.moe_lists(ids, self.offsets, pairs, ws=self.ws)
+            _lib.moe_grouped_f8(codes, scales, self.w13, self.s13, self.offsets, hidden, act="swiglu", pairs=pairs,
+                                gather=self.topk)
+            codes, scales = self.h.of(hidden)
+            _lib.moe_grouped_f8(codes, scales, self.w2, self.s2, self.offsets, out, pairs=pairs, scatter=True)
+        return out
+
+    def combine(self, rows: torch.Tensor, weights: torch.Tensor, y: torch.Tensor | None = None, *, stream=None):
+        """Weighted top-k combine of the rows, as MoeLayer's."""
+        if y is None:
+            y = torch.empty(weights.shape[0], self.D, dtype=torch.bfloat16, device=self.device)
+        _lib.moe_combine(rows, weights, y, stream=stream)
+        return y
+
+
+class SharedExpertF8:
+    def __init__(self, w13, s13, w2, s2, *, B_max: int, device="cuda"):
+        """w13 float8_e4m3fn [2I, D] (gate rows, then up rows) with FP32 scales [2 ceil(I / 128), ceil(D / 128)], w2
+        [D, I] with [ceil(D / 128), ceil(I / 128)]; D and I multiples of 16."""
+        w2 = torch.as_tensor(w2)
+        if w2.dim() != 2:
+            raise ValueError("shared expert: w2: expected [D, I]")
+        self.D, self.I = map(int, w2.shape)
+        self.B_max = int(B_max)
+        if self.D % 16 or self.I % 16 or self.B_max < 1:
+            raise ValueError("shared expert: D and I must be multiples of 16")
+        D, I, b = self.D, self.I, lambda n: (n + 127) // 128
+        self.w13, self.s13 = _f8_weight(w13, s13, device, ((2 * I, D), (2 * b(I), b(D))), "shared expert: w13")
+        self.w2, self.s2 = _f8_weight(w2, s2, device, ((D, I), (b(D), b(I))), "shared expert: w2")
+        self.device = self.w2.device  # with its index: "cuda" would mean another GPU where another is current
+        self.x = _CodesF8(self.B_max, D, self.device)
+        self.hidden = torch.empty(self.B_max, I, dtype=torch.bfloat16, device=self.device)
+        self.h = _CodesF8(self.B_max, I, self.device)
+
+    def forward(self, x, *, add: torch.Tensor | None = None, out: torch.Tensor | None = None,
+                stream=None) -> torch.Tensor:
+        """x: BF16 [B, D], or its codes and scales -> BF16 [B, D], plus `add` if given (which may be out itself).  The
+        hidden is rounded to BF16 between the products."""
+        given = isinstance(x, (tuple, list))
+        B = (x[0] if given else x).shape[0]
+        if B > self.B_max:
+            raise ValueError("batch larger than B_max")
+        with _on(stream, self.device) as give:
+            if out is None:
+                out = give(torch.empty(B, self.D, dtype=torch.bfloat16, device=self.device))
+            codes, scales = x if given else self.x.of(x)
+            hidden = self.hidden[:B]
+            _lib.moe_linear_f8(codes, scales, self.w13, self.s13, hidden, act="swiglu")
+            codes, scales = self.h.of(hidden)
+            _lib.moe_linear_f8(codes, scales, self.w2, self.s2, out, add=add)
+        return out
+
+
+class Norm:
+    """The root-mean-square norm in front of a layer, and the residual stream's addition before it."""
+
+    def __init__(self, weight, *, eps: float = 1e-6, device="cuda"):
+        """weight: [D], kept in FP32."""
+        self.weight = torch.as_tensor(weight).to(device, torch.float32).contiguous()
+        if self.weight.dim() != 1:
+            raise ValueError("norm: expected a weight [D]")
+        self.device, self.D, self.eps = self.weight.device, int(self.weight.shape[0]), float(eps)
+
+    def forward(self, x: torch.Tensor, residual: torch.Tensor | None = None, *, codes=None, stream=None):
+        """x: [B, D] (BF16, FP16 or FP32) -> the norm of x + residual, of x's type; `residual` is overwritten with the
+        sum.  codes: None, torch.int8 or torch.float8_e4m3fn; with it (norm, codes, scales) is returned."""
+        B = x.shape[0]
+        with _on(stream, self.device) as give:
+            out = torch.empty(B, self.D, dtype=x.dtype, device=self.device)
+            q = s = None
+            if codes is not None:
+                q = torch.empty(B, self.D, dtype=codes, device=self.device)
+                s = torch.empty(*((B,) if codes == torch.int8 else (B, (self.D + 127) // 128)), device=self.device)
+            _lib.moe_rms_norm(x, self.weight, out=out, residual=residual, total=residual, codes=q, scales=s, eps=self.eps)
+            return give(out) if codes is None else (give(out), give(q), give(s))
+
+
 class MoeBlock:
-    def __init__(self, router: Router, layer: MoeLayer, shared: SharedExpertI8 | None = None):
+    def __init__(self, router: Router, layer: MoeLayer | ExpertsF8,
+                 shared: SharedExpertI8 | SharedExpertF8 | None = None, norm: Norm | None = None):
+        """norm: None, or the norm in front of the layer; its 8-bit codes then go straight to the FP8 parts."""
         if (router.E, router.D, router.topk) != (layer.E, layer.D, layer.topk):
             raise ValueError("router and experts differ in E, D or topk")
         if shared is not None and shared.D != layer.D:
             raise ValueError("shared expert and experts differ in D")
-        self.router, self.layer, self.shared = router, layer, shared
+        if norm is not None and norm.D != layer.D:
+            raise ValueError("norm and experts differ in D")
+        self.router, self.layer, self.shared, self.norm = router, layer, shared, norm
 
-    def forward(self, x: torch.Tensor, *, stream=None, path: str = "auto") -> torch.Tensor:
+    def forward(self, x: torch.Tensor, *, residual: torch.Tensor | None = None, stream=None,
+                path: str = "auto") -> torch.Tensor:
         """x: BF16 [B, D], contiguous -> the layer's output BF16 [B, D]: the weighted sum of the routed experts'
-        rows, rounded to BF16, plus the shared expert's."""
+        rows, rounded to BF16, plus the shared expert's.  With a norm the layer sees the norm of x + residual, and
+        `residual`, where it is given, is overwritten with that sum."""
         if x.dtype != torch.bfloat16 or not x.is_contiguous():
             raise ValueError("x: expected contiguous BF16 [B, D]")
+        if residual is not None and self.norm is None:
+            raise ValueError("a residual without a norm")
         with torch.cuda.device(x.device), _on(stream, x.device) as give:
-            return give(self._forward(x, path))
+            return give(self._forward(x, residual, path))
 
-    def _forward(self, x, path):
+    def _forward(self, x, residual, path):
+        x8 = x
+        f8 = isinstance(self.layer, ExpertsF8), isinstance(self.shared, SharedExpertF8)
+        if self.norm is not None and any(f8):
+            x, *x8 = self.norm.forward(x, residual, codes=_F8)
+        elif self.norm is not None:
+            x = x8 = self.norm.forward(x, residual)
         ids, weights = self.router.forward(x)
-        rows = self.layer.forward(x, ids, path=path)
+        rows = self.layer.forward(x8 if f8[0] else x, ids, path=path)
         y = self.layer.combine(rows, weights)
         if self.shared is not None:
-            self.shared.forward(x, add=y, out=y)
+            self.shared.forward(x8 if f8[1] else x, add=y, out=y)
         return y

@@ -14,7 +14,7 @@ from concurrent.futures import ThreadPoolExecutor
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
-SOURCES = [os.path.join(HERE, "csrc", name) for name in ("moe_mx.hip", "moe_dense.hip")]
+SOURCES = [os.path.join(HERE, "csrc", name) for name in ("moe_mx.hip", "moe_dense.hip", "moe_norm.hip", "moe_f8.hip")]
 LIB = os.path.join(HERE, "libmoe_mx.so")
 BINDING_SOURCE = os.path.join(HERE, "csrc", "dense_binding.cpp")
 BINDING = os.path.join(HERE, "_dense.so")

@@ -1,0 +1,495 @@
+// moe_f8.hip -- MI355X (gfx950) kernels of the layer in block-scaled FP8: routes sorted by expert, the
+// product of e4m3 matrices with a scale for each block of 128, and the same product grouped by
+// expert, behind the C ABI of include/moe_mx.h.
+#include <algorithm>
+#include <cstring>
+
+#include "dense_common.h"
+
+namespace {
+
+typedef int v8i __attribute__((ext_vector_type(8)));
+
+// --------------------------------------------------------------------- lists
+// A stable counting sort: counts of each wave's share of the routes, their prefix over the waves (and
+// over the workgroups before), then each wave places its routes in order.  Up to 8192 routes one
+// workgroup does it; beyond that a first launch counts, the second places.
+constexpr int kListWaves = 16, kListThreads = 64 * kListWaves, kListOne = 8192;
+
+struct ListArgs {
+  const int32_t* ids;
+  int32_t *offsets, *pairs;
+  uint32_t* counts;  // [workgroups][E], of the first launch
+  uint32_t R, E, share;  // routes a wave (a multiple of 64)
+};
+
+__device__ __forceinline__ void count_ids(const ListArgs& a, uint32_t first, uint32_t last, uint32_t* counts, int lane) {
+  for (uint32_t i = first + lane; i < last; i += 64) {
+    const uint32_t id = static_cast<uint32_t>(a.ids[i]);
+    if (id < a.E) atomicAdd(counts + id, 1u);
+  }
+}
+
+__global__ __launch_bounds__(kListThreads) void lists_count_kernel(ListArgs a) {
+  extern __shared__ uint32_t list_lds[];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  for (uint32_t e = threadIdx.x; e < a.E; e += kListThreads) list_lds[e] = 0;
+  __syncthreads();
+  const uint64_t begin = (static_cast<uint64_t>(blockIdx.x) * kListWaves + wave) * a.share;
+  const uint32_t first = static_cast<uint32_t>(begin < a.R ? begin : a.R), last = a.R - first < a.share ? a.R : first + a.share;
+  count_ids(a, first, last, list_lds, lane);
+  __syncthreads();
+  for (uint32_t e = threadIdx.x; e < a.E; e += kListThreads) a.counts[static_cast<uint64_t>(blockIdx.x) * a.E + e] = list_lds[e];
+}
+
+// Placing.  E <= kListThreads: thread e adds up expert e.
+__global__ __launch_bounds__(kListThreads) void lists_place_kernel(ListArgs a) {
+  extern __shared__ uint32_t list_lds[];  // [waves][E]: counts, then where the wave's next route goes; sums
+  uint32_t* const sums = list_lds + kListWaves * a.E;
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const uint32_t e = threadIdx.x;
+  for (uint32_t i = threadIdx.x; i < kListWaves * a.E; i += kListThreads) list_lds[i] = 0;
+  __syncthreads();
+  const uint64_t begin = (static_cast<uint64_t>(blockIdx.x) * kListWaves + wave) * a.share;
+  const uint32_t first = static_cast<uint32_t>(begin < a.R ? begin : a.R), last = a.R - first < a.share ? a.R : first + a.share;
+  count_ids(a, first, last, list_lds + wave * a.E, lane);
+  __syncthreads();
+  // routes of expert e in all, and in the workgroups before this one
+  uint32_t all = 0, before = 0;
+  if (e < a.E) {
+    if (gridDim.x > 1) {
+#pragma unroll 8
+      for (uint32_t g = 0; g < gridDim.x; ++g) {
+        const uint32_t c = a.counts[static_cast<uint64_t>(g) * a.E + e];
+        all += c;
+        before += g < blockIdx.x ? c : 0;
+      }
+    } else {
+#pragma unroll
+      for (int w = 0; w < kListWaves; ++w) all += list_lds[w * a.E + e];
+    }
+  }
+  // where expert e begins: the sum of `all` over the threads before
+  uint32_t begins = all;
+#pragma unroll
+  for (int d = 1; d < 64; d *= 2) {
+    const uint32_t o = __shfl_up(begins, d);
+    if (lane >= d) begins += o;
+  }
+  if (lane == 63) sums[wave] = begins;
+  __syncthreads();
+  begins -= all;
+  uint32_t total = 0;
+#pragma unroll
+  for (int w = 0; w < kListWaves; ++w) {
+    begins += w < wave ? sums[w] : 0;
+    total += sums[w];
+  }
+  if (e < a.E) {
+    if (blockIdx.x == 0) a.offsets[e] = static_cast<int32_t>(begins);
+    uint32_t next = begins + before;
+#pragma unroll
+    for (int w = 0; w < kListWaves; ++w) {
+      const uint32_t c = list_lds[w * a.E + e];
+      list_lds[w * a.E + e] = next;
+      next += c;
+    }
+  }
+  if (blockIdx.x == 0 && threadIdx.x == 0) a.offsets[a.E] = static_cast<int32_t>(total);
+  __syncthreads();
+  uint32_t* const next = list_lds + wave * a.E;
+  const int bits = 32 - __builtin_clz(a.E);  // ids and E itself, which stands for those left out
+  for (uint32_t i0 = first; i0 < last; i0 += 64) {
+    const uint32_t i = i0 + lane;
+    uint32_t id = i < last ? static_cast<uint32_t>(a.ids[i]) : a.E;
+    id = id < a.E ? id : a.E;
+    uint64_t same = ~0ull;  // lanes with this lane's id
+    for (int b = 0; b < bits; ++b) {
+      const bool set = id >> b & 1;
+      const uint64_t m = __ballot(set);
+      same &= set ? m : ~m;
+    }
+    const uint32_t rank = static_cast<uint32_t>(__popcll(same & ((1ull << lane) - 1)));
+    uint32_t at = 0;
+    if (id < a.E) at = next[id];
+    wave_sync();
+    if (id < a.E) {
+      a.pairs[at + rank] = static_cast<int32_t>(i);
+      if (rank == 0) next[id] = at + static_cast<uint32_t>(__popcll(same));
+    }
+    wave_sync();
+  }
+  // behind the last list; each workgroup its share of the places
+  const uint32_t span = kListWaves * a.share;
+  const uint64_t p0 = static_cast<uint64_t>(blockIdx.x) * span;
+  for (uint64_t p = p0 + threadIdx.x; p < p0 + span && p < a.R; p += kListThreads)
+    if (p >= total) a.pairs[p] = -1;
+}
+
+// ------------------------------------------------------------------- product
+struct F8Args {
+  const uint8_t *a, *w;
+  const float *sa, *sw, *bias;
+  const void* add;
+  void* out;
+  const int32_t *offsets, *pairs;  // grouped
+  int64_t lda, ldw, ldwe, ldsa, ldo, ldadd, a_rows, out_rows;
+  int32_t M, N, K, E, gather, scatter;
+};
+
+// A run of up to BM rows that share a weight.
+struct Unit {
+  int e, first, rows;
+};
+// Sum over the lanes up to this one.
+__device__ __forceinline__ int scan64(int v) {
+  v += __builtin_amdgcn_update_dpp(0, v, 0x111, 0xf, 0xf, false);  // from the lane 1, 2, 4, 8 before, within 16
+  v += __builtin_amdgcn_update_dpp(0, v, 0x112, 0xf, 0xf, false);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x114, 0xf, 0xf, false);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x118, 0xf, 0xf, false);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x142, 0xa, 0xf, false);  // lanes 15 and 47 to the 16 behind each
+  v += __builtin_amdgcn_update_dpp(0, v, 0x143, 0xc, 0xf, false);  // lane 31 to the upper half
+  return v;
+}
+// Unit `u` of a grouped product, by the prefix of the experts' unit counts; all lanes of a wave together.
+// false: there are not as many.
+template <int BM>
+__device__ __forceinline__ bool find_unit(const F8Args& a, uint32_t u, Unit& unit) {
+  const int lane = threadIdx.x & 63;
+  for (int e0 = 0; e0 < a.E; e0 += 256) {
+    int b[5], n[4], sum = 0;
+#pragma unroll
+    for (int i = 0; i < 5; ++i) {
+      const int e = e0 + lane * 4 + i, v = a.offsets[e < a.E ? e : a.E];
+      b[i] = v < 0 ? 0 : v > a.M ? a.M : v;
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      n[i] = b[i + 1] > b[i] ? b[i + 1] - b[i] : 0;
+      sum += static_cast<int>((static_cast<uint32_t>(n[i]) + BM - 1) / BM);
+    }
+    const int upto = scan64(sum);
+    const uint32_t all = static_cast<uint32_t>(__builtin_amdgcn_readlane(upto, 63));
+    if (u < all) {
+      uint32_t in = u - static_cast<uint32_t>(upto - sum);
+      const uint64_t here = __ballot(u >= static_cast<uint32_t>(upto - sum) && u < static_cast<uint32_t>(upto));
+      int e = 0, first = 0, rows = 0;
+      bool found = false;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const uint32_t c = (static_cast<uint32_t>(n[i]) + BM - 1) / BM;
+        if (!found && in < c) {
+          found = true;
+          e = e0 + lane * 4 + i;
+          first = b[i] + static_cast<int>(in) * BM;
+          rows = n[i] - static_cast<int>(in) * BM;
+        }
+        in -= c;
+      }
+      const int l = static_cast<int>(__builtin_ctzll(here));
+      unit.e = __builtin_amdgcn_readlane(e, l);
+      unit.first = __builtin_amdgcn_readlane(first, l);
+      rows = __builtin_amdgcn_readlane(rows, l);
+      unit.rows = rows < BM ? rows : BM;
+      return true;
+    }
+    u -= all;
+  }
+  return false;
+}
+
+// Row of a, and of out, of place i of the lists (-1: none).
+__device__ __forceinline__ int64_t row_of_a(const F8Args& a, int i) {
+  if (!a.gather) return i;
+  const int p = a.pairs[i];
+  const int64_t r = p < 0 ? -1 : static_cast<uint32_t>(p) / static_cast<uint32_t>(a.gather);
+  return r < a.a_rows ? r : -1;
+}
+__device__ __forceinline__ int64_t row_of_out(const F8Args& a, int i) {
+  if (!a.pairs) return i;
+  const int p = a.pairs[i];
+  if (p < 0 || (a.gather && static_cast<uint32_t>(p) / static_cast<uint32_t>(a.gather) >= a.a_rows)) return -1;
+  if (!a.scatter) return i;
+  return p < a.out_rows ? p : -1;
+}
+
+// A block's sum for a 16 x 16 tile, w's rows times a's.  The FP8 matrix cores add eight neighbouring
+// products at a time with 13 bits behind the largest of them, the rest cut off (measured: a product 2^-13 of
+// the largest counts, one of 2^-14 does not, unless they are in different eights): some 1.5e-5 of
+// the sum, which an output of 16 bits does not show (2^-9 and 2^-12 of it on average).  For FP32 outputs the
+// codes become BF16, exactly, and the BF16 cores add them with FP32's bits at half the rate.
+template <bool PRECISE>
+struct Operand {
+  using T = v8i;
+  static __device__ __forceinline__ T make(v4i lo, v4i hi) { return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7); }
+  static __device__ __forceinline__ v4f product(const T& w, const T& a) {
+    return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(w, a, v4f{0, 0, 0, 0}, 0, 0, 0, 0, 0, 0);
+  }
+};
+template <>
+struct Operand<true> {
+  struct T {
+    v8bf q[4];
+  };
+  static __device__ __forceinline__ T make(v4i lo, v4i hi) {
+    T r;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const uint32_t c = static_cast<uint32_t>(i < 4 ? lo[i] : hi[i - 4]);
+      const auto x = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(c, 1.0f, false), y = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(c, 1.0f, true);
+      r.q[i / 2][i % 2 * 4] = x[0];
+      r.q[i / 2][i % 2 * 4 + 1] = x[1];
+      r.q[i / 2][i % 2 * 4 + 2] = y[0];
+      r.q[i / 2][i % 2 * 4 + 3] = y[1];
+    }
+    return r;
+  }
+  static __device__ __forceinline__ v4f product(const T& w, const T& a) {
+    v4f d = {0, 0, 0, 0};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) d = __builtin_amdgcn_mfma_f32_16x16x32_bf16(w.q[i], a.q[i], d, 0, 0, 0);
+    return d;
+  }
+};
+
+// ------------------------------------------------------------ product: few rows
+// The weight is read once, so its bytes bound the product.  A workgroup takes 16 RT weight rows
+// (SwiGLU: 16 gate rows and their 16 up rows) and 16 TT rows of a; its WV waves split K in blocks of
+// 128.  A wave loads a block's rows eight lanes to a row, some blocks ahead, and turns them into operands
+// through LDS of its own; a 16x16x128 MFMA is one block's sum, which is scaled and added in FP32.
+// Lane l's operand holds parts l / 16 and 4 + l / 16 of its row's eight: any order of k within the block
+// will do that both sides have, and this one meets all banks of LDS.
+template <int OUT, bool SWIGLU, bool GROUPED, int RT, int TT, int WV>
+__global__ __launch_bounds__(64 * WV) void f8_stream_kernel(F8Args a, uint32_t nx) {
+  extern __shared__ __attribute__((aligned(16))) unsigned char smem[];
+  constexpr int COLS = SWIGLU ? 16 : 16 * RT, NL = 2 * (RT + TT), NS = SWIGLU ? 2 : 1;
+  constexpr int kRegs = (2048 / WV - 4 * RT * TT - 12 * (RT + TT) - 48) / (NL * 4 + TT + NS);
+  constexpr int U = kRegs > 6 ? 6 : kRegs < 2 ? 2 : kRegs;  // blocks in flight
+  static_assert(!SWIGLU || RT == 2, "a gate and an up tile");
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int H = SWIGLU ? a.N / 2 : a.N, n0 = blockIdx.x % nx * COLS;
+  const int blocks = (a.K + 127) / 128, per = (blocks + WV - 1) / WV, c0 = wave * per;
+  const int n = blocks - c0 < per ? (blocks > c0 ? blocks - c0 : 0) : per;
+  Unit unit;
+  if constexpr (GROUPED) {
+    if (!find_unit<16 * TT>(a, blockIdx.x / nx, unit)) return;
+  } else {
+    unit.e = 0;
+    unit.first = blockIdx.x / nx * (16 * TT);
+    unit.rows = a.M - unit.first < 16 * TT ? a.M - unit.first : 16 * TT;
+  }
+  // load i brings rows 8 i .. 8 i + 7 of the wave's tile: weight rows first, then rows of a
+  const int part = lane & 7;
+  const uint8_t* rows[NL];
+  const float* scale[TT + NS];
+  const uint8_t* const w = a.w + unit.e * a.ldwe;
+#pragma unroll
+  for (int i = 0; i < NL; ++i) {
+    const int r = i * 8 + (lane >> 3);
+    if (i < 2 * RT) {
+      const int c = n0 + (SWIGLU ? r & 15 : r);
+      rows[i] = w + ((c < H ? c : H - 1) + (SWIGLU ? static_cast<int64_t>(r >> 4) * H : 0)) * a.ldw;
+    } else {
+      const int m = r - 16 * RT;
+      const int64_t at = GROUPED ? row_of_a(a, unit.first + (m < unit.rows ? m : unit.rows - 1))
+                                 : unit.first + (m < unit.rows ? m : unit.rows - 1);
+      rows[i] = a.a + (at < 0 ? 0 : at) * a.lda;
+    }
+  }
+#pragma unroll
+  for (int j = 0; j < TT; ++j) {
+    const int m = j * 16 + (lane & 15);
+    const int64_t at = GROUPED ? row_of_a(a, unit.first + (m < unit.rows ? m : unit.rows - 1))
+                               : unit.first + (m < unit.rows ? m : unit.rows - 1);
+    scale[j] = a.sa + (at < 0 ? 0 : at) * a.ldsa;
+  }
+  const int halves = SWIGLU ? 2 : 1, nb = (H + 127) / 128;  // blocks of weight rows in each
+#pragma unroll
+  for (int h = 0; h < NS; ++h) scale[TT + h] = a.sw + ((static_cast<int64_t>(unit.e) * halves + h) * nb + n0 / 128) * blocks;
+  v4i held[U][NL];
+  float held_scale[U][TT + NS];
+  // 16 bytes lie wholly inside the row or wholly behind it; those behind are read from the row's last 16, and
+  // the weight's set to zero when used
+  auto load = [&](int u, int c) {
+    const int k = (c0 + c) * 128 + part * 16;
+#pragma unroll
+    for (int i = 0; i < NL; ++i) held[u][i] = *reinterpret_cast<const v4i*>(rows[i] + (k < a.K ? k : a.K - 16));
+#pragma unroll
+    for (int i = 0; i < TT + NS; ++i) held_scale[u][i] = scale[i][c0 + c];
+  };
+  unsigned char* const own = smem + wave * (NL * 1024);
+  auto place = [](int r, int c) { return r * 128 + (c ^ ((r >> 1) & 7)) * 16; };
+  v4f acc[RT][TT] = {};
+#pragma unroll
+  for (int u = 0; u < U; ++u)
+    if (u < n) load(u, u);
+  compiler_fence();
+  for (int c = 0; c < n; c += U) {
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+      if (c + u < n) {
+        const bool behind = (c0 + c + u) * 128 + part * 16 >= a.K;
+        float s[TT + NS];
+#pragma unroll
+        for (int i = 0; i < NL; ++i)
+          *reinterpret_cast<v4i*>(own + place(i * 8 + (lane >> 3), part)) = i < 2 * RT && behind ? v4i{0, 0, 0, 0} : held[u][i];
+#pragma unroll
+        for (int i = 0; i < TT + NS; ++i) s[i] = held_scale[u][i];
+        if (c + u + U < n) load(u, c + u + U);
+        wave_sync();
+        using Op = Operand<OUT == MOE_F32>;
+        typename Op::T fw[RT], fa[TT];
+        auto operand = [&](int tile) {
+          return Op::make(*reinterpret_cast<const v4i*>(own + place(tile * 16 + (lane & 15), lane >> 4)),
+                          *reinterpret_cast<const v4i*>(own + place(tile * 16 + (lane & 15), 4 + (lane >> 4))));
+        };
+#pragma unroll
+        for (int i = 0; i < RT; ++i) fw[i] = operand(i);
+#pragma unroll
+        for (int j = 0; j < TT; ++j) fa[j] = operand(RT + j);
+#pragma unroll
+        for (int i = 0; i < RT; ++i)
+#pragma unroll
+          for (int j = 0; j < TT; ++j) {
+            const v4f d = Op::product(fw[i], fa[j]);
+            const float f = s[j] * s[TT + (SWIGLU ? i : 0)];
+#pragma unroll
+            for (int x = 0; x < 4; ++x) acc[i][j][x] = __builtin_fmaf(d[x], f, acc[i][j][x]);
+          }
+        wave_sync();
+      }
+  }
+  // [wave][row of a][weight row], padded by four words a row
+  constexpr int kRow = 16 * RT + 4, kTile = 16 * TT * kRow;
+  float* const sums = reinterpret_cast<float*>(smem);
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < RT; ++i)
+#pragma unroll
+    for (int j = 0; j < TT; ++j)
+      *reinterpret_cast<v4f*>(sums + wave * kTile + (j * 16 + (lane & 15)) * kRow + i * 16 + (lane >> 4) * 4) = acc[i][j];
+  __syncthreads();
+  using T = typename Elem<OUT>::T;
+  for (int o = threadIdx.x; o < COLS * 16 * TT; o += 64 * WV) {
+    const int r = o / COLS, c = n0 + o % COLS;
+    if (r >= unit.rows || c >= H) continue;
+    const int64_t m = GROUPED ? row_of_out(a, unit.first + r) : unit.first + r;
+    if (GROUPED && m < 0) continue;
+    const float* p = sums + r * kRow + o % COLS;
+    float y = 0.0f, up = 0.0f;
+#pragma unroll
+    for (int v = 0; v < WV; ++v) {
+      y += p[v * kTile];
+      if (SWIGLU) up += p[v * kTile + 16];
+    }
+    if (a.bias) y += a.bias[c];
+    if (SWIGLU) y = silu(y) * (a.bias ? up + a.bias[H + c] : up);
+    if (a.add) y += to_f32<OUT>(static_cast<const T*>(a.add)[m * a.ldadd + c]);
+    static_cast<T*>(a.out)[m * a.ldo + c] = from_f32<OUT>(y);
+  }
+}
+
+// ---------------------------------------------------------------------- host
+template <int OUT, bool SWIGLU, bool GROUPED, int RT, int TT, int WV>
+int launch_stream(const F8Args& a, hipStream_t st) {
+  static std::atomic<uint64_t> done{0};
+  constexpr size_t lds = WV * std::max(2048 * (RT + TT), 64 * TT * (16 * RT + 4));
+  static_assert(lds <= 160 * 1024, "LDS of a CU");
+  if (!allow_lds(f8_stream_kernel<OUT, SWIGLU, GROUPED, RT, TT, WV>, lds, done)) return hip_failed();
+  const int64_t cols = SWIGLU ? a.N / 2 : a.N, per = SWIGLU ? 16 : 16 * RT, nx = (cols + per - 1) / per;
+  constexpr int BM = 16 * TT;
+  // grouped: the experts' last runs may be short
+  const int64_t units = GROUPED ? (a.M + static_cast<int64_t>(std::min(a.E, a.M)) * (BM - 1)) / BM : (a.M + BM - 1) / BM;
+  if (nx * units > 0x7fffffff) return MOE_EINVAL;
+  return launch(f8_stream_kernel<OUT, SWIGLU, GROUPED, RT, TT, WV>, static_cast<uint32_t>(nx * units), 64 * WV, lds, st, a,
+                static_cast<uint32_t>(nx));
+}
+
+template <int OUT, bool SWIGLU, bool GROUPED>
+int launch_product(const F8Args& a, hipStream_t st) {
+  constexpr int R1 = SWIGLU ? 2 : 1;
+  const int64_t rows = GROUPED ? (a.M + std::min(a.E, a.M) - 1) / std::min(a.E, a.M) : a.M;  // that share a weight
+  if (rows <= 16) return launch_stream<OUT, SWIGLU, GROUPED, R1, 1, 16>(a, st);
+  if (rows <= 32) return launch_stream<OUT, SWIGLU, GROUPED, R1, 2, 8>(a, st);
+  return launch_stream<OUT, SWIGLU, GROUPED, 2, 4, 8>(a, st);
+}
+template <bool GROUPED>
+int launch_product(const F8Args& a, int32_t out_type, bool swiglu, hipStream_t st) {
+  if (out_type == MOE_F32) return swiglu ? launch_product<MOE_F32, true, GROUPED>(a, st) : launch_product<MOE_F32, false, GROUPED>(a, st);
+  if (out_type == MOE_F16) return swiglu ? launch_product<MOE_F16, true, GROUPED>(a, st) : launch_product<MOE_F16, false, GROUPED>(a, st);
+  return swiglu ? launch_product<MOE_BF16, true, GROUPED>(a, st) : launch_product<MOE_BF16, false, GROUPED>(a, st);
+}
+
+constexpr int64_t kMaxLd = 1 << 22, kMaxRoutes = 1 << 26;
+uint32_t list_groups(int64_t R) {  // workgroups: 4096 routes each, 256 at most
+  return static_cast<uint32_t>(R <= kListOne ? 1 : std::min<int64_t>((R + 4095) / 4096, 256));
+}
+bool product_ok(const void* a, int64_t lda, const float* sa, int64_t ldsa, const void* w, int64_t ldw, const float* sw, int32_t N,
+                int32_t K, int32_t act, const void* out, int32_t out_type, int64_t ldo) {
+  return a && sa && w && sw && out && type_ok(out_type) && N >= 1 && N <= 1 << 20 && K >= 16 && K <= 65536 && lda >= K && ldw >= K &&
+         lda < kMaxLd && ldw < kMaxLd && ldsa < kMaxLd && ldsa >= (K + 127) / 128 && act >= 0 && act <= 1 &&
+         !(act == 1 && N % 2) && ldo >= (act == 1 ? N / 2 : N) &&
+         (reinterpret_cast<uintptr_t>(a) | reinterpret_cast<uintptr_t>(w) | lda | ldw | static_cast<uintptr_t>(K)) % 16 == 0;
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t moe_lists_ws_bytes(int64_t R, int32_t E) {
+  if (R < 1 || R > kMaxRoutes || E < 1 || E > 1024 || R <= kListOne) return 0;
+  return static_cast<size_t>(list_groups(R)) * E * 4;
+}
+
+int moe_lists(const int32_t* ids, int64_t R, int32_t E, int32_t* offsets, int32_t* pairs, void* ws, size_t ws_bytes, void* stream) {
+  if (!ids || !offsets || !pairs || R < 1 || R > kMaxRoutes || E < 1 || E > 1024) return MOE_EINVAL;
+  const size_t need = moe_lists_ws_bytes(R, E);
+  if (need && (!ws || reinterpret_cast<uintptr_t>(ws) % 4)) return MOE_EINVAL;
+  if (ws_bytes < need) return MOE_ENOSPACE;
+  const uint32_t groups = list_groups(R);
+  const int64_t waves = static_cast<int64_t>(groups) * kListWaves, share = ((R + waves - 1) / waves + 63) / 64 * 64;
+  const ListArgs a = {ids, offsets, pairs, static_cast<uint32_t*>(ws), static_cast<uint32_t>(R), static_cast<uint32_t>(E),
+                      static_cast<uint32_t>(share)};
+  hipStream_t st = as_stream(stream);
+  static std::atomic<uint64_t> done{0};
+  const size_t lds = static_cast<size_t>(kListWaves) * (E + 1) * 4;
+  if (lds > 65536 && !allow_lds(lists_place_kernel, static_cast<size_t>(kListWaves) * 1025 * 4, done)) return hip_failed();
+  if (groups > 1) {
+    const int r = launch(lists_count_kernel, groups, kListThreads, E * 4, st, a);
+    if (r != MOE_OK) return r;
+  }
+  return launch(lists_place_kernel, groups, kListThreads, lds, st, a);
+}
+
+int moe_linear_f8(const uint8_t* a, int64_t lda, const float* sa, int64_t ldsa, const uint8_t* w, int64_t ldw, const float* sw,
+                  int32_t M, int32_t N, int32_t K, const moe_linear_opts_t* opts, void* out, int32_t out_type, int64_t ldo,
+                  void* stream) {
+  moe_linear_opts_t o;
+  std::memset(&o, 0, sizeof(o));
+  if (opts) o = *opts;
+  if (!product_ok(a, lda, sa, ldsa, w, ldw, sw, N, K, o.act, out, out_type, ldo) || M < 1 || M > kMaxRows ||
+      static_cast<int64_t>(M) * N > 1LL << 34 || (o.add_dev && o.ldadd < (o.act == 1 ? N / 2 : N)))
+    return MOE_EINVAL;
+  F8Args r = {a, w, sa, sw, o.bias_dev, o.add_dev, out, nullptr, nullptr, lda, ldw, 0, ldsa, ldo, o.ldadd, M, M, M, N, K, 1, 0, 0};
+  return launch_product<false>(r, out_type, o.act == 1, as_stream(stream));
+}
+
+int moe_grouped_f8(const uint8_t* a, int64_t lda, const float* sa, int64_t ldsa, int64_t a_rows, const uint8_t* w, int64_t ldw,
+                   int64_t ldwe, const float* sw, const int32_t* offsets, int64_t R, int32_t E, int32_t N, int32_t K,
+                   const moe_grouped_opts_t* opts, void* out, int32_t out_type, int64_t ldo, int64_t out_rows, void* stream) {
+  moe_grouped_opts_t o;
+  std::memset(&o, 0, sizeof(o));
+  if (opts) o = *opts;
+  if (!product_ok(a, lda, sa, ldsa, w, ldw, sw, N, K, o.act, out, out_type, ldo) || !offsets || R < 1 || R > kMaxRoutes || E < 1 ||
+      E > 1024 || R * N > 1LL << 40 || o.gather < 0 || o.scatter < 0 || o.scatter > 1 ||
+      ldwe < (static_cast<int64_t>(N) - 1) * ldw + K || ldwe % 16 || a_rows < 1 || out_rows < 1)
+    return MOE_EINVAL;
+  if (o.gather || o.scatter ? !o.pairs_dev : o.pairs_dev != nullptr) return MOE_EINVAL;
+  if (o.gather ? a_rows * lda >= 1LL << 31 : a_rows < R) return MOE_EINVAL;
+  if (!o.scatter && out_rows < R) return MOE_EINVAL;
+  F8Args r = {a,    w,    sa,  sw,      nullptr, nullptr, out,      offsets,
+              o.pairs_dev, lda, ldw,    ldwe,    ldsa,    ldo,      0,       a_rows, out_rows, static_cast<int32_t>(R), N, K, E, o.gather, o.scatter};
+  return launch_product<true>(r, out_type, o.act == 1, as_stream(stream));
+}
+
+}  // extern "C"
