@@ -505,7 +505,8 @@ int moe_rms_norm(const void* x_dev, int32_t type, int64_t ldx, int32_t M, int32_
  * [NB, KB], contiguous: NB = ceil(N / 128), with act 1 NB = 2 ceil(N/2 / 128), as the gate rows (0 ..
  * N/2 - 1) and the up rows have blocks of their own.  out_dev [M, N or N/2] of out_type (ldo).
  * opts as moe_linear_i8's.  16-byte alignment of a_dev, w_dev, lda and ldw, K % 16 == 0.
- * 1 <= N <= 2^20, M * N <= 2^34, 16 <= K <= 65536, lda, ldw and ldsa < 2^22; MOE_EINVAL otherwise. */
+ * 1 <= N <= 2^20, M * N <= 2^34, 16 <= K <= 65536, lda and ldw < 2^22, ldsa < 2^20;
+ * MOE_EINVAL otherwise. */
 int moe_linear_f8(const uint8_t* a_dev, int64_t lda, const float* a_scales_dev, int64_t ldsa, const uint8_t* w_dev,
                   int64_t ldw, const float* w_scales_dev, int32_t M, int32_t N, int32_t K,
                   const moe_linear_opts_t* opts, void* out_dev, int32_t out_type, int64_t ldo, void* stream);
@@ -538,7 +539,7 @@ typedef struct {
  *   ascending; R the most rows that they may hold; out_dev [out_rows, N or N/2] (ldo).
  * Without gather a_rows >= R, without scatter out_rows >= R.  Rows behind offsets[E], and those whose
  * pair names no row of a or out, are left as they were; offsets outside 0 .. R are cut to it.
- * With gather a_rows * lda < 2^31.  1 <= E <= 1024, 1 <= R <= 2^26, R * N <= 2^40; other limits as
+ * With gather a_rows * lda < 2^31 and a_rows * ldsa < 2^29.  1 <= E <= 1024, 1 <= R <= 2^26, R * N <= 2^40; other limits as
  * moe_linear_f8's. */
 int moe_grouped_f8(const uint8_t* a_dev, int64_t lda, const float* a_scales_dev, int64_t ldsa, int64_t a_rows,
                    const uint8_t* w_dev, int64_t ldw, int64_t ldwe, const float* w_scales_dev,

@@ -198,6 +198,26 @@ __device__ __forceinline__ bool find_unit(const F8Args& a, uint32_t u, Unit& uni
   return false;
 }
 
+// Units there are.
+template <int BM>
+__device__ __forceinline__ uint32_t count_units(const F8Args& a) {
+  const int lane = threadIdx.x & 63;
+  uint32_t all = 0;
+  for (int e0 = 0; e0 < a.E; e0 += 256) {
+    int b[5], sum = 0;
+#pragma unroll
+    for (int i = 0; i < 5; ++i) {
+      const int e = e0 + lane * 4 + i, v = a.offsets[e < a.E ? e : a.E];
+      b[i] = v < 0 ? 0 : v > a.M ? a.M : v;
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      sum += b[i + 1] > b[i] ? static_cast<int>((static_cast<uint32_t>(b[i + 1] - b[i]) + BM - 1) / BM) : 0;
+    all += static_cast<uint32_t>(__builtin_amdgcn_readlane(scan64(sum), 63));
+  }
+  return all;
+}
+
 // Row of a, and of out, of place i of the lists (-1: none).
 __device__ __forceinline__ int64_t row_of_a(const F8Args& a, int i) {
   if (!a.gather) return i;
@@ -389,6 +409,255 @@ __global__ __launch_bounds__(64 * WV) void f8_stream_kernel(F8Args a, uint32_t n
   }
 }
 
+// ----------------------------------------------------------- product: many rows
+__device__ __forceinline__ void dma4s(v4i rsrc, uint32_t voff, uint32_t soff, uint32_t lds) {  // 4 bytes a lane
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dword %1, %2, %3 offen lds"
+               :
+               : "s"(lds), "v"(voff), "s"(rsrc), "s"(soff)
+               : "m0", "memory");
+}
+
+// Workgroup tile of BM rows of a x BN weight rows, WM x WN waves, each with TM x TN tiles of 16 x 16.  K goes
+// through LDS in stages of one block, NS deep, by LDS DMA; with the stage come the scales of a's rows, while those of
+// the weight's blocks lie in LDS from the start.  A row's 16-byte parts lie permuted by its index (as in
+// the int8 product's tiles).  A wave holds its rows of a for a whole block and takes its weight rows 16 at a
+// time; behind the last of them the next block's rows of a follow into the registers that each product leaves.
+template <int BM, int BN, int WM, int WN, int NS, int OUT, bool SWIGLU, bool GROUPED>
+__global__ __launch_bounds__(64 * WM * WN, 1) void f8_tile_kernel(F8Args a, uint32_t nm, uint32_t nn, uint32_t per_xcd) {
+  extern __shared__ __attribute__((aligned(16))) unsigned char smem[];
+  constexpr int NW = WM * WN, kRows = (BM + BN) * 128, kStage = kRows + BM * 4;
+  constexpr int RA = BM / 8 / NW, RW = BN / 8 / NW, kIssue = RA + RW + 1;  // DMAs of a wave: 8 rows each, and scales
+  constexpr int TM = BM / WM / 16, TN = BN / WN / 16, kWaveRows = BN / WN;
+  constexpr int NB = SWIGLU ? 2 : BN > 128 ? BN / 128 : 1;  // scale blocks of the weight
+  static_assert(BM % (8 * NW) == 0 && BN % (8 * NW) == 0 && BM / 64 <= NW && TN % 2 == 0 && kWaveRows <= 128, "whole DMAs, whole blocks");
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int H = SWIGLU ? a.N / 2 : a.N, KB = (a.K + 127) / 128, KBP = (KB + 63) / 64 * 64;
+  constexpr int kLag = 2;  // a product is scaled and added behind the second one after it
+  constexpr int kCols = SWIGLU ? BN / 2 : BN;
+  // each XCD (workgroups go round the eight) takes a contiguous range of tiles: what runs at once on an XCD
+  // shares operands in its L2
+  Unit unit;
+  int n0;
+  if constexpr (GROUPED) {
+    const uint32_t tiles = count_units<BM>(a) * nn, per = (tiles + 7) / 8, tile = blockIdx.x % 8 * per + blockIdx.x / 8;
+    if (blockIdx.x / 8 >= per || tile >= tiles || !find_unit<BM>(a, tile / nn, unit)) return;
+    n0 = static_cast<int>(tile % nn) * kCols;
+  } else {
+    const uint32_t tile = blockIdx.x % 8 * per_xcd + blockIdx.x / 8;
+    if (blockIdx.x / 8 >= per_xcd || tile >= nm * nn) return;
+    const uint32_t band = tile / (8 * nn), left = nm - band * 8, height = left < 8 ? left : 8, in = tile - band * 8 * nn;
+    unit.e = 0;
+    unit.first = static_cast<int>(band * 8 + in % height) * BM;
+    unit.rows = a.M - unit.first < BM ? a.M - unit.first : BM;
+    n0 = static_cast<int>(in / height) * kCols;
+  }
+  const uint32_t lds0 = static_cast<uint32_t>(reinterpret_cast<uintptr_t>((__attribute__((address_space(3))) void*)smem));
+  constexpr int kDummy = NS * kStage, kMap = kDummy + 256, kScales = kMap + BM * 4;
+  int* const out_row = reinterpret_cast<int*>(smem + kMap);
+
+  for (int r = threadIdx.x; r < BM; r += 64 * NW)
+    out_row[r] = r >= unit.rows ? -1 : GROUPED ? static_cast<int>(row_of_out(a, unit.first + r)) : unit.first + r;
+  auto place = [](int r, int c) { return c ^ ((r >> 1) & 7); };
+  // what this lane moves: a part of row lane / 8 of its wave's blocks of 8 rows
+  const bool gather = GROUPED && a.gather;
+  const uint64_t base = gather ? 0 : static_cast<uint64_t>(unit.first);
+  const uint32_t extent_rows = gather ? static_cast<uint32_t>(a.a_rows) : static_cast<uint32_t>(unit.rows);
+  auto row_in = [&](int r) -> uint32_t {  // row r of the tile, counted from the base; behind the last: none
+    if (r >= unit.rows) return ~0u;
+    if (!gather) return static_cast<uint32_t>(r);
+    return static_cast<uint32_t>(row_of_a(a, unit.first + r));
+  };
+  const v4i ra = make_rsrc(a.a + base * a.lda, static_cast<uint32_t>((extent_rows - 1) * a.lda + a.K));
+  const v4i rs = make_rsrc(a.sa + base * a.ldsa, static_cast<uint32_t>(((extent_rows - 1) * a.ldsa + KB) * 4));
+  uint32_t va[RA], vw[RW], vs;
+  int ka[RA], kw[RW];  // the part's offset in the block
+  v4i rw[RW];
+#pragma unroll
+  for (int i = 0; i < RA; ++i) {
+    const int r = (wave * RA + i) * 8 + (lane >> 3);
+    const uint32_t at = row_in(r);
+    ka[i] = place(r, lane & 7) * 16;
+    va[i] = at != ~0u ? at * static_cast<uint32_t>(a.lda) + ka[i] : kOutside;
+  }
+  {
+    const uint32_t at = wave < BM / 64 ? row_in(wave * 64 + lane) : ~0u;
+    vs = at != ~0u ? at * static_cast<uint32_t>(a.ldsa) * 4u : kOutside;
+  }
+  {
+    const int nrows = H - n0 < kCols ? H - n0 : kCols;
+    const uint32_t bytes = static_cast<uint32_t>((nrows - 1) * a.ldw + a.K);
+    const uint8_t* const w = a.w + unit.e * a.ldwe + static_cast<int64_t>(n0) * a.ldw;
+#pragma unroll
+    for (int i = 0; i < RW; ++i) {
+      // SwiGLU: a wave's gate rows, then its up rows
+      const int first = (wave * RW + i) * 8, slot = first + (lane >> 3), half = SWIGLU ? first / (kWaveRows / 2) & 1 : 0;
+      const int row = SWIGLU ? slot / kWaveRows * (kWaveRows / 2) + slot % (kWaveRows / 2) : slot;
+      kw[i] = place(slot, lane & 7) * 16;
+      rw[i] = make_rsrc(w + static_cast<int64_t>(half) * H * a.ldw, bytes);
+      vw[i] = row < nrows ? static_cast<uint32_t>(row) * static_cast<uint32_t>(a.ldw) + kw[i] : kOutside;
+    }
+  }
+  // DMA d of this wave for stage s into the LDS at buf; parts behind K, and whole stages behind it, are zeros (with no
+  // scalar offset then: nothing says that the bounds check's difference does not wrap)
+  auto issue = [&](int s, int buf, int d) {
+    const int k0 = s * 128;
+    const bool in = k0 < a.K;
+    const uint32_t soff = in ? k0 : 0;
+    if (d < RA) {
+      dma16(ra, k0 + ka[d] < a.K ? va[d] : kOutside, soff, lds0 + buf + (wave * RA + d) * 1024);
+    } else if (d < RA + RW) {
+      d -= RA;
+      dma16(rw[d], k0 + kw[d] < a.K ? vw[d] : kOutside, soff, lds0 + buf + BM * 128 + (wave * RW + d) * 1024);
+    } else {
+      dma4s(rs, in ? vs : kOutside, in ? s * 4 : 0, lds0 + (wave < BM / 64 ? buf + kRows + wave * 256 : kDummy));
+    }
+  };
+
+  const int wm = wave % WM * (BM / WM), wn = wave / WM * kWaveRows;
+  using Op = Operand<OUT == MOE_F32>;
+  const int la0 = (lane & 15) * 128 + place(lane & 15, lane >> 4) * 16, la1 = (lane & 15) * 128 + place(lane & 15, 4 + (lane >> 4)) * 16;
+  auto operand = [&](int at) {
+    return Op::make(*reinterpret_cast<const v4i*>(smem + at + la0), *reinterpret_cast<const v4i*>(smem + at + la1));
+  };
+  v4f acc[TN][TM] = {};
+  typename Op::T fa[TM], fw[2];
+  float sa[TM], sw[2];
+  const float* const wscale = reinterpret_cast<const float*>(smem + kScales) + (SWIGLU ? 0 : wn / 128 * KBP);
+  auto read_scales = [&](int buf, int s) {
+#pragma unroll
+    for (int j = 0; j < TM; ++j) sa[j] = *reinterpret_cast<const float*>(smem + buf + kRows + (wm + j * 16 + (lane & 15)) * 4);
+    s = s < KB ? s : KB - 1;
+    sw[0] = wscale[s];
+    if (SWIGLU) sw[1] = wscale[KBP + s];
+  };
+  // the weight's scales first
+  {
+    const int halves = SWIGLU ? 2 : 1, nb = (H + 127) / 128;
+    for (int d = wave; d < NB * KBP / 64; d += NW) {
+      const int h = d / (KBP / 64), k = d % (KBP / 64) * 64, block = n0 / 128 + (SWIGLU ? 0 : h);
+      const int64_t row = (static_cast<int64_t>(unit.e) * halves + (SWIGLU ? h : 0)) * nb + (block < nb ? block : nb - 1);
+      dma4(make_rsrc(a.sw + row * KB, static_cast<uint32_t>(KB) * 4u), k + lane < KB ? (k + lane) * 4u : kOutside,
+           lds0 + kScales + (h * KBP + k) * 4);
+    }
+  }
+  // a stage's DMAs are issued behind the rows of products that follow its buffer's release
+  auto slot = [](int p) { return p * kIssue / TN; };
+#pragma unroll
+  for (int s = 0; s < NS; ++s) {
+#pragma unroll
+    for (int d = 0; d < (s < NS - 1 ? kIssue : slot(1)); ++d) issue(s, s * kStage, d);
+  }
+  wait_vm<kIssue*(NS - 2) + slot(1)>();
+  __builtin_amdgcn_s_barrier();
+  compiler_fence();
+#pragma unroll
+  for (int j = 0; j < TM; ++j) fa[j] = operand((wm + j * 16) * 128);
+  fw[0] = operand((BM + wn) * 128);
+  read_scales(0, 0);
+  int prev = (NS - 1) * kStage, cur = 0;  // LDS offsets of stages s - 1 and s
+  for (int s = 0; s < KB; ++s) {
+    const int next = cur + kStage == NS * kStage ? 0 : cur + kStage;
+    v4f d[kLag + 1];
+    auto add = [&](int m) {  // product m of the block
+      const int i = m / TM, j = m % TM;
+      const float f = sa[j] * sw[SWIGLU && i >= TN / 2 ? 1 : 0];
+#pragma unroll
+      for (int x = 0; x < 4; ++x) acc[i][j][x] = __builtin_fmaf(d[m % (kLag + 1)][x], f, acc[i][j][x]);
+    };
+#pragma unroll
+    for (int i = 0; i < TN; ++i) {
+      if (i == TN - 1) {
+        // this stage is read out and the next has landed, for every wave
+        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+        wait_vm<kIssue*(NS - 2)>();
+        __builtin_amdgcn_s_barrier();
+        compiler_fence();
+        __builtin_amdgcn_sched_barrier(0);
+      }
+      fw[(i + 1) & 1] = operand((i == TN - 1 ? next : cur) + (BM + wn + (i + 1) % TN * 16) * 128);
+#pragma unroll
+      for (int j = 0; j < TM; ++j) {
+        const int m = i * TM + j;
+        d[m % (kLag + 1)] = Op::product(fw[i & 1], fa[j]);
+        if (i == TN - 1) fa[j] = operand(next + (wm + j * 16) * 128);
+        if (m >= kLag) add(m - kLag);
+      }
+      const int p = (i + 1) % TN;
+#pragma unroll
+      for (int x = slot(p); x < slot(p + 1); ++x) {
+        if (i == TN - 1) issue(s + NS, cur, x);
+        else issue(s + NS - 1, prev, x);
+      }
+      __builtin_amdgcn_sched_barrier(0);
+    }
+#pragma unroll
+    for (int m = TN * TM - kLag; m < TN * TM; ++m) add(m);
+    read_scales(next, s + 1);
+    prev = cur;
+    cur = next;
+    compiler_fence();
+  }
+  wait_vm<0>();
+  __syncthreads();
+  // 32 rows of out at a time go through LDS, so that whole rows' pieces are added to and stored
+  using T = typename Elem<OUT>::T;
+  constexpr int kOut = SWIGLU ? kWaveRows / 2 : kWaveRows, kRow = kOut + 4, PER = 16 / sizeof(T), kPieces = kOut / PER;
+  static_assert(NW * 32 * kRow * 4 <= NS * kStage && TM % 2 == 0, "epilogue fits the stages");
+  float* const buf = reinterpret_cast<float*>(smem) + wave * 32 * kRow;
+  const int nw0 = n0 + (SWIGLU ? wn / 2 : wn);
+  const bool vec = (reinterpret_cast<uintptr_t>(a.out) | (a.ldo * sizeof(T))) % 16 == 0 &&
+                   (!a.add || (reinterpret_cast<uintptr_t>(a.add) | (a.ldadd * sizeof(T))) % 16 == 0);
+#pragma unroll
+  for (int j0 = 0; j0 < TM; j0 += 2) {
+#pragma unroll
+    for (int j = j0; j < j0 + 2; ++j)
+#pragma unroll
+      for (int i = 0; i < (SWIGLU ? TN / 2 : TN); ++i) {
+        const int c = i * 16 + (lane >> 4) * 4;
+        v4f y = acc[i][j];
+        if (a.bias) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) y[e] += nw0 + c + e < H ? a.bias[nw0 + c + e] : 0.0f;
+        }
+        if constexpr (SWIGLU) {
+          v4f up = acc[i + TN / 2][j];
+          if (a.bias) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) up[e] += nw0 + c + e < H ? a.bias[H + nw0 + c + e] : 0.0f;
+          }
+#pragma unroll
+          for (int e = 0; e < 4; ++e) y[e] = silu(y[e]) * up[e];
+        }
+        *reinterpret_cast<v4f*>(buf + ((j - j0) * 16 + (lane & 15)) * kRow + c) = y;
+      }
+    wave_sync();
+    for (int p = lane; p < 32 * kPieces; p += 64) {
+      const int row = p / kPieces, c = p % kPieces * PER, col = nw0 + c;
+      const int64_t m = out_row[wm + j0 * 16 + row];
+      if (m < 0 || col >= H) continue;
+      float y[PER];
+#pragma unroll
+      for (int e = 0; e < PER; ++e) y[e] = buf[row * kRow + c + e];
+      T* out = static_cast<T*>(a.out) + m * a.ldo + col;
+      const T* add = static_cast<const T*>(a.add) + m * a.ldadd + col;
+      if (vec && col + PER <= H) {
+        T v[PER];
+        if (a.add) {
+          __builtin_memcpy(v, __builtin_assume_aligned(add, 16), 16);
+#pragma unroll
+          for (int e = 0; e < PER; ++e) y[e] += to_f32<OUT>(v[e]);
+        }
+#pragma unroll
+        for (int e = 0; e < PER; ++e) v[e] = from_f32<OUT>(y[e]);
+        __builtin_memcpy(__builtin_assume_aligned(out, 16), v, 16);
+      } else {
+        for (int e = 0; e < PER && col + e < H; ++e) out[e] = from_f32<OUT>(a.add ? y[e] + to_f32<OUT>(add[e]) : y[e]);
+      }
+    }
+    wave_sync();
+  }
+}
+
 // ---------------------------------------------------------------------- host
 template <int OUT, bool SWIGLU, bool GROUPED, int RT, int TT, int WV>
 int launch_stream(const F8Args& a, hipStream_t st) {
@@ -405,13 +674,35 @@ int launch_stream(const F8Args& a, hipStream_t st) {
                 static_cast<uint32_t>(nx));
 }
 
+template <int BM, int BN, int WM, int WN, int NS, int OUT, bool SWIGLU, bool GROUPED>
+int launch_tile(const F8Args& a, hipStream_t st) {
+  static std::atomic<uint64_t> done{0};
+  constexpr int NB = SWIGLU ? 2 : BN > 128 ? BN / 128 : 1;
+  constexpr size_t fixed = NS * ((BM + BN) * 128 + BM * 4) + 256 + BM * 4, most = fixed + NB * 512 * 4;  // K <= 65536
+  static_assert(most <= 160 * 1024, "LDS of a CU");
+  if (!allow_lds(f8_tile_kernel<BM, BN, WM, WN, NS, OUT, SWIGLU, GROUPED>, most, done)) return hip_failed();
+  const size_t lds = fixed + NB * static_cast<size_t>((a.K + 8191) / 8192 * 64) * 4;
+  const int64_t bn = SWIGLU ? BN / 2 : BN, nn = ((SWIGLU ? a.N / 2 : a.N) + bn - 1) / bn;
+  const int64_t nm = GROUPED ? (a.M + static_cast<int64_t>(std::min(a.E, a.M)) * (BM - 1)) / BM : (a.M + BM - 1) / BM;
+  if (nm * nn > 0x7ffffff0) return MOE_EINVAL;
+  const uint32_t per = static_cast<uint32_t>((nm * nn + 7) / 8);
+  return launch(f8_tile_kernel<BM, BN, WM, WN, NS, OUT, SWIGLU, GROUPED>, per * 8, 64 * WM * WN, lds, st, a, static_cast<uint32_t>(nm),
+                static_cast<uint32_t>(nn), per);
+}
+
 template <int OUT, bool SWIGLU, bool GROUPED>
 int launch_product(const F8Args& a, hipStream_t st) {
   constexpr int R1 = SWIGLU ? 2 : 1;
   const int64_t rows = GROUPED ? (a.M + std::min(a.E, a.M) - 1) / std::min(a.E, a.M) : a.M;  // that share a weight
   if (rows <= 16) return launch_stream<OUT, SWIGLU, GROUPED, R1, 1, 16>(a, st);
   if (rows <= 32) return launch_stream<OUT, SWIGLU, GROUPED, R1, 2, 8>(a, st);
-  return launch_stream<OUT, SWIGLU, GROUPED, 2, 4, 8>(a, st);
+  if (rows <= 64) return launch_stream<OUT, SWIGLU, GROUPED, 2, 4, 8>(a, st);
+  if constexpr (OUT == MOE_F32) {
+    return launch_tile<128, 128, 2, 4, 2, OUT, SWIGLU, GROUPED>(a, st);
+  } else {
+    if (rows <= 256) return launch_tile<128, 128, 2, 4, 2, OUT, SWIGLU, GROUPED>(a, st);
+    return launch_tile<256, 256, 2, 4, 2, OUT, SWIGLU, GROUPED>(a, st);
+  }
 }
 template <bool GROUPED>
 int launch_product(const F8Args& a, int32_t out_type, bool swiglu, hipStream_t st) {
@@ -427,7 +718,7 @@ uint32_t list_groups(int64_t R) {  // workgroups: 4096 routes each, 256 at most
 bool product_ok(const void* a, int64_t lda, const float* sa, int64_t ldsa, const void* w, int64_t ldw, const float* sw, int32_t N,
                 int32_t K, int32_t act, const void* out, int32_t out_type, int64_t ldo) {
   return a && sa && w && sw && out && type_ok(out_type) && N >= 1 && N <= 1 << 20 && K >= 16 && K <= 65536 && lda >= K && ldw >= K &&
-         lda < kMaxLd && ldw < kMaxLd && ldsa < kMaxLd && ldsa >= (K + 127) / 128 && act >= 0 && act <= 1 &&
+         lda < kMaxLd && ldw < kMaxLd && ldsa < kMaxLd / 4 && ldsa >= (K + 127) / 128 && act >= 0 && act <= 1 &&
          !(act == 1 && N % 2) && ldo >= (act == 1 ? N / 2 : N) &&
          (reinterpret_cast<uintptr_t>(a) | reinterpret_cast<uintptr_t>(w) | lda | ldw | static_cast<uintptr_t>(K)) % 16 == 0;
 }
@@ -485,7 +776,7 @@ int moe_grouped_f8(const uint8_t* a, int64_t lda, const float* sa, int64_t ldsa,
       ldwe < (static_cast<int64_t>(N) - 1) * ldw + K || ldwe % 16 || a_rows < 1 || out_rows < 1)
     return MOE_EINVAL;
   if (o.gather || o.scatter ? !o.pairs_dev : o.pairs_dev != nullptr) return MOE_EINVAL;
-  if (o.gather ? a_rows * lda >= 1LL << 31 : a_rows < R) return MOE_EINVAL;
+  if (o.gather ? a_rows > 1LL << 26 || a_rows * lda >= 1LL << 31 || a_rows * ldsa >= 1LL << 29 : a_rows < R) return MOE_EINVAL;
   if (!o.scatter && out_rows < R) return MOE_EINVAL;
   F8Args r = {a,    w,    sa,  sw,      nullptr, nullptr, out,      offsets,
               o.pairs_dev, lda, ldw,    ldwe,    ldsa,    ldo,      0,       a_rows, out_rows, static_cast<int32_t>(R), N, K, E, o.gather, o.scatter};
