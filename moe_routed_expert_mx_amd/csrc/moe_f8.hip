@@ -469,47 +469,50 @@ __global__ __launch_bounds__(64 * WM * WN, 1) void f8_tile_kernel(F8Args a, uint
   };
   const v4i ra = make_rsrc(a.a + base * a.lda, static_cast<uint32_t>((extent_rows - 1) * a.lda + a.K));
   const v4i rs = make_rsrc(a.sa + base * a.ldsa, static_cast<uint32_t>(((extent_rows - 1) * a.ldsa + KB) * 4));
-  uint32_t va[RA], vw[RW], vs;
-  int ka[RA], kw[RW];  // the part's offset in the block
-  v4i rw[RW];
+  // parts of row r lie in the order place() gives, so that DMAs of even and of odd blocks of 8 rows differ: by 64 in k
+  const int kpart = ((lane & 7) ^ (lane >> 4)) * 16;
+  auto part_of = [&](int block) { return kpart ^ (block & 1) * 64; };
+  uint32_t va[GROUPED ? RA : 2], vw[2], vs;
+  if constexpr (GROUPED) {
 #pragma unroll
-  for (int i = 0; i < RA; ++i) {
-    const int r = (wave * RA + i) * 8 + (lane >> 3);
-    const uint32_t at = row_in(r);
-    ka[i] = place(r, lane & 7) * 16;
-    va[i] = at != ~0u ? at * static_cast<uint32_t>(a.lda) + ka[i] : kOutside;
+    for (int i = 0; i < RA; ++i) {
+      const uint32_t at = row_in((wave * RA + i) * 8 + (lane >> 3));
+      va[i] = at != ~0u ? at * static_cast<uint32_t>(a.lda) + part_of(wave * RA + i) : kOutside;
+    }
+  } else {
+    // (rows behind the last lie behind the extent)
+#pragma unroll
+    for (int i = 0; i < 2; ++i) va[i] = (lane >> 3) * static_cast<uint32_t>(a.lda) + part_of(wave * RA + i);
   }
+#pragma unroll
+  for (int i = 0; i < 2; ++i) vw[i] = (lane >> 3) * static_cast<uint32_t>(a.ldw) + part_of(wave * RW + i);
   {
     const uint32_t at = wave < BM / 64 ? row_in(wave * 64 + lane) : ~0u;
     vs = at != ~0u ? at * static_cast<uint32_t>(a.ldsa) * 4u : kOutside;
   }
-  {
-    const int nrows = H - n0 < kCols ? H - n0 : kCols;
-    const uint32_t bytes = static_cast<uint32_t>((nrows - 1) * a.ldw + a.K);
-    const uint8_t* const w = a.w + unit.e * a.ldwe + static_cast<int64_t>(n0) * a.ldw;
-#pragma unroll
-    for (int i = 0; i < RW; ++i) {
-      // SwiGLU: a wave's gate rows, then its up rows
-      const int first = (wave * RW + i) * 8, slot = first + (lane >> 3), half = SWIGLU ? first / (kWaveRows / 2) & 1 : 0;
-      const int row = SWIGLU ? slot / kWaveRows * (kWaveRows / 2) + slot % (kWaveRows / 2) : slot;
-      kw[i] = place(slot, lane & 7) * 16;
-      rw[i] = make_rsrc(w + static_cast<int64_t>(half) * H * a.ldw, bytes);
-      vw[i] = row < nrows ? static_cast<uint32_t>(row) * static_cast<uint32_t>(a.ldw) + kw[i] : kOutside;
-    }
-  }
+  const int nrows = H - n0 < kCols ? H - n0 : kCols;
+  const uint8_t* const w = a.w + unit.e * a.ldwe + static_cast<int64_t>(n0) * a.ldw;
+  const v4i rw = make_rsrc(w, static_cast<uint32_t>((nrows - 1) * a.ldw + a.K));
+  const v4i ru = SWIGLU ? make_rsrc(w + static_cast<int64_t>(H) * a.ldw, static_cast<uint32_t>((nrows - 1) * a.ldw + a.K)) : rw;
   // DMA d of this wave for stage s into the LDS at buf; parts behind K, and whole stages behind it, are zeros (with no
   // scalar offset then: nothing says that the bounds check's difference does not wrap)
   auto issue = [&](int s, int buf, int d) {
-    const int k0 = s * 128;
-    const bool in = k0 < a.K;
-    const uint32_t soff = in ? k0 : 0;
+    const int left = a.K - s * 128;
+    const uint32_t soff = left > 0 ? s * 128 : 0;
     if (d < RA) {
-      dma16(ra, k0 + ka[d] < a.K ? va[d] : kOutside, soff, lds0 + buf + (wave * RA + d) * 1024);
+      const int block = wave * RA + d;
+      uint32_t v;
+      if constexpr (GROUPED) v = va[d];
+      else v = va[d & 1] + static_cast<uint32_t>(block * 8) * static_cast<uint32_t>(a.lda);
+      dma16(ra, part_of(block) < left ? v : kOutside, soff, lds0 + buf + block * 1024);
     } else if (d < RA + RW) {
-      d -= RA;
-      dma16(rw[d], k0 + kw[d] < a.K ? vw[d] : kOutside, soff, lds0 + buf + BM * 128 + (wave * RW + d) * 1024);
+      // SwiGLU: a wave's gate rows, then its up rows
+      const int block = wave * RW + d - RA, slot = block * 8, half = SWIGLU ? slot / (kWaveRows / 2) & 1 : 0;
+      const int row = SWIGLU ? slot / kWaveRows * (kWaveRows / 2) + slot % (kWaveRows / 2) : slot;
+      const uint32_t v = vw[(d - RA) & 1] + static_cast<uint32_t>(row) * static_cast<uint32_t>(a.ldw);
+      dma16(half ? ru : rw, part_of(block) < left ? v : kOutside, soff, lds0 + buf + BM * 128 + block * 1024);
     } else {
-      dma4s(rs, in ? vs : kOutside, in ? s * 4 : 0, lds0 + (wave < BM / 64 ? buf + kRows + wave * 256 : kDummy));
+      dma4s(rs, left > 0 ? vs : kOutside, left > 0 ? s * 4 : 0, lds0 + (wave < BM / 64 ? buf + kRows + wave * 256 : kDummy));
     }
   };
 
@@ -521,14 +524,13 @@ __global__ __launch_bounds__(64 * WM * WN, 1) void f8_tile_kernel(F8Args a, uint
   };
   v4f acc[TN][TM] = {};
   typename Op::T fa[TM], fw[2];
-  float sa[TM], sw[2];
+  float sa[TM];
   const float* const wscale = reinterpret_cast<const float*>(smem + kScales) + (SWIGLU ? 0 : wn / 128 * KBP);
-  auto read_scales = [&](int buf, int s) {
+  // the factors of the rows for stage s, gate (half 0) or up rows
+  auto read_scales = [&](int buf, int s, int half) {
+    const float f = wscale[(s < KB ? s : KB - 1) + half * KBP];
 #pragma unroll
-    for (int j = 0; j < TM; ++j) sa[j] = *reinterpret_cast<const float*>(smem + buf + kRows + (wm + j * 16 + (lane & 15)) * 4);
-    s = s < KB ? s : KB - 1;
-    sw[0] = wscale[s];
-    if (SWIGLU) sw[1] = wscale[KBP + s];
+    for (int j = 0; j < TM; ++j) sa[j] = *reinterpret_cast<const float*>(smem + buf + kRows + (wm + j * 16 + (lane & 15)) * 4) * f;
   };
   // the weight's scales first
   {
@@ -553,16 +555,14 @@ __global__ __launch_bounds__(64 * WM * WN, 1) void f8_tile_kernel(F8Args a, uint
 #pragma unroll
   for (int j = 0; j < TM; ++j) fa[j] = operand((wm + j * 16) * 128);
   fw[0] = operand((BM + wn) * 128);
-  read_scales(0, 0);
+  read_scales(0, 0, 0);
   int prev = (NS - 1) * kStage, cur = 0;  // LDS offsets of stages s - 1 and s
   for (int s = 0; s < KB; ++s) {
     const int next = cur + kStage == NS * kStage ? 0 : cur + kStage;
     v4f d[kLag + 1];
     auto add = [&](int m) {  // product m of the block
-      const int i = m / TM, j = m % TM;
-      const float f = sa[j] * sw[SWIGLU && i >= TN / 2 ? 1 : 0];
 #pragma unroll
-      for (int x = 0; x < 4; ++x) acc[i][j][x] = __builtin_fmaf(d[m % (kLag + 1)][x], f, acc[i][j][x]);
+      for (int x = 0; x < 4; ++x) acc[m / TM][m % TM][x] = __builtin_fmaf(d[m % (kLag + 1)][x], sa[m % TM], acc[m / TM][m % TM][x]);
     };
 #pragma unroll
     for (int i = 0; i < TN; ++i) {
@@ -581,6 +581,8 @@ __global__ __launch_bounds__(64 * WM * WN, 1) void f8_tile_kernel(F8Args a, uint
         d[m % (kLag + 1)] = Op::product(fw[i & 1], fa[j]);
         if (i == TN - 1) fa[j] = operand(next + (wm + j * 16) * 128);
         if (m >= kLag) add(m - kLag);
+        if (SWIGLU && m == TN / 2 * TM + kLag - 1) read_scales(cur, s, 1);  // behind the last gate row's sums
+        __builtin_amdgcn_sched_barrier(0);
       }
       const int p = (i + 1) % TN;
 #pragma unroll
@@ -592,7 +594,7 @@ __global__ __launch_bounds__(64 * WM * WN, 1) void f8_tile_kernel(F8Args a, uint
     }
 #pragma unroll
     for (int m = TN * TM - kLag; m < TN * TM; ++m) add(m);
-    read_scales(next, s + 1);
+    read_scales(next, s + 1, 0);
     prev = cur;
     cur = next;
     compiler_fence();
