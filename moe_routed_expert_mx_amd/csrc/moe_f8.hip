@@ -524,13 +524,15 @@ __global__ __launch_bounds__(64 * WM * WN, 1) void f8_tile_kernel(F8Args a, uint
   };
   v4f acc[TN][TM] = {};
   typename Op::T fa[TM], fw[2];
-  float sa[TM];
+  float sa[TM], sw[2];
   const float* const wscale = reinterpret_cast<const float*>(smem + kScales) + (SWIGLU ? 0 : wn / 128 * KBP);
-  // the factors of the rows for stage s, gate (half 0) or up rows
-  auto read_scales = [&](int buf, int s, int half) {
-    const float f = wscale[(s < KB ? s : KB - 1) + half * KBP];
+  // a's scales of the stage at buf, and the weight's: of the gate rows, and of the up rows
+  auto read_scales = [&](int buf, int s) {
 #pragma unroll
-    for (int j = 0; j < TM; ++j) sa[j] = *reinterpret_cast<const float*>(smem + buf + kRows + (wm + j * 16 + (lane & 15)) * 4) * f;
+    for (int j = 0; j < TM; ++j) sa[j] = *reinterpret_cast<const float*>(smem + buf + kRows + (wm + j * 16 + (lane & 15)) * 4);
+    s = s < KB ? s : KB - 1;
+    sw[0] = wscale[s];
+    if (SWIGLU) sw[1] = wscale[KBP + s];
   };
   // the weight's scales first
   {
@@ -542,27 +544,37 @@ __global__ __launch_bounds__(64 * WM * WN, 1) void f8_tile_kernel(F8Args a, uint
            lds0 + kScales + (h * KBP + k) * 4);
     }
   }
-  // a stage's DMAs are issued behind the rows of products that follow its buffer's release
-  auto slot = [](int p) { return p * kIssue / TN; };
+  // a stage's DMAs are issued one by one behind the products that follow its buffer's release, the last of them
+  // when three quarters of a stage are done
+  constexpr int kAll = TN * TM;
+  auto slot = [](int q) { return q * 4 / 3 * kIssue / kAll < kIssue ? q * 4 / 3 * kIssue / kAll : kIssue; };
 #pragma unroll
   for (int s = 0; s < NS; ++s) {
 #pragma unroll
-    for (int d = 0; d < (s < NS - 1 ? kIssue : slot(1)); ++d) issue(s, s * kStage, d);
+    for (int d = 0; d < (s < NS - 1 ? kIssue : slot(TM)); ++d) issue(s, s * kStage, d);
   }
-  wait_vm<kIssue*(NS - 2) + slot(1)>();
+  wait_vm<kIssue*(NS - 2) + slot(TM)>();
   __builtin_amdgcn_s_barrier();
   compiler_fence();
 #pragma unroll
   for (int j = 0; j < TM; ++j) fa[j] = operand((wm + j * 16) * 128);
   fw[0] = operand((BM + wn) * 128);
-  read_scales(0, 0, 0);
+  read_scales(0, 0);
   int prev = (NS - 1) * kStage, cur = 0;  // LDS offsets of stages s - 1 and s
   for (int s = 0; s < KB; ++s) {
     const int next = cur + kStage == NS * kStage ? 0 : cur + kStage;
     v4f d[kLag + 1];
     auto add = [&](int m) {  // product m of the block
+      const int i = m / TM, j = m % TM;
+      float f;
+      if constexpr (SWIGLU) {
+        f = sa[j] * sw[i >= TN / 2];
+      } else {
+        if (i == 0) sa[j] *= sw[0];
+        f = sa[j];
+      }
 #pragma unroll
-      for (int x = 0; x < 4; ++x) acc[m / TM][m % TM][x] = __builtin_fmaf(d[m % (kLag + 1)][x], sa[m % TM], acc[m / TM][m % TM][x]);
+      for (int x = 0; x < 4; ++x) acc[i][j][x] = __builtin_fmaf(d[m % (kLag + 1)][x], f, acc[i][j][x]);
     };
 #pragma unroll
     for (int i = 0; i < TN; ++i) {
@@ -574,27 +586,26 @@ __global__ __launch_bounds__(64 * WM * WN, 1) void f8_tile_kernel(F8Args a, uint
         compiler_fence();
         __builtin_amdgcn_sched_barrier(0);
       }
+      if (SWIGLU) asm volatile("" : "+v"(sw[0]), "+v"(sw[1]));  // (the factors are made again for each row: registers)
       fw[(i + 1) & 1] = operand((i == TN - 1 ? next : cur) + (BM + wn + (i + 1) % TN * 16) * 128);
 #pragma unroll
       for (int j = 0; j < TM; ++j) {
-        const int m = i * TM + j;
+        const int m = i * TM + j, q = (m + TM) % kAll;
         d[m % (kLag + 1)] = Op::product(fw[i & 1], fa[j]);
+        __builtin_amdgcn_sched_barrier(0);
         if (i == TN - 1) fa[j] = operand(next + (wm + j * 16) * 128);
         if (m >= kLag) add(m - kLag);
-        if (SWIGLU && m == TN / 2 * TM + kLag - 1) read_scales(cur, s, 1);  // behind the last gate row's sums
+#pragma unroll
+        for (int x = slot(q); x < slot(q + 1); ++x) {
+          if (i == TN - 1) issue(s + NS, cur, x);
+          else issue(s + NS - 1, prev, x);
+        }
         __builtin_amdgcn_sched_barrier(0);
       }
-      const int p = (i + 1) % TN;
-#pragma unroll
-      for (int x = slot(p); x < slot(p + 1); ++x) {
-        if (i == TN - 1) issue(s + NS, cur, x);
-        else issue(s + NS - 1, prev, x);
-      }
-      __builtin_amdgcn_sched_barrier(0);
     }
 #pragma unroll
-    for (int m = TN * TM - kLag; m < TN * TM; ++m) add(m);
-    read_scales(next, s + 1, 0);
+    for (int m = kAll - kLag; m < kAll; ++m) add(m);
+    read_scales(next, s + 1);
     prev = cur;
     cur = next;
     compiler_fence();
