@@ -3,6 +3,7 @@
 // expert, behind the C ABI of include/moe_mx.h.
 #include <algorithm>
 #include <cstring>
+#include <type_traits>
 
 #include "dense_common.h"
 
@@ -429,17 +430,19 @@ __global__ __launch_bounds__(64 * WM * WN, 1) void f8_tile_kernel(F8Args a, uint
   constexpr int RA = BM / 8 / NW, RW = BN / 8 / NW, kIssue = RA + RW + 1;  // DMAs of a wave: 8 rows each, and scales
   constexpr int TM = BM / WM / 16, TN = BN / WN / 16, kWaveRows = BN / WN;
   constexpr int NB = SWIGLU ? 2 : BN > 128 ? BN / 128 : 1;  // scale blocks of the weight
-  static_assert(BM % (8 * NW) == 0 && BN % (8 * NW) == 0 && BM / 64 <= NW && TN % 2 == 0 && kWaveRows <= 128, "whole DMAs, whole blocks");
+  static_assert(BM % (8 * NW) == 0 && BN % (8 * NW) == 0 && BM / 64 <= NW && TN % 2 == 0 && TM % 2 == 0 && kWaveRows <= 128, "whole DMAs, whole blocks");
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int H = SWIGLU ? a.N / 2 : a.N, KB = (a.K + 127) / 128, KBP = (KB + 63) / 64 * 64;
-  constexpr int kLag = 2;  // a product is scaled and added behind the second one after it
+  constexpr int kLag = 2;     // a product is scaled and added behind the second one after it
+  constexpr int kSpread = 4;  // a stage's DMAs go out in the first quarter of the time that they have
   constexpr int kCols = SWIGLU ? BN / 2 : BN;
   // each XCD (workgroups go round the eight) takes a contiguous range of tiles: what runs at once on an XCD
   // shares operands in its L2
   Unit unit;
   int n0;
   if constexpr (GROUPED) {
-    const uint32_t tiles = count_units<BM>(a) * nn, per = (tiles + 7) / 8, tile = blockIdx.x % 8 * per + blockIdx.x / 8;
+    const uint32_t units = count_units<BM>(a);  // (lists that overlap could have more than the grid was made for)
+    const uint32_t tiles = (units < nm ? units : nm) * nn, per = (tiles + 7) / 8, tile = blockIdx.x % 8 * per + blockIdx.x / 8;
     if (blockIdx.x / 8 >= per || tile >= tiles || !find_unit<BM>(a, tile / nn, unit)) return;
     n0 = static_cast<int>(tile % nn) * kCols;
   } else {
@@ -494,25 +497,39 @@ __global__ __launch_bounds__(64 * WM * WN, 1) void f8_tile_kernel(F8Args a, uint
   const uint8_t* const w = a.w + unit.e * a.ldwe + static_cast<int64_t>(n0) * a.ldw;
   const v4i rw = make_rsrc(w, static_cast<uint32_t>((nrows - 1) * a.ldw + a.K));
   const v4i ru = SWIGLU ? make_rsrc(w + static_cast<int64_t>(H) * a.ldw, static_cast<uint32_t>((nrows - 1) * a.ldw + a.K)) : rw;
-  // DMA d of this wave for stage s into the LDS at buf; parts behind K, and whole stages behind it, are zeros (with no
-  // scalar offset then: nothing says that the bounds check's difference does not wrap)
-  auto issue = [&](int s, int buf, int d) {
+  // What stage s adds to the offsets of even and of odd blocks: parts behind K, and whole stages behind it, are
+  // outside, which makes them zeros (with no scalar offset then: nothing says that the bounds check's difference does
+  // not wrap).
+  struct Stage {
+    uint32_t out[2], soff, scale;
+    bool in;
+  };
+  auto stage = [&](int s) {
     const int left = a.K - s * 128;
-    const uint32_t soff = left > 0 ? s * 128 : 0;
+    Stage r;
+    r.in = left > 0;
+    r.soff = r.in ? s * 128 : 0;
+    r.scale = r.in ? s * 4 : 0;
+    r.out[0] = kpart < left ? 0 : kOutside;
+    r.out[1] = (kpart ^ 64) < left ? 0 : kOutside;
+    return r;
+  };
+  // DMA d of this wave for a stage into the LDS at buf
+  auto issue = [&](const Stage& s, int buf, int d) {
     if (d < RA) {
       const int block = wave * RA + d;
       uint32_t v;
       if constexpr (GROUPED) v = va[d];
       else v = va[d & 1] + static_cast<uint32_t>(block * 8) * static_cast<uint32_t>(a.lda);
-      dma16(ra, part_of(block) < left ? v : kOutside, soff, lds0 + buf + block * 1024);
+      dma16(ra, v | s.out[block & 1], s.soff, lds0 + buf + block * 1024);
     } else if (d < RA + RW) {
       // SwiGLU: a wave's gate rows, then its up rows
       const int block = wave * RW + d - RA, slot = block * 8, half = SWIGLU ? slot / (kWaveRows / 2) & 1 : 0;
       const int row = SWIGLU ? slot / kWaveRows * (kWaveRows / 2) + slot % (kWaveRows / 2) : slot;
       const uint32_t v = vw[(d - RA) & 1] + static_cast<uint32_t>(row) * static_cast<uint32_t>(a.ldw);
-      dma16(half ? ru : rw, part_of(block) < left ? v : kOutside, soff, lds0 + buf + BM * 128 + block * 1024);
+      dma16(half ? ru : rw, v | s.out[block & 1], s.soff, lds0 + buf + BM * 128 + block * 1024);
     } else {
-      dma4s(rs, left > 0 ? vs : kOutside, left > 0 ? s * 4 : 0, lds0 + (wave < BM / 64 ? buf + kRows + wave * 256 : kDummy));
+      dma4s(rs, s.in ? vs : kOutside, s.scale, lds0 + (wave < BM / 64 ? buf + kRows + wave * 256 : kDummy));
     }
   };
 
@@ -523,13 +540,17 @@ __global__ __launch_bounds__(64 * WM * WN, 1) void f8_tile_kernel(F8Args a, uint
     return Op::make(*reinterpret_cast<const v4i*>(smem + at + la0), *reinterpret_cast<const v4i*>(smem + at + la1));
   };
   v4f acc[TN][TM] = {};
-  typename Op::T fa[TM], fw[2];
-  float sa[TM], sw[2];
+  // The weight rows of a block are held, and replaced by the next block's as the last tile leaves them; a's come 16 at
+  // a time, a tile ahead.
+  typename Op::T fa[2], fw[TN];
+  float sa[2], sw[2];
   const float* const wscale = reinterpret_cast<const float*>(smem + kScales) + (SWIGLU ? 0 : wn / 128 * KBP);
-  // a's scales of the stage at buf, and the weight's: of the gate rows, and of the up rows
-  auto read_scales = [&](int buf, int s) {
-#pragma unroll
-    for (int j = 0; j < TM; ++j) sa[j] = *reinterpret_cast<const float*>(smem + buf + kRows + (wm + j * 16 + (lane & 15)) * 4);
+  auto read_a = [&](int buf, int j) {
+    fa[j & 1] = operand(buf + (wm + j * 16) * 128);
+    sa[j & 1] = *reinterpret_cast<const float*>(smem + buf + kRows + (wm + j * 16 + (lane & 15)) * 4);
+  };
+  auto read_w = [&](int buf, int i) { fw[i] = operand(buf + (BM + wn + i * 16) * 128); };
+  auto read_sw = [&](int s) {  // of the gate rows, and of the up rows
     s = s < KB ? s : KB - 1;
     sw[0] = wscale[s];
     if (SWIGLU) sw[1] = wscale[KBP + s];
@@ -544,68 +565,65 @@ __global__ __launch_bounds__(64 * WM * WN, 1) void f8_tile_kernel(F8Args a, uint
            lds0 + kScales + (h * KBP + k) * 4);
     }
   }
-  // a stage's DMAs are issued one by one behind the products that follow its buffer's release, the last of them
-  // when three quarters of a stage are done
-  constexpr int kAll = TN * TM;
-  auto slot = [](int q) { return q * 4 / 3 * kIssue / kAll < kIssue ? q * 4 / 3 * kIssue / kAll : kIssue; };
+  // a stage's DMAs are issued one by one behind the products that follow its buffer's release
+  constexpr int kAll = TN * TM, kFree = (TM - 1) * TN;  // products of a block; those before the release
+  auto slot = [](int q) { return q * kSpread * kIssue / kAll < kIssue ? q * kSpread * kIssue / kAll : kIssue; };
 #pragma unroll
   for (int s = 0; s < NS; ++s) {
+    const Stage st = stage(s);
 #pragma unroll
-    for (int d = 0; d < (s < NS - 1 ? kIssue : slot(TM)); ++d) issue(s, s * kStage, d);
+    for (int d = 0; d < (s < NS - 1 ? kIssue : slot(kAll - kFree)); ++d) issue(st, s * kStage, d);
   }
-  wait_vm<kIssue*(NS - 2) + slot(TM)>();
+  wait_vm<kIssue*(NS - 2) + slot(kAll - kFree)>();
   __builtin_amdgcn_s_barrier();
   compiler_fence();
 #pragma unroll
-  for (int j = 0; j < TM; ++j) fa[j] = operand((wm + j * 16) * 128);
-  fw[0] = operand((BM + wn) * 128);
-  read_scales(0, 0);
+  for (int i = 0; i < TN; ++i) read_w(0, i);
+  read_sw(0);
+  read_a(0, 0);
   int prev = (NS - 1) * kStage, cur = 0;  // LDS offsets of stages s - 1 and s
   for (int s = 0; s < KB; ++s) {
     const int next = cur + kStage == NS * kStage ? 0 : cur + kStage;
+    Stage st = stage(s + NS - 1);
     v4f d[kLag + 1];
+    float f[2], g[2];  // of the tile before and of this one
     auto add = [&](int m) {  // product m of the block
-      const int i = m / TM, j = m % TM;
-      float f;
-      if constexpr (SWIGLU) {
-        f = sa[j] * sw[i >= TN / 2];
-      } else {
-        if (i == 0) sa[j] *= sw[0];
-        f = sa[j];
-      }
+      const int j = m / TN, i = m % TN;
+      const float x = SWIGLU && i >= TN / 2 ? g[j & 1] : f[j & 1];
 #pragma unroll
-      for (int x = 0; x < 4; ++x) acc[i][j][x] = __builtin_fmaf(d[m % (kLag + 1)][x], f, acc[i][j][x]);
+      for (int e = 0; e < 4; ++e) acc[i][j][e] = __builtin_fmaf(d[m % (kLag + 1)][e], x, acc[i][j][e]);
     };
 #pragma unroll
-    for (int i = 0; i < TN; ++i) {
-      if (i == TN - 1) {
-        // this stage is read out and the next has landed, for every wave
+    for (int j = 0; j < TM; ++j) {
+      f[j & 1] = sa[j & 1] * sw[0];
+      if (SWIGLU) g[j & 1] = sa[j & 1] * sw[1];
+      if (j == TM - 1) {
+        // this stage is read out (but for what the products to come hold) and the next has landed, for every wave
         asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
         wait_vm<kIssue*(NS - 2)>();
         __builtin_amdgcn_s_barrier();
         compiler_fence();
         __builtin_amdgcn_sched_barrier(0);
+        st = stage(s + NS);
+        read_sw(s + 1);
+        read_a(next, 0);
+      } else {
+        read_a(cur, j + 1);
       }
-      if (SWIGLU) asm volatile("" : "+v"(sw[0]), "+v"(sw[1]));  // (the factors are made again for each row: registers)
-      fw[(i + 1) & 1] = operand((i == TN - 1 ? next : cur) + (BM + wn + (i + 1) % TN * 16) * 128);
 #pragma unroll
-      for (int j = 0; j < TM; ++j) {
-        const int m = i * TM + j, q = (m + TM) % kAll;
-        d[m % (kLag + 1)] = Op::product(fw[i & 1], fa[j]);
+      for (int i = 0; i < TN; ++i) {
+        const int m = j * TN + i, q = (m - kFree + kAll) % kAll;
+        d[m % (kLag + 1)] = Op::product(fw[i], fa[j & 1]);
         __builtin_amdgcn_sched_barrier(0);
-        if (i == TN - 1) fa[j] = operand(next + (wm + j * 16) * 128);
+        if (j == TM - 1) read_w(next, i);
         if (m >= kLag) add(m - kLag);
 #pragma unroll
-        for (int x = slot(q); x < slot(q + 1); ++x) {
-          if (i == TN - 1) issue(s + NS, cur, x);
-          else issue(s + NS - 1, prev, x);
-        }
+        for (int x = slot(q); x < slot(q + 1); ++x) issue(st, m >= kFree ? cur : prev, x);
         __builtin_amdgcn_sched_barrier(0);
       }
     }
 #pragma unroll
     for (int m = kAll - kLag; m < kAll; ++m) add(m);
-    read_scales(next, s + 1);
     prev = cur;
     cur = next;
     compiler_fence();
@@ -710,10 +728,22 @@ int launch_product(const F8Args& a, hipStream_t st) {
   if (rows <= 16) return launch_stream<OUT, SWIGLU, GROUPED, R1, 1, 16>(a, st);
   if (rows <= 32) return launch_stream<OUT, SWIGLU, GROUPED, R1, 2, 8>(a, st);
   if (rows <= 64) return launch_stream<OUT, SWIGLU, GROUPED, 2, 4, 8>(a, st);
-  if constexpr (OUT == MOE_F32) {
-    return launch_tile<128, 128, 2, 4, 2, OUT, SWIGLU, GROUPED>(a, st);
-  } else {
-    if (rows <= 256) return launch_tile<128, 128, 2, 4, 2, OUT, SWIGLU, GROUPED>(a, st);
+  // Rounds of tiles over 256 CUs, weighed with a round's time at K = 4096 (us): large tiles move fewer bytes for each
+  // product, small ones fill the CUs.  Two of the smallest fit a CU.
+  const int64_t cols = SWIGLU ? a.N / 2 : a.N;
+  auto tiles = [&](int bm, int bn) {
+    const int64_t b = SWIGLU ? bn / 2 : bn;
+    // (grouped: on average half a tile of each expert is empty)
+    return (GROUPED ? a.M / bm + (std::min(a.E, a.M) + 1) / 2 : (a.M + bm - 1) / bm) * ((cols + b - 1) / b);
+  };
+  const int64_t n0 = tiles(64, 128), c0 = n0 <= 256 ? 20 : (n0 + 511) / 512 * 25, c1 = (tiles(128, 128) + 255) / 256 * 24,
+                c2 = (tiles(128, 256) + 255) / 256 * 39, c3 = (tiles(256, 256) + 255) / 256 * 65;
+  if (OUT == MOE_F32 || std::min(c0, c1) <= std::min(c2, c3)) {
+    if (c0 < c1) return launch_tile<64, 128, 2, 2, 3, OUT, SWIGLU, GROUPED>(a, st);
+    return launch_tile<128, 128, 4, 2, 4, OUT, SWIGLU, GROUPED>(a, st);
+  }
+  if constexpr (OUT != MOE_F32) {
+    if (c2 < c3) return launch_tile<128, 256, 2, 4, 3, OUT, SWIGLU, GROUPED>(a, st);
     return launch_tile<256, 256, 2, 4, 2, OUT, SWIGLU, GROUPED>(a, st);
   }
 }
