@@ -733,28 +733,35 @@ template <int OUT, bool SWIGLU, bool GROUPED>
 int launch_product(const F8Args& a, hipStream_t st) {
   constexpr int R1 = SWIGLU ? 2 : 1;
   const int64_t rows = GROUPED ? (a.M + std::min(a.E, a.M) - 1) / std::min(a.E, a.M) : a.M;  // that share a weight
-  // Few blocks of K leave nothing to split: where the rows fill the CUs (of 32, over four waves each), every wave takes
-  // a tile of its own (experts of 1 and of 64 tokens, 3584 x 384 and 3584 x 256: 33 and 360 us with K split)
-  const int64_t met = GROUPED ? std::min(a.E, a.M) : 1, cut = a.N / 32;
-  if (a.K <= 1024 && rows <= 32 && met * cut >= 1024) {
-    if (rows <= 16) return launch_stream<OUT, SWIGLU, GROUPED, 2, 1, 4, 1>(a, st);
-    return launch_stream<OUT, SWIGLU, GROUPED, 2, 2, 4, 1>(a, st);
-  }
-  if (rows <= 16) return launch_stream<OUT, SWIGLU, GROUPED, R1, 1, 16>(a, st);
-  if (rows <= 32) return launch_stream<OUT, SWIGLU, GROUPED, R1, 2, 8>(a, st);
-  if (rows <= 64) return launch_stream<OUT, SWIGLU, GROUPED, 2, 4, 8>(a, st);
-  // Rounds of tiles over 256 CUs, weighed with a round's time at K = 4096 (us): large tiles move fewer bytes for each
-  // product, small ones fill the CUs.  Two of the smallest fit a CU.
   const int64_t cols = SWIGLU ? a.N / 2 : a.N;
   auto tiles = [&](int bm, int bn) {
     const int64_t b = SWIGLU ? bn / 2 : bn;
-    // (grouped: on average half a tile of each expert is empty)
-    return (GROUPED ? a.M / bm + (std::min(a.E, a.M) + 1) / 2 : (a.M + bm - 1) / bm) * ((cols + b - 1) / b);
+    // (grouped: as if the experts had equal shares)
+    return (GROUPED ? std::min(a.E, a.M) * ((rows + bm - 1) / bm) : (a.M + bm - 1) / bm) * ((cols + b - 1) / b);
   };
-  const int64_t n0 = tiles(64, 128), c0 = n0 <= 256 ? 20 : (n0 + 511) / 512 * 25, c1 = (tiles(128, 128) + 255) / 256 * 24,
+  const int64_t n0 = tiles(64, 128), met = GROUPED ? std::min(a.E, a.M) : 1;
+  const bool shallow = a.K <= 1024;  // few blocks of K: nothing to split among waves, little to keep in flight
+  // The streaming kernel where the smallest tiles leave CUs idle, or hardly any row shares a weight.  Experts of 3584 x
+  // 384 (160, 16 a token) took, us: both products of one token 12 and 6 with it, 19 and 7 with tiles; of 8 tokens 58 and
+  // 27, 41 and 29; of 50 tokens 115 and 49, 79 and 47.
+  if (shallow && rows <= 4 && met * (a.N / 32) >= 1024) return launch_stream<OUT, SWIGLU, GROUPED, 2, 1, 4, 1>(a, st);
+  if (rows <= 64 && n0 < 256) {
+    if (rows <= 16) return GROUPED ? launch_stream<OUT, SWIGLU, GROUPED, 2, 1, 8, 4>(a, st)
+                                   : launch_stream<OUT, SWIGLU, GROUPED, R1, 1, 16>(a, st);
+    if (rows <= 32) return launch_stream<OUT, SWIGLU, GROUPED, R1, 2, 8>(a, st);
+    return launch_stream<OUT, SWIGLU, GROUPED, 2, 4, 8>(a, st);
+  }
+  // Rounds of tiles over 256 CUs, weighed with a round's time at K = 4096 (us): large tiles move fewer bytes for each
+  // product, small ones fill the CUs.  Two or three of the smallest fit a CU.
+  const int64_t c0 = n0 <= 256 ? 20 : (n0 + 511) / 512 * 25, c1 = (tiles(128, 128) + 255) / 256 * 24,
                 c2 = (tiles(128, 256) + 255) / 256 * 39, c3 = (tiles(256, 256) + 255) / 256 * 65;
   if (OUT == MOE_F32 || std::min(c0, c1) <= std::min(c2, c3)) {
-    if (c0 < c1) return launch_tile<64, 128, 2, 2, 3, OUT, SWIGLU, GROUPED>(a, st);
+    if (c0 < c1) {
+      // two stages: three workgroups a CU (50 tokens' second product 47 us, against 53 with three stages and two
+      // workgroups; their first one 94 against 79, 8 tokens' first one, 540 tiles, 41 against 48)
+      if (shallow || (n0 > 512 && n0 <= 768)) return launch_tile<64, 128, 2, 2, 2, OUT, SWIGLU, GROUPED>(a, st);
+      return launch_tile<64, 128, 2, 2, 3, OUT, SWIGLU, GROUPED>(a, st);
+    }
     return launch_tile<128, 128, 4, 2, 4, OUT, SWIGLU, GROUPED>(a, st);
   }
   if constexpr (OUT != MOE_F32) {

@@ -3,6 +3,7 @@
 // the C ABI of include/moe_mx.h.
 #include <cmath>
 #include <cstring>
+#include <type_traits>
 
 #include "dense_common.h"
 
@@ -21,19 +22,6 @@ __device__ __forceinline__ void load8(float (&v)[VE], const typename Elem<TYPE>:
   }
 #pragma unroll
   for (int e = 0; e < VE; ++e) v[e] = to_f32<TYPE>(t[e]);
-}
-template <int TYPE>
-__device__ __forceinline__ void store8(typename Elem<TYPE>::T* p, int i, int K, const float (&v)[VE]) {
-  typename Elem<TYPE>::T t[VE];
-#pragma unroll
-  for (int e = 0; e < VE; ++e) t[e] = from_f32<TYPE>(v[e]);
-  if ((i + 1) * VE <= K) {
-    __builtin_memcpy(p + i * VE, t, sizeof(t));
-  } else {
-#pragma unroll
-    for (int e = 0; e < VE; ++e)
-      if (i * VE + e < K) p[i * VE + e] = t[e];
-  }
 }
 __device__ __forceinline__ void store_codes(uint8_t* p, int i, int K, const uint32_t (&c)[2]) {
   if ((i + 1) * VE <= K) {
@@ -123,7 +111,57 @@ struct NormArgs {
   int32_t M, K, format;
 };
 
-// W waves a row, which they hold in registers as FP32: NV pieces of 8 elements a lane.  One pass over
+// Two values as 16-bit ones in a word.
+template <int TYPE>
+__device__ __forceinline__ uint32_t pack2(float a, float b) {
+  typedef std::conditional_t<TYPE == MOE_BF16, __bf16, _Float16> E;
+  typedef E v2 __attribute__((ext_vector_type(2)));
+  const v2 v = {static_cast<E>(a), static_cast<E>(b)};
+  uint32_t w;
+  __builtin_memcpy(&w, &v, 4);
+  return w;
+}
+// 8 elements as they lie in memory.
+template <int TYPE>
+struct Piece {
+  static constexpr int N = TYPE == MOE_F32 ? 8 : 4;
+  uint32_t w[N];
+  __device__ __forceinline__ float at(int e) const {
+    if constexpr (TYPE == MOE_F32) return __uint_as_float(w[e]);
+    else return to_f32<TYPE>(static_cast<uint16_t>(e & 1 ? w[e >> 1] >> 16 : w[e >> 1]));
+  }
+  __device__ __forceinline__ void set2(int e, float a, float b) {
+    if constexpr (TYPE == MOE_F32) {
+      w[e] = __float_as_uint(a);
+      w[e + 1] = __float_as_uint(b);
+    } else {
+      w[e >> 1] = pack2<TYPE>(a, b);
+    }
+  }
+  __device__ __forceinline__ void load(const typename Elem<TYPE>::T* p, int i, int K) {  // any alignment; zeros behind K
+    if ((i + 1) * VE <= K) {
+      __builtin_memcpy(w, p + i * VE, sizeof(w));
+    } else {
+      typename Elem<TYPE>::T t[VE];
+#pragma unroll
+      for (int e = 0; e < VE; ++e) t[e] = i * VE + e < K ? p[i * VE + e] : typename Elem<TYPE>::T(0);
+      __builtin_memcpy(w, t, sizeof(w));
+    }
+  }
+  __device__ __forceinline__ void store(typename Elem<TYPE>::T* p, int i, int K) const {
+    if ((i + 1) * VE <= K) {
+      __builtin_memcpy(p + i * VE, w, sizeof(w));
+    } else {
+      typename Elem<TYPE>::T t[VE];
+      __builtin_memcpy(t, w, sizeof(w));
+#pragma unroll
+      for (int e = 0; e < VE; ++e)
+        if (i * VE + e < K) p[i * VE + e] = t[e];
+    }
+  }
+};
+
+// W waves a row, which they hold in registers, in its own type: NV pieces of 8 elements a lane.  One pass over
 // the data; bytes bound it.  The sum of squares is FP64 (two instructions an element, hidden behind the
 // loads), so that r, and with it every code, is the same however the sum is cut.
 template <int TYPE, int WTYPE, int W, int NV>
@@ -138,42 +176,38 @@ __global__ __launch_bounds__(256) void norm_kernel(NormArgs a) {
   const int K = a.K;
   const T* const x = static_cast<const T*>(a.x) + row * a.ldx;
   const T* const residual = static_cast<const T*>(a.residual) + row * a.ldr;
-  float v[NV][VE];
+  Piece<TYPE> h[NV] = {};
 #pragma unroll
   for (int j = 0; j < NV; ++j) {
     const int i = lane + 64 * W * j;
-#pragma unroll
-    for (int e = 0; e < VE; ++e) v[j][e] = 0.0f;
-    if (i * VE < K) load8<TYPE>(v[j], x, i, K);
+    if (i * VE < K) h[j].load(x, i, K);
   }
   if (a.residual) {
-    float r[NV][VE];
+    Piece<TYPE> r[NV] = {};
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
       const int i = lane + 64 * W * j;
-#pragma unroll
-      for (int e = 0; e < VE; ++e) r[j][e] = 0.0f;
-      if (i * VE < K) load8<TYPE>(r[j], residual, i, K);
+      if (i * VE < K) r[j].load(residual, i, K);
     }
 #pragma unroll
     for (int j = 0; j < NV; ++j)
 #pragma unroll
-      for (int e = 0; e < VE; ++e) v[j][e] = to_f32<TYPE>(from_f32<TYPE>(v[j][e] + r[j][e]));
+      for (int e = 0; e < VE; e += 2) h[j].set2(e, h[j].at(e) + r[j].at(e), h[j].at(e + 1) + r[j].at(e + 1));
   }
   double sum = 0.0;
 #pragma unroll
   for (int j = 0; j < NV; ++j)
 #pragma unroll
     for (int e = 0; e < VE; ++e) {
-      const double h = static_cast<double>(v[j][e]);
-      sum = __builtin_fma(h, h, sum);
+      const double v = static_cast<double>(h[j].at(e));
+      sum = __builtin_fma(v, v, sum);
     }
   if (a.total) {
     T* const total = static_cast<T*>(a.total) + row * a.ldt;
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
       const int i = lane + 64 * W * j;
-      if (i * VE < K) store8<TYPE>(total, i, K, v[j]);
+      if (i * VE < K) h[j].store(total, i, K);
     }
   }
   sum = lanes_sum<64>(sum);
@@ -186,29 +220,23 @@ __global__ __launch_bounds__(256) void norm_kernel(NormArgs a) {
   }
   const float r = static_cast<float>(1.0 / __builtin_sqrt(sum / K + a.eps));
   const TW* const weight = static_cast<const TW*>(a.weight);
+  T* const out = static_cast<T*>(a.out) + row * a.ldo;
+  uint8_t* const codes = a.codes + row * a.ldc;
+  uint32_t top = 0;
+  float v[NV][VE];  // y, zeros behind K
 #pragma unroll
   for (int j = 0; j < NV; ++j) {
     const int i = lane + 64 * W * j;
-    float w[VE] = {};
-    if (i * VE < K) load8<WTYPE>(w, weight, i, K);
+    Piece<WTYPE> w = {};
+    if (i * VE < K) w.load(weight, i, K);
 #pragma unroll
-    for (int e = 0; e < VE; ++e) v[j][e] = (v[j][e] * r) * w[e];
-  }
-  if (a.out) {
-    T* const out = static_cast<T*>(a.out) + row * a.ldo;
+    for (int e = 0; e < VE; ++e) v[j][e] = i * VE + e < K ? (h[j].at(e) * r) * w.at(e) : 0.0f;
+    if (a.out) {
 #pragma unroll
-    for (int j = 0; j < NV; ++j) {
-      const int i = lane + 64 * W * j;
-      if (i * VE < K) store8<TYPE>(out, i, K, v[j]);
+      for (int e = 0; e < VE; e += 2) h[j].set2(e, v[j][e], v[j][e + 1]);
+      if (i * VE < K) h[j].store(out, i, K);
     }
-  }
-  uint8_t* const codes = a.codes + row * a.ldc;
-  if (a.format == MOE_CODES_E4M3) {
-#pragma unroll
-    for (int j = 0; j < NV; ++j) {
-      const int i = lane + 64 * W * j;
-#pragma unroll
-      for (int e = 0; e < VE; ++e) v[j][e] = i * VE + e < K ? v[j][e] : 0.0f;  // (0 * r is NaN where r is)
+    if (a.format == MOE_CODES_E4M3) {
       uint32_t c[2];
       const float scale = codes_e4m3(v[j], c);
       if (i * VE < K) {
@@ -216,14 +244,11 @@ __global__ __launch_bounds__(256) void norm_kernel(NormArgs a) {
         if (lane % 16 == 0) a.scales[row * a.lds + i / 16] = scale;
       }
     }
-  } else if (a.format == MOE_CODES_I8) {
+  }
+  if (a.format == MOE_CODES_I8) {
     constexpr float kMagic = 12582912.0f;
-    uint32_t top = 0;
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-      const int i = lane + 64 * W * j;
-#pragma unroll
-      for (int e = 0; e < VE; ++e) v[j][e] = i * VE + e < K ? v[j][e] : 0.0f;
       const uint32_t t = top_of(v[j]);
       top = t > top ? t : top;
     }
@@ -298,12 +323,12 @@ int launch_norm(const NormArgs& a, hipStream_t st) {
 template <int TYPE, int WTYPE>
 int launch_norm(const NormArgs& a, hipStream_t st) {
   const int pieces = (a.K + VE - 1) / VE;
-  // many rows: a wave each, no step waits for another wave; few: four waves each
-  if (a.M >= 1024 && pieces <= 8 * 64) {
+  // many short rows: a wave each, no step waits for another wave (us, against four waves: 16384 x 512 14.9 and 36.9,
+  // 16384 x 1024 33 and 42); few or long ones: four waves each (16384 x 3584 101, against 110)
+  if (a.M >= 1024 && pieces <= 4 * 64) {
     if (pieces <= 64) return launch_norm<TYPE, WTYPE, 1, 1>(a, st);
     if (pieces <= 2 * 64) return launch_norm<TYPE, WTYPE, 1, 2>(a, st);
-    if (pieces <= 4 * 64) return launch_norm<TYPE, WTYPE, 1, 4>(a, st);
-    return launch_norm<TYPE, WTYPE, 1, 8>(a, st);
+    return launch_norm<TYPE, WTYPE, 1, 4>(a, st);
   }
   if (pieces <= 2 * 256) return launch_norm<TYPE, WTYPE, 4, 2>(a, st);
   return launch_norm<TYPE, WTYPE, 4, 8>(a, st);
