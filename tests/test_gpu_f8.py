@@ -690,3 +690,103 @@ def test_an_earlier_error_is_not_this_calls(m, through):
     # the block's largest value is 1: scale 2^-8, code 256
     assert (s == 2.0 ** -8).all() and (q.float() == 256).all()
     assert torch.equal(y, torch.full_like(y, 128.0 * 256 * 256 * 2.0 ** -8)) and torch.equal(y, z) and o.tolist() == [0, 3]
+
+
+# --------------------------------------------------------------- every tile
+def _whole(m, M, N, K, dtype, act, seed, plain=True):
+    """A product whose out (and add) is contiguous, its rows 16-byte aligned where N allows."""
+    g = _gen(seed)
+    cols = N // 2 if act == "swiglu" else N
+    nb = 2 * ref.kb(cols) if act == "swiglu" else ref.kb(N)
+    a, w = _codes((M, K), g, 4), _codes((N, K), g, 4)
+    sa, sw, b = torch.rand(M, ref.kb(K), generator=g), torch.rand(nb, ref.kb(K), generator=g) / K ** 0.5, torch.randn(N, generator=g)
+    d = None if plain else torch.randn(M, cols, generator=g).to(dtype)
+    out = torch.empty(M, cols, dtype=dtype, device=DEV)
+    m.moe_linear_f8(a.to(DEV), sa.to(DEV), w.to(DEV), sw.to(DEV), out, act=act, bias=None if plain else b.to(DEV),
+                    add=None if plain else d.to(DEV))
+    torch.cuda.synchronize()
+    y, e = ref.linear(_np(a.float()), _np(sa), _np(w.float()), _np(sw), act=act, bias=None if plain else _np(b),
+                      add=None if plain else _np(d), cut=dtype != F32)
+    _check(_np(out), y, e, dtype, (M, N, K, act))
+
+
+# sizes for which each of the tiles (64 and 128 x 128 two and four deep, 128 and 256 x 256) is chosen, with rows and
+# columns over
+@pytest.mark.parametrize("M,N", [(100, 4096), (800, 9000), (230, 2048), (990, 3600), (1990, 4000), (1985, 3990), (4090, 4064),
+                                 (4081, 4070), (700, 32768)])
+@pytest.mark.parametrize("dtype,act,plain", [(BF, "none", True), (F16, "swiglu", False), (BF, "swiglu", True), (F16, "none", False),
+                                             (F32, "none", False), (F32, "swiglu", True)])
+def test_linear_tiles(m, M, N, dtype, act, plain):
+    K = (144, 272, 400)[(M + N) % 3]
+    log(f"linear_f8 tiles {M}x{N}x{K} {dtype} {act}")
+    _whole(m, M, N, K, dtype, act, M + N, plain)
+
+
+@pytest.mark.parametrize("K", [16, 128, 256, 384, 1024, 1040, 2048, 8320])
+def test_linear_depths(m, K):
+    """K of fewer blocks than stages, and of many, in each tile."""
+    log(f"linear_f8 K = {K}")
+    for M, N in ((70, 33000), (200, 1024), (1000, 3584)):
+        if M * N * K < 1 << 35:
+            _whole(m, M, N, K, BF, "none", K)
+            _whole(m, M, N, K, F32, "swiglu", K)
+    _whole(m, 5, 96, 65536 if K == 8320 else K, BF, "none", K)
+
+
+@pytest.mark.parametrize("B,topk,E,N", [(1000, 2, 8, 4000), (2040, 2, 8, 4064), (300, 2, 30, 1030), (50, 16, 160, 272), (8, 16, 160, 768),
+                                        (700, 1, 16, 2048), (1, 16, 160, 3584), (6, 16, 1024, 160)])
+@pytest.mark.parametrize("kind", ["uniform", "zipf"])
+def test_grouped_tiles(m, B, topk, E, N, kind):
+    K = (144, 1168)[E % 16 == 0]
+    log(f"grouped tiles {B}x{topk} of {E}, {N}x{K} {kind}")
+    ids = _ids(B, topk, E, kind)
+    _grouped(m, ids, E, N, K, dtype=BF, act="swiglu", scatter=False)
+    _grouped(m, ids, E, N, K, dtype=F16)
+    if B <= 300:
+        _grouped(m, ids, E, N, K, dtype=F32, gather=False)
+
+
+def test_grouped_two_streams_share_inputs(m):
+    """Two calls at once on the same weights and lists, each with its own rows."""
+    g = _gen(91)
+    E, N, K, B, topk = 6, 512, 512, 300, 2
+    ids = _ids(B, topk, E, "uniform").to(DEV)
+    o, p = torch.empty(E + 1, dtype=I32, device=DEV), torch.empty(B * topk, dtype=I32, device=DEV)
+    m.moe_lists(ids, o, p)
+    w, sw = _codes((E, N, K), g).to(DEV), torch.rand(E, 4, 4, generator=g).to(DEV)
+    xs = [(_codes((B, K), g).to(DEV), torch.rand(B, 4, generator=g).to(DEV)) for _ in range(2)]
+    want = []
+    for a, sa in xs:
+        out = torch.empty(B * topk, N, device=DEV, dtype=BF)
+        m.moe_grouped_f8(a, sa, w, sw, o, out, pairs=p, gather=topk, scatter=True)
+        want.append(out)
+    torch.cuda.synchronize()
+    streams, outs = [torch.cuda.Stream() for _ in xs], [torch.zeros_like(t) for t in want]
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for (a, sa), s, out in zip(xs, streams, outs):
+            m.moe_grouped_f8(a, sa, w, sw, o, out, pairs=p, gather=topk, scatter=True, stream=s)
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(outs, want))
+
+
+def test_lists_captured(m):
+    """Both launches in a graph, replayed with other ids; eager calls with a workspace of their own between."""
+    R, E = 20000, 40
+    ids = torch.zeros(R, 1, dtype=I32, device=DEV)
+    o, p = torch.empty(E + 1, dtype=I32, device=DEV), torch.empty(R, dtype=I32, device=DEV)
+    ws = torch.empty(m.moe_lists_ws_bytes(R, E), dtype=torch.uint8, device=DEV)
+    m.moe_lists(ids, o, p, ws=ws)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        m.moe_lists(ids, o, p, ws=ws)
+    for seed in range(4):
+        new = torch.randint(-1, E, (R, 1), generator=_gen(seed), dtype=I32)
+        ids.copy_(new)
+        graph.replay()
+        want = _lists(m, new, E)
+        torch.cuda.synchronize()
+        assert np.array_equal(o.cpu().numpy(), want[0]) and np.array_equal(p.cpu().numpy(), want[1])
+        ro, rp = ref.lists(new.numpy(), E)
+        assert np.array_equal(want[0], ro) and np.array_equal(want[1], rp)
