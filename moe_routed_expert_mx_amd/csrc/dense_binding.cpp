@@ -1,4 +1,4 @@
-// dense_binding.cpp -- the short way from Python to the dense side's entry points.
+// dense_binding.cpp -- the short way from Python to the entry points of the dense side and of the block-scaled FP8 layer.
 //
 // A decode step's kernels take 3 to 6 us, and so do the checks and argument conversions of a
 // ctypes call.  Each function here takes what its namesake in _lib.py takes (options as plain

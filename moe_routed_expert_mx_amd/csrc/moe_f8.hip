@@ -47,24 +47,36 @@ __global__ __launch_bounds__(kListThreads) void lists_count_kernel(ListArgs a) {
 __global__ __launch_bounds__(kListThreads) void lists_place_kernel(ListArgs a) {
   extern __shared__ uint32_t list_lds[];  // [waves][E]: counts, then where the wave's next route goes; sums
   uint32_t* const sums = list_lds + kListWaves * a.E;
+  uint32_t* const joined = sums + kListWaves;  // [2][E]
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const uint32_t e = threadIdx.x;
   for (uint32_t i = threadIdx.x; i < kListWaves * a.E; i += kListThreads) list_lds[i] = 0;
+  for (uint32_t i = threadIdx.x; i < 2 * a.E; i += kListThreads) joined[i] = 0;
   __syncthreads();
   const uint64_t begin = (static_cast<uint64_t>(blockIdx.x) * kListWaves + wave) * a.share;
   const uint32_t first = static_cast<uint32_t>(begin < a.R ? begin : a.R), last = a.R - first < a.share ? a.R : first + a.share;
-  count_ids(a, first, last, list_lds + wave * a.E, lane);
-  __syncthreads();
-  // routes of expert e in all, and in the workgroups before this one
-  uint32_t all = 0, before = 0;
-  if (e < a.E) {
-    if (gridDim.x > 1) {
-#pragma unroll 8
-      for (uint32_t g = 0; g < gridDim.x; ++g) {
-        const uint32_t c = a.counts[static_cast<uint64_t>(g) * a.E + e];
+  // routes of each expert in all, and in the workgroups before this one: all threads share the counts out
+  if (gridDim.x > 1) {
+    const uint32_t parts = kListThreads / a.E, part = e / a.E, mine = e % a.E;
+    if (part < parts) {
+      uint32_t all = 0, before = 0;
+#pragma unroll 4
+      for (uint32_t g = part; g < gridDim.x; g += parts) {
+        const uint32_t c = a.counts[static_cast<uint64_t>(g) * a.E + mine];
         all += c;
         before += g < blockIdx.x ? c : 0;
       }
+      atomicAdd(joined + mine, all);
+      atomicAdd(joined + a.E + mine, before);
+    }
+  }
+  count_ids(a, first, last, list_lds + wave * a.E, lane);
+  __syncthreads();
+  uint32_t all = 0, before = 0;
+  if (e < a.E) {
+    if (gridDim.x > 1) {
+      all = joined[e];
+      before = joined[a.E + e];
     } else {
 #pragma unroll
       for (int w = 0; w < kListWaves; ++w) all += list_lds[w * a.E + e];
@@ -278,7 +290,8 @@ struct Operand<true> {
 // rows (SwiGLU: 16 gate rows and their 16 up rows) and 16 TT rows of a, and split K in blocks of 128.  A wave loads a block's rows eight lanes to a row, some blocks ahead, and turns them into operands
 // through LDS of its own; a 16x16x128 MFMA is one block's sum, which is scaled and added in FP32.
 // Lane l's operand holds parts l / 16 and 4 + l / 16 of its row's eight: any order of k within the block
-// will do that both sides have, and this one meets all banks of LDS.
+// will do that both sides have, and this one meets all banks of LDS.  The 16 experts of one token (gate and up rows of 384
+// x 3584, 44 MB) take 12 us, 3.7 TB/s, their second product 6 us (22 MB).
 template <int OUT, bool SWIGLU, bool GROUPED, int RT, int TT, int WV, int WK>
 __global__ __launch_bounds__(64 * WV) void f8_stream_kernel(F8Args a, uint32_t nx) {
   extern __shared__ __attribute__((aligned(16))) unsigned char smem[];
@@ -437,8 +450,12 @@ __device__ __forceinline__ void dma4s(v4i rsrc, uint32_t voff, uint32_t soff, ui
 // Workgroup tile of BM rows of a x BN weight rows, WM x WN waves, each with TM x TN tiles of 16 x 16.  K goes
 // through LDS in stages of one block, NS deep, by LDS DMA; with the stage come the scales of a's rows, while those of
 // the weight's blocks lie in LDS from the start.  A row's 16-byte parts lie permuted by its index (as in
-// the int8 product's tiles).  A wave holds its rows of a for a whole block and takes its weight rows 16 at a
-// time; behind the last of them the next block's rows of a follow into the registers that each product leaves.
+// the int8 product's tiles).  A wave holds its 64 weight rows for a whole block and takes its rows of a 16 at a
+// time; as the last of them leaves the weight's registers the next block's rows follow.
+//   8192 x 8192 x 8192 with tiles of 256 x 256: 508 us, 2.16 PFLOP/s (a library product without block scales 411).
+// The DMA bounds it, 64 KB for 2048 cycles of products: without it 394 us, from L2-hot lines 450; the scaled sums take 36
+// us, the products alone 292.  8192 x 7168 x 3584, SwiGLU: 217 us, 1.94 PFLOP/s, in four rounds of which the last is half
+// empty.  Stages of 128 x 256 tiles fit three deep, but move 1.5 times the bytes (8192 x 8192 x 8192 607 us).
 template <int BM, int BN, int WM, int WN, int NS, int OUT, bool SWIGLU, bool GROUPED>
 __global__ __launch_bounds__(64 * WM * WN, 1) void f8_tile_kernel(F8Args a, uint32_t nm, uint32_t nn, uint32_t per_xcd) {
   extern __shared__ __attribute__((aligned(16))) unsigned char smem[];
@@ -808,8 +825,8 @@ int moe_lists(const int32_t* ids, int64_t R, int32_t E, int32_t* offsets, int32_
                       static_cast<uint32_t>(share)};
   hipStream_t st = as_stream(stream);
   static std::atomic<uint64_t> done{0};
-  const size_t lds = static_cast<size_t>(kListWaves) * (E + 1) * 4;
-  if (lds > 65536 && !allow_lds(lists_place_kernel, static_cast<size_t>(kListWaves) * 1025 * 4, done)) return hip_failed();
+  const size_t lds = (static_cast<size_t>(kListWaves) * (E + 1) + 2 * E) * 4;
+  if (lds > 65536 && !allow_lds(lists_place_kernel, (static_cast<size_t>(kListWaves) * 1025 + 2048) * 4, done)) return hip_failed();
   if (groups > 1) {
     const int r = launch(lists_count_kernel, groups, kListThreads, E * 4, st, a);
     if (r != MOE_OK) return r;

@@ -790,3 +790,28 @@ def test_lists_captured(m):
         assert np.array_equal(o.cpu().numpy(), want[0]) and np.array_equal(p.cpu().numpy(), want[1])
         ro, rp = ref.lists(new.numpy(), E)
         assert np.array_equal(want[0], ro) and np.array_equal(want[1], rp)
+
+
+@pytest.mark.parametrize("dtype", [BF, F16])
+@pytest.mark.parametrize("M", [4, 100, 2000])
+def test_linear_special_codes_in_16_bits(m, M, dtype):
+    """NaN codes and scales through the FP8 cores: they stay in their rows and columns, also in the last block and in
+    padded rows of a tile."""
+    g = _gen(M)
+    N, K = 4000 if M == 2000 else 300, 272
+    a, w = _codes((M, K), g), _codes((N, K), g)
+    a.view(torch.uint8)[1, 271] = 0x7f
+    w.view(torch.uint8)[N - 1, 0] = 0xff
+    sa, sw = torch.ones(M, 3), torch.ones(ref.kb(N), 3)
+    sa[M - 1, 2] = NAN
+    sw[0, 1] = 0.0
+    out = torch.empty(M, N, dtype=dtype, device=DEV)
+    m.moe_linear_f8(a.to(DEV), sa.to(DEV), w.to(DEV), sw.to(DEV), out)
+    torch.cuda.synchronize()
+    got = _np(out)
+    with np.errstate(invalid="ignore"):
+        y, e = ref.linear(_np(a.float()), _np(sa), _np(w.float()), _np(sw))
+    fine = np.isfinite(y)
+    assert not fine[[1, M - 1]].any() and not fine[:, N - 1].any() and fine[0, 0]
+    assert np.array_equal(np.isfinite(got), fine)
+    _check(got[fine], y[fine], np.nan_to_num(e[fine]), dtype)
