@@ -60,17 +60,35 @@ __global__ __launch_bounds__(kListThreads) void lists_place_kernel(ListArgs a) {
     const uint32_t parts = kListThreads / a.E, part = e / a.E, mine = e % a.E;
     if (part < parts) {
       uint32_t all = 0, before = 0;
-#pragma unroll 4
-      for (uint32_t g = part; g < gridDim.x; g += parts) {
-        const uint32_t c = a.counts[static_cast<uint64_t>(g) * a.E + mine];
-        all += c;
-        before += g < blockIdx.x ? c : 0;
+      for (uint32_t g0 = part; g0 < gridDim.x; g0 += 16 * parts) {  // (from other XCDs: far away, so many at once)
+        uint32_t c[16];
+#pragma unroll
+        for (int k = 0; k < 16; ++k) {
+          const uint32_t g = g0 + k * parts;
+          c[k] = g < gridDim.x ? a.counts[static_cast<uint64_t>(g) * a.E + mine] : 0;
+        }
+#pragma unroll
+        for (int k = 0; k < 16; ++k) {
+          all += c[k];
+          before += g0 + k * parts < blockIdx.x ? c[k] : 0;
+        }
       }
       atomicAdd(joined + mine, all);
       atomicAdd(joined + a.E + mine, before);
     }
   }
-  count_ids(a, first, last, list_lds + wave * a.E, lane);
+  // the wave's first 512 ids stay in registers (all of them up to 2^21 routes), E for those left out
+  constexpr int kHeld = 8;
+  uint32_t held[kHeld];
+#pragma unroll
+  for (int k = 0; k < kHeld; ++k) {
+    const uint32_t i = first + k * 64 + lane;
+    held[k] = i < last ? static_cast<uint32_t>(a.ids[i]) : a.E;
+  }
+#pragma unroll
+  for (int k = 0; k < kHeld; ++k)
+    if (held[k] < a.E) atomicAdd(list_lds + wave * a.E + held[k], 1u);
+  if (last - first > kHeld * 64) count_ids(a, first + kHeld * 64, last, list_lds + wave * a.E, lane);
   __syncthreads();
   uint32_t all = 0, before = 0;
   if (e < a.E) {
@@ -112,9 +130,7 @@ __global__ __launch_bounds__(kListThreads) void lists_place_kernel(ListArgs a) {
   __syncthreads();
   uint32_t* const next = list_lds + wave * a.E;
   const int bits = 32 - __builtin_clz(a.E);  // ids and E itself, which stands for those left out
-  for (uint32_t i0 = first; i0 < last; i0 += 64) {
-    const uint32_t i = i0 + lane;
-    uint32_t id = i < last ? static_cast<uint32_t>(a.ids[i]) : a.E;
+  auto place = [&](uint32_t i, uint32_t id) {
     id = id < a.E ? id : a.E;
     uint64_t same = ~0ull;  // lanes with this lane's id
     for (int b = 0; b < bits; ++b) {
@@ -131,7 +147,11 @@ __global__ __launch_bounds__(kListThreads) void lists_place_kernel(ListArgs a) {
       if (rank == 0) next[id] = at + static_cast<uint32_t>(__popcll(same));
     }
     wave_sync();
-  }
+  };
+#pragma unroll
+  for (int k = 0; k < kHeld; ++k)
+    if (first + k * 64 < last) place(first + k * 64 + lane, held[k]);
+  for (uint32_t i0 = first + kHeld * 64; i0 < last; i0 += 64) place(i0 + lane, i0 + lane < last ? static_cast<uint32_t>(a.ids[i0 + lane]) : a.E);
   // behind the last list; each workgroup its share of the places
   const uint32_t span = kListWaves * a.share;
   const uint64_t p0 = static_cast<uint64_t>(blockIdx.x) * span;
