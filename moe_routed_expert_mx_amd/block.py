@@ -121,20 +121,25 @@ class SharedExpertI8:
 
     def forward(self, x: torch.Tensor, *, add: torch.Tensor | None = None, out: torch.Tensor | None = None,
                 stream=None) -> torch.Tensor:
-        """x: BF16 [B, D] -> BF16 [B, D], plus `add` if given (which may be out itself).  The hidden is rounded to
-        BF16 between the products."""
-        B = x.shape[0]
+        """x: BF16 [B, D], or its codes and scales (as moe_quant_i8 or moe_rms_norm made them) -> BF16 [B, D], plus `add`
+        if given (which may be out itself).  The hidden is rounded to BF16 between the products."""
+        given = isinstance(x, (tuple, list))
+        first = x[0] if given else x
+        B = first.shape[0]
         if B > self.B_max:
             raise ValueError("batch larger than B_max")
-        with _on(stream, x.device) as give:
+        with _on(stream, first.device) as give:
             if out is None:
                 out = give(torch.empty(B, self.D, dtype=torch.bfloat16, device=self.device))
             # rows of the code buffers are packed for each product, so that they stay 16-byte aligned
             flat = self.codes.view(-1)
             scales, hidden = self.scales[:B], self.hidden[:B]
-            q = flat[:B * self.D].view(B, self.D)
-            _lib.moe_quant_i8(x, q, scales)
-            _lib.moe_linear_i8(q, scales, self.w13, self.s13, hidden, act="swiglu")
+            if given:
+                q, first_scales = x
+            else:
+                q, first_scales = flat[:B * self.D].view(B, self.D), scales
+                _lib.moe_quant_i8(x, q, scales)
+            _lib.moe_linear_i8(q, first_scales, self.w13, self.s13, hidden, act="swiglu")
             q = flat[:B * self.I].view(B, self.I)
             _lib.moe_quant_i8(hidden, q, scales)
             _lib.moe_linear_i8(q, scales, self.w2, self.s2, out, add=add)
@@ -214,7 +219,7 @@ class ExpertsF8:
                 path: str = "auto") -> torch.Tensor:
         """x: BF16 [B, D], or its codes and scales (as moe_quant_f8 or moe_rms_norm made them); ids: int32 [B, topk]
         -> rows BF16 [B * topk, D] in the order of the ids, no routing weight applied.  Ids outside [0, E) have no
-        expert here, their rows of `out` are left as they were.  The hidden is rounded to BF16 between the products.
+        expert here: their rows of `out` are left as they were (of a new buffer, undefined).  The hidden is rounded to BF16 between the products.
         path: "auto" (there is one)."""
         given = isinstance(x, (tuple, list))
         B = (x[0] if given else x).shape[0]
@@ -308,7 +313,8 @@ class Norm:
 class MoeBlock:
     def __init__(self, router: Router, layer: MoeLayer | ExpertsF8,
                  shared: SharedExpertI8 | SharedExpertF8 | None = None, norm: Norm | None = None):
-        """norm: None, or the norm in front of the layer; its 8-bit codes then go straight to the FP8 parts."""
+        """norm: None, or the norm in front of the layer; its 8-bit codes then go straight to the parts in FP8, or to an
+        int8 shared expert beside experts that are not."""
         if (router.E, router.D, router.topk) != (layer.E, layer.D, layer.topk):
             raise ValueError("router and experts differ in E, D or topk")
         if shared is not None and shared.D != layer.D:
@@ -330,15 +336,18 @@ class MoeBlock:
             return give(self._forward(x, residual, path))
 
     def _forward(self, x, residual, path):
-        x8 = x
         f8 = isinstance(self.layer, ExpertsF8), isinstance(self.shared, SharedExpertF8)
-        if self.norm is not None and any(f8):
-            x, *x8 = self.norm.forward(x, residual, codes=_F8)
-        elif self.norm is not None:
-            x = x8 = self.norm.forward(x, residual)
+        x8, codes = x, None
+        if self.norm is not None:
+            # (one kind of codes a norm: e4m3 where a part takes them, else int8 for an int8 shared expert)
+            codes = _F8 if any(f8) else torch.int8 if isinstance(self.shared, SharedExpertI8) else None
+            if codes is None:
+                x = self.norm.forward(x, residual)
+            else:
+                x, *x8 = self.norm.forward(x, residual, codes=codes)
         ids, weights = self.router.forward(x)
         rows = self.layer.forward(x8 if f8[0] else x, ids, path=path)
         y = self.layer.combine(rows, weights)
         if self.shared is not None:
-            self.shared.forward(x8 if f8[1] else x, add=y, out=y)
+            self.shared.forward(x8 if f8[1] or codes == torch.int8 else x, add=y, out=y)
         return y

@@ -815,3 +815,26 @@ def test_linear_special_codes_in_16_bits(m, M, dtype):
     assert not fine[[1, M - 1]].any() and not fine[:, N - 1].any() and fine[0, 0]
     assert np.array_equal(np.isfinite(got), fine)
     _check(got[fine], y[fine], np.nan_to_num(e[fine]), dtype)
+
+
+@pytest.mark.parametrize("B", [1, 40])
+def test_block_with_norm_and_int8_shared_expert(m, B):
+    """FP4 experts and an int8 shared expert behind a norm: that one's int8 codes; without a shared expert none."""
+    log(f"block with norm, int8 B={B}")
+    g = _gen(B + 3)
+    block = _block(g, f8=(False, False))
+    x, r = torch.randn(B, 512, generator=g).to(BF).to(DEV), torch.randn(B, 512, generator=g).to(BF).to(DEV)
+    r1 = r.clone()
+    y = block.forward(x, residual=r1)
+    n, q, s = block.norm.forward(r1, codes=torch.int8)
+    ids, wts = block.router.forward(n)
+    comb = block.layer.combine(block.layer.forward(n, ids), wts)
+    want = block.shared.forward((q, s), add=comb)
+    torch.cuda.synchronize()
+    assert torch.equal(y, want) and torch.equal(r1, (x.float() + r.float()).to(BF))
+    h, eh = dense_ref.linear(q.cpu().numpy(), s.cpu().numpy(), block.shared.w13.cpu().numpy(), block.shared.s13.cpu().numpy(), act="swiglu")
+    block.shared.forward((q, s))
+    torch.cuda.synchronize()
+    assert np.all(np.abs(_np(block.shared.hidden[:B]) - h) <= eh + 2.0 ** -8 * (np.abs(h) + eh))
+    bare = type(block)(block.router, block.layer, None, block.norm)
+    assert torch.equal(bare.forward(r1), comb)
