@@ -426,7 +426,7 @@ int moe_quant_i8(const void* x_dev, int32_t type, int64_t ldx, int32_t M, int32_
 typedef struct {
   int32_t act;           /* 0 = none; 1 = SwiGLU: rows 0..N/2-1 of w are the gate, N/2..N-1 up
                             (N even), and out has N/2 columns */
-  int32_t reserved;
+  int32_t exact;         /* moe_linear_f8: see there; moe_linear_i8 is always exact */
   const float* bias_dev; /* optional FP32 [N], before the activation */
   const void* add_dev;   /* optional [M, columns of out], out's type, added last; may be out_dev
                             itself with ldadd == ldo */
@@ -499,8 +499,10 @@ int moe_rms_norm(const void* x_dev, int32_t type, int64_t ldx, int32_t M, int32_
  *   y[m, n] = sum over blocks b of a_scales[m, b] * w_scales[n / 128, b] * (sum over k in b of
  *             a[m, k] * w[n, k]) + bias[n];   act 1: y[m, n] = silu(y[m, n]) * y[m, N/2 + n];
  *   out = y + add, rounded once;   sums and scales in FP32, in an order that the sizes decide.
- * Products of codes are exact; for outputs in 16 bits of many rows the matrix cores then cut each at
- * 2^-13 of the largest of its eight neighbours along k (some 1.5e-5 of a sum), for FP32 outputs they do not.
+ * Products of codes are exact.  For FP32 outputs, and with opts.exact = 1 for all, FP32 sums add them as they are;
+ * with opts.exact = 0 outputs in 16 bits, of any number of rows, come from the FP8 matrix cores, which cut each product
+ * at 2^-13 of the largest of its eight neighbours along k: some 1.5e-5 of a sum, which the output's rounding hides
+ * where it is final, and at times a code where it is quantized again.  Exact sums take up to twice as long.
  * a_dev [M, K] (lda), a_scales_dev FP32 [M, KB] (ldsa >= KB); w_dev [N, K] (ldw), w_scales_dev FP32
  * [NB, KB], contiguous: NB = ceil(N / 128), with act 1 NB = 2 ceil(N/2 / 128), as the gate rows (0 ..
  * N/2 - 1) and the up rows have blocks of their own.  out_dev [M, N or N/2] of out_type (ldo).
@@ -528,7 +530,7 @@ typedef struct {
   int32_t act;              /* as moe_linear_opts_t */
   int32_t gather;           /* 0: row i is a[i]; g > 0: a[pairs[i] / g] */
   int32_t scatter;          /* 0: its result is out[i]; 1: out[pairs[i]] */
-  int32_t reserved;
+  int32_t exact;            /* as moe_linear_f8's */
   const int32_t* pairs_dev; /* i32 [R], from moe_lists; NULL without gather and scatter */
 } moe_grouped_opts_t;
 

@@ -55,7 +55,7 @@ class moe_route_opts_t(ctypes.Structure):
 
 
 class moe_linear_opts_t(ctypes.Structure):
-    _fields_ = [("act", ctypes.c_int32), ("reserved", ctypes.c_int32), ("bias_dev", ctypes.c_void_p),
+    _fields_ = [("act", ctypes.c_int32), ("exact", ctypes.c_int32), ("bias_dev", ctypes.c_void_p),
                 ("add_dev", ctypes.c_void_p), ("ldadd", ctypes.c_int64)]
 
 
@@ -69,7 +69,7 @@ class moe_norm_opts_t(ctypes.Structure):
 
 class moe_grouped_opts_t(ctypes.Structure):
     _fields_ = [("act", ctypes.c_int32), ("gather", ctypes.c_int32), ("scatter", ctypes.c_int32),
-                ("reserved", ctypes.c_int32), ("pairs_dev", ctypes.c_void_p)]
+                ("exact", ctypes.c_int32), ("pairs_dev", ctypes.c_void_p)]
 
 
 class moe_prefetch_row_t(ctypes.Structure):
@@ -621,15 +621,18 @@ def _f8_weight_blocks(N: int, K: int, mode: int) -> tuple:
     return (2 * ((N // 2 + 127) // 128) if mode else (N + 127) // 128, _kb(K))
 
 
-def moe_linear_f8(a, a_scales, w, w_scales, out, *, act: str = "none", bias=None, add=None, stream=None):
+def moe_linear_f8(a, a_scales, w, w_scales, out, *, act: str = "none", bias=None, add=None, exact: bool = False,
+                  stream=None):
     """Product of block-scaled e4m3 matrices: a float8_e4m3fn [M, K] with scales FP32 [M, ceil(K / 128)], w
     float8_e4m3fn [N, K] with scales FP32 [ceil(N / 128), ceil(K / 128)] -> out [M, N] (FP32, BF16 or FP16), plus bias
     (FP32 [N]); act "swiglu": the first N/2 rows of w are the gate, the others up, each half with scale blocks of its
     own ([2 ceil(N/2 / 128), ..]), and out is [M, N/2]; add (as out, may be out itself) is added last.  K a multiple
-    of 16, rows 16-byte aligned."""
+    of 16, rows 16-byte aligned.  exact: the codes' products are added in FP32 as they are, as for FP32 outputs always;
+    otherwise the FP8 matrix cores cut some 1.5e-5 of a sum off, in as little as half the time.  Ask for it where `out` is
+    quantized again."""
     mode = _ACTS.get(act)
     if stream is None:
-        status = _dense.linear_f8(a, a_scales, w, w_scales, out, mode, bias, add)
+        status = _dense.linear_f8(a, a_scales, w, w_scales, out, mode, bias, add, exact)
         if status != _NOT_TAKEN:
             return _check("moe_linear_f8", status)
     shape, kind = _matrix(a, "a"), _MOE_TYPE.get(out.dtype)
@@ -655,7 +658,7 @@ def moe_linear_f8(a, a_scales, w, w_scales, out, *, act: str = "none", bias=None
         ldd, pd = _rows(add, "add", (M, cols)), add.data_ptr()
         tensors += (add,)
     _enqueue("moe_linear_f8", lib.moe_linear_f8, stream, tensors, a.data_ptr(), lda, a_scales.data_ptr(), ldsa,
-             w.data_ptr(), ldw, psw, M, N, K, _LINEAR_OPTS.pack(mode, 0, pb, pd, ldd), out.data_ptr(), kind, ldo)
+             w.data_ptr(), ldw, psw, M, N, K, _LINEAR_OPTS.pack(mode, 1 if exact else 0, pb, pd, ldd), out.data_ptr(), kind, ldo)
 
 
 def moe_lists_ws_bytes(R: int, E: int) -> int:
@@ -694,14 +697,14 @@ def moe_lists(ids, offsets, pairs, *, ws=None, stream=None):
 
 
 def moe_grouped_f8(a, a_scales, w, w_scales, offsets, out, *, act: str = "none", pairs=None, gather: int = 0,
-                   scatter: bool = False, stream=None):
+                   scatter: bool = False, exact: bool = False, stream=None):
     """Products grouped by expert: rows offsets[e] .. offsets[e + 1] - 1 with w[e], w float8_e4m3fn [E, N, K] with
     scales FP32 [E, blocks of rows, ceil(K / 128)], otherwise as moe_linear_f8.  Row i is a[i], or with gather = g
     a[pairs[i] / g] (g = topk: the tokens' rows); its result is out[i], or with scatter out[pairs[i]].  offsets and
     pairs from moe_lists.  Without pairs a and out have a row for each place of the lists."""
     mode = _ACTS.get(act)
     if stream is None:
-        status = _dense.grouped_f8(a, a_scales, w, w_scales, offsets, out, mode, pairs, gather, scatter)
+        status = _dense.grouped_f8(a, a_scales, w, w_scales, offsets, out, mode, pairs, gather, scatter, exact)
         if status != _NOT_TAKEN:
             return _check("moe_grouped_f8", status)
     kind = _MOE_TYPE.get(out.dtype)
@@ -731,5 +734,5 @@ def moe_grouped_f8(a, a_scales, w, w_scales, offsets, out, *, act: str = "none",
     elif pairs is not None:
         _refuse("pairs without gather or scatter")
     _enqueue("moe_grouped_f8", lib.moe_grouped_f8, stream, tensors, a.data_ptr(), lda, a_scales.data_ptr(), ldsa, shape[0],
-             w.data_ptr(), ldw, ldwe, psw, po, R, E, N, K, _GROUPED_OPTS.pack(mode, gather, 1 if scatter else 0, 0, pp),
+             w.data_ptr(), ldw, ldwe, psw, po, R, E, N, K, _GROUPED_OPTS.pack(mode, gather, 1 if scatter else 0, 1 if exact else 0, pp),
              out.data_ptr(), kind, ldo, rows_out)

@@ -246,8 +246,8 @@ long norm(PyObject* const* v, Py_ssize_t) {
   return g_norm(x, type_of(v[0]), ldx, static_cast<int32_t>(M), static_cast<int32_t>(K), w->data_ptr(), type_of(v[1]), &o, st);
 }
 
-// linear_f8(a, a_scales, w, w_scales, out, act, bias, add)
-long linear_f8(PyObject* const* v, Py_ssize_t) {
+// linear_f8(a, a_scales, w, w_scales, out, act, bias, add[, exact])
+long linear_f8(PyObject* const* v, Py_ssize_t n) {
   Call c;
   int64_t M = -1, K = -1, N = -1, lda = 0, ldw = 0, ldo = 0, ldsa = 0;
   const long act = PyLong_AsLong(v[5]);
@@ -258,8 +258,9 @@ long linear_f8(PyObject* const* v, Py_ssize_t) {
   void* out = c.matrix(v[4], M, cols, ldo);
   void* sa = c.matrix(v[1], M, kb, ldsa);
   const float* sw = c.blocks(v[3], -1, act == 1 ? 2 * blocks_of(cols) : blocks_of(cols), kb);
-  c.need(c.ok && is(v[0], kE4m3) && is(v[2], kE4m3) && is(v[1], at::kFloat) && type_of(v[4]) >= 0);
-  moe_linear_opts_t o = {static_cast<int32_t>(act), 0, nullptr, nullptr, 0};
+  const int exact = n > 8 ? PyObject_IsTrue(v[8]) : 0;
+  c.need(c.ok && is(v[0], kE4m3) && is(v[2], kE4m3) && is(v[1], at::kFloat) && type_of(v[4]) >= 0 && exact >= 0);
+  moe_linear_opts_t o = {static_cast<int32_t>(act), exact, nullptr, nullptr, 0};
   if (v[6] != Py_None) o.bias_dev = c.vector(v[6], N);
   if (v[7] != Py_None) {
     o.add_dev = c.matrix(v[7], M, cols, o.ldadd);
@@ -297,18 +298,18 @@ long lists(PyObject* const* v, Py_ssize_t) {
   return g_lists(static_cast<const int32_t*>(ids), R, static_cast<int32_t>(E1 - 1), offsets, pairs, ws, bytes, st);
 }
 
-// grouped_f8(a, a_scales, w, w_scales, offsets, out, act, pairs, gather, scatter)
-long grouped_f8(PyObject* const* v, Py_ssize_t) {
+// grouped_f8(a, a_scales, w, w_scales, offsets, out, act, pairs, gather, scatter[, exact])
+long grouped_f8(PyObject* const* v, Py_ssize_t n) {
   Call c;
   int64_t A = -1, O = -1, lda = 0, ldo = 0, ldsa = 0;
   const long act = PyLong_AsLong(v[6]), gather = PyLong_AsLong(v[8]);
-  const int scatter = PyObject_IsTrue(v[9]);
+  const int scatter = PyObject_IsTrue(v[9]), exact = n > 10 ? PyObject_IsTrue(v[10]) : 0;
   const at::Tensor* w = c.tensor(v[2]);
   if (!c.ok || w->dim() != 3 || w->scalar_type() != kE4m3) return kNotTaken;
   int64_t E = w->size(0), N = w->size(1), K = w->size(2), E1 = E + 1;
   const int64_t ldw = N == 1 ? K : w->stride(1), ldwe = E == 1 ? ((N - 1) * ldw + K + 15) & ~15LL : w->stride(0);
   c.need((w->stride(2) == 1 || K == 1) && ldw >= K && ldwe >= (N - 1) * ldw + K && E <= INT32_MAX && N <= INT32_MAX &&
-         K <= INT32_MAX && (act == 0 || act == 1) && !(act == 1 && N % 2) && gather >= 0 && gather <= INT32_MAX && scatter >= 0);
+         K <= INT32_MAX && (act == 0 || act == 1) && !(act == 1 && N % 2) && gather >= 0 && gather <= INT32_MAX && scatter >= 0 && exact >= 0);
   int64_t cols = act == 1 ? N / 2 : N, kb = blocks_of(K), R = -1;
   void* a = c.matrix(v[0], A, K, lda);
   void* sa = c.matrix(v[1], A, kb, ldsa);
@@ -317,7 +318,7 @@ long grouped_f8(PyObject* const* v, Py_ssize_t) {
   void* out = c.matrix(v[5], O, cols, ldo);
   c.need(c.ok && is(v[0], kE4m3) && is(v[1], at::kFloat) && type_of(v[5]) >= 0);
   c.need((v[7] != Py_None) == (gather > 0 || scatter > 0));
-  moe_grouped_opts_t o = {static_cast<int32_t>(act), static_cast<int32_t>(gather), scatter, 0, nullptr};
+  moe_grouped_opts_t o = {static_cast<int32_t>(act), static_cast<int32_t>(gather), scatter, exact, nullptr};
   if (c.ok && v[7] != Py_None) o.pairs_dev = c.list(v[7], R);
   else R = A < O ? A : O;
   void* st = c.stream();
@@ -376,9 +377,9 @@ PyMethodDef methods[] = {{"gate", FAST((entry<gate, 5, 1>))},
                          {"linear", FAST((entry<linear, 8>))},
                          {"norm", FAST((entry<norm, 8>))},
                          {"quant_f8", FAST((entry<quant_f8, 3>))},
-                         {"linear_f8", FAST((entry<linear_f8, 8>))},
+                         {"linear_f8", FAST((entry<linear_f8, 8, 1>))},
                          {"lists", FAST((entry<lists, 4>))},
-                         {"grouped_f8", FAST((entry<grouped_f8, 10>))},
+                         {"grouped_f8", FAST((entry<grouped_f8, 10, 1>))},
                          {"bind", bind, METH_VARARGS, nullptr},
                          {"bind_f8", bind_f8, METH_VARARGS, nullptr},
                          {nullptr, nullptr, 0, nullptr}};

@@ -1,0 +1,69 @@
+"""Choices and refusals of the block-scaled FP8 layer that hold without a GPU, beside those of test_f8_checks.py."""
+import ctypes
+
+import pytest
+import torch
+
+import moe_routed_expert_mx_amd as m
+from moe_routed_expert_mx_amd import block
+
+L, EINVAL = m._lib.lib, m._lib.MOE_EINVAL
+FAKE = ctypes.c_void_p(0x1000)
+BF, F32, F8, I32 = torch.bfloat16, torch.float32, torch.float8_e4m3fn, torch.int32
+
+
+def _z(*shape, dtype=F32):
+    return torch.zeros(*shape, dtype=dtype)
+
+
+def _experts(E=4, D=64, I=48, **k):
+    w13, s13 = block.f8_weight_blocks(torch.ones(E, 2 * I, D), halves=True)
+    w2, s2 = block.f8_weight_blocks(torch.ones(E, D, I))
+    return block.ExpertsF8(w13, s13, w2, s2, **{"topk": 2, "B_max": 4, "device": "cpu", **k})
+
+
+def _shared(D=64, I=48, **k):
+    w13, s13 = block.f8_weight_blocks(torch.ones(2 * I, D), halves=True)
+    w2, s2 = block.f8_weight_blocks(torch.ones(D, I))
+    return block.SharedExpertF8(w13, s13, w2, s2, **{"B_max": 4, "device": "cpu", **k})
+
+
+def test_exact_is_0_or_1():
+    for exact in (-1, 2):
+        o = m.moe_linear_opts_t(exact=exact)
+        assert L.moe_linear_f8(FAKE, 128, FAKE, 1, FAKE, 128, FAKE, 1, 8, 128, ctypes.byref(o), FAKE, 0, 8, None) == EINVAL
+        o = m.moe_grouped_opts_t(exact=exact)
+        assert L.moe_grouped_f8(FAKE, 128, FAKE, 1, 4, FAKE, 128, 8 * 128, FAKE, FAKE, 4, 2, 8, 128, ctypes.byref(o), FAKE, 0, 8, 4,
+                                None) == EINVAL
+
+
+def test_exact_reaches_both_ways_of_a_call(monkeypatch):
+    """The native binding takes it as its last argument, ctypes as a field of the options."""
+    seen = []
+    for name in ("linear_f8", "grouped_f8"):
+        monkeypatch.setattr(m._lib._dense, name, lambda *a: seen.append(a[-1]) or -100)
+    fields = {"moe_linear_f8": (m._lib._LINEAR_OPTS, 1), "moe_grouped_f8": (m._lib._GROUPED_OPTS, 3)}
+
+    def enqueue(name, fn, stream, tensors, *a):
+        opts, i = fields[name]
+        seen.append(opts.unpack(next(b for b in a if isinstance(b, bytes)))[i])
+
+    monkeypatch.setattr(m._lib, "_enqueue", enqueue)
+    q, s, o = _z(4, 256, dtype=F8), _z(4, 2), _z(3, dtype=I32)
+    for exact in (False, True):
+        m.moe_linear_f8(q, s, q, _z(1, 2), _z(4, 4), exact=exact)
+        m.moe_grouped_f8(q, s, q[None], _z(1, 1, 2), o[:2], _z(4, 4), exact=exact)
+        assert seen == [exact] * 4
+        seen.clear()
+
+
+@pytest.mark.parametrize("exact", [True, False])
+def test_first_product_of_the_experts_is_exact_unless_told(monkeypatch, exact):
+    """Its result is quantized again; the second one's is not."""
+    calls = []
+    for name in ("moe_quant_f8", "moe_lists", "moe_grouped_f8", "moe_linear_f8"):
+        monkeypatch.setattr(m._lib, name, lambda *a, **k: calls.append(k) if "act" in k or "scatter" in k or "add" in k else None)
+    opts = {} if exact else dict(exact=False)
+    _experts(**opts).forward(_z(3, 64, dtype=BF), _z(3, 2, dtype=I32))
+    _shared(**opts).forward(_z(3, 64, dtype=BF))
+    assert [bool(k.get("exact")) for k in calls] == [exact, False] * 2
