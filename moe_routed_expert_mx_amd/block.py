@@ -243,9 +243,10 @@ class ExpertsF8:
 
     def combine(self, rows: torch.Tensor, weights: torch.Tensor, y: torch.Tensor | None = None, *, stream=None):
         """Weighted top-k combine of the rows, as MoeLayer's."""
-        if y is None:
-            y = torch.empty(weights.shape[0], self.D, dtype=torch.bfloat16, device=self.device)
-        _lib.moe_combine(rows, weights, y, stream=stream)
+        with torch.cuda.device(self.device), _on(stream, self.device) as give:
+            if y is None:
+                y = give(torch.empty(weights.shape[0], self.D, dtype=torch.bfloat16, device=self.device))
+            _lib.moe_combine(rows, weights, y)
         return y
 
 

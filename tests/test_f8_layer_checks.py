@@ -1,5 +1,7 @@
 """Choices and refusals of the block-scaled FP8 layer that hold without a GPU, beside those of test_f8_checks.py."""
+import contextlib
 import ctypes
+import types
 
 import pytest
 import torch
@@ -67,3 +69,57 @@ def test_first_product_of_the_experts_is_exact_unless_told(monkeypatch, exact):
     _experts(**opts).forward(_z(3, 64, dtype=BF), _z(3, 2, dtype=I32))
     _shared(**opts).forward(_z(3, 64, dtype=BF))
     assert [bool(k.get("exact")) for k in calls] == [exact, False] * 2
+
+
+class _Streams:
+    """Stand-ins for the streams and devices: where tensors are allocated, library calls made and results recorded."""
+
+    def __init__(self, monkeypatch):
+        self.here, self.side = types.SimpleNamespace(name="here"), types.SimpleNamespace(name="side", cuda_stream=7, device_index=None)
+        self.current, self.device, self.allocated, self.calls, self.recorded = self.here, None, [], [], []
+        empty, streams = torch.empty, self
+
+        class Tensors(torch.Tensor):
+            def record_stream(self, s):
+                streams.recorded.append(s)
+
+        def allocate(*a, **k):
+            self.allocated.append(self.current)
+            return empty(*a, **k).as_subclass(Tensors)
+
+        @contextlib.contextmanager
+        def entered(name, value):
+            before = getattr(self, name)
+            setattr(self, name, value)
+            yield
+            setattr(self, name, before)
+
+        monkeypatch.setattr(torch, "empty", allocate)
+        monkeypatch.setattr(torch.cuda, "stream", lambda s: entered("current", s))
+        monkeypatch.setattr(torch.cuda, "current_stream", lambda *a: self.current)
+        monkeypatch.setattr(torch.cuda, "device", lambda d: entered("device", torch.device(d)))
+        monkeypatch.setattr(torch.cuda, "ExternalStream", lambda h, device=None: self.side if h == 7 else None)
+
+    def called(self, *a, stream=None, **k):
+        self.calls.append((self.device, self.current if stream is None else self.side if stream == 7 else stream))
+
+    def clear(self):
+        for record in (self.allocated, self.calls, self.recorded):
+            record.clear()
+
+
+@pytest.mark.parametrize("stream", [None, "side", 7])
+def test_combine_allocates_and_runs_on_its_stream(monkeypatch, stream):
+    """On `stream` and on the experts' GPU, whichever is current; what it returns is recorded on the caller's stream."""
+    ex = _experts()
+    s = _Streams(monkeypatch)
+    monkeypatch.setattr(m._lib, "moe_combine", s.called)
+    named = s.side if stream == "side" else stream
+    ran = s.here if stream is None else s.side
+    y = ex.combine(_z(6, 64, dtype=BF), _z(3, 2), stream=named)
+    assert y.shape == (3, 64) and s.allocated == [ran] and s.calls == [(ex.device, ran)]
+    assert s.recorded == ([] if stream is None else [s.here]) and s.current is s.here and s.device is None
+    s.clear()
+    mine = _z(3, 64, dtype=BF)
+    assert ex.combine(_z(6, 64, dtype=BF), _z(3, 2), mine, stream=named) is mine
+    assert s.allocated == [] and s.calls == [(ex.device, ran)]

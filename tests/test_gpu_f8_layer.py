@@ -1,0 +1,61 @@
+"""The block-scaled FP8 layer's parts on the GPU, beside test_gpu_f8.py: streams, long lists, the shared expert's numbers."""
+import numpy as np
+import pytest
+import torch
+
+import f8_ref as ref
+from helpers import log
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda"
+BF, F16, F32, F8, I32 = torch.bfloat16, torch.float16, torch.float32, torch.float8_e4m3fn, torch.int32
+
+
+@pytest.fixture(scope="module")
+def m():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    import moe_routed_expert_mx_amd as pkg
+    return pkg
+
+
+def _gen(seed):
+    return torch.Generator("cpu").manual_seed(seed)
+
+
+def _np(t):
+    return t.cpu().double().numpy()
+
+
+def _experts(g, E=12, topk=3, D=320, I=144, B_max=300):
+    from moe_routed_expert_mx_amd.block import ExpertsF8, f8_weight_blocks
+    w13, s13 = f8_weight_blocks(torch.randn(E, 2 * I, D, generator=g) / D ** 0.5, halves=True)
+    w2, s2 = f8_weight_blocks(torch.randn(E, D, I, generator=g) / I ** 0.5)
+    return ExpertsF8(w13, s13, w2, s2, topk=topk, B_max=B_max)
+
+
+def _ids(B, topk, E, g):
+    return torch.rand(B, E, generator=g).argsort(1)[:, :topk].to(I32).contiguous()
+
+
+@pytest.mark.parametrize("raw", [False, True])
+def test_combine_on_a_side_stream(m, raw):
+    """On a stream that lags behind: the rows it waits for, and no buffer that the current stream allocates meanwhile."""
+    log(f"combine on a side stream raw={raw}")
+    g = _gen(31)
+    ex = _experts(g, D=512)
+    x, ids, w = torch.randn(40, 512, generator=g).to(BF).to(DEV), _ids(40, 3, 12, g).to(DEV), torch.rand(40, 3, generator=g).to(DEV)
+    want = ex.combine(ex.forward(x, ids), w).clone()
+    rows, big = torch.zeros(120, 512, dtype=BF, device=DEV), torch.randn(4096, 4096, device=DEV)
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    with torch.cuda.stream(s):
+        for _ in range(8):
+            torch.mm(big, big)
+    ex.forward(x, ids, rows, stream=s)
+    y = ex.combine(rows, w, stream=s.cuda_stream if raw else s)
+    junk = [torch.zeros(40, 512, dtype=BF, device=DEV) for _ in range(3)]
+    torch.cuda.current_stream().wait_stream(s)
+    got = y.clone()
+    torch.cuda.synchronize()
+    assert torch.equal(got, want) and not any(j.any() for j in junk)
