@@ -17,35 +17,12 @@ stream: after the usual wait for `stream` it may be read there and dropped at an
 """
 from __future__ import annotations
 
-import contextlib
-
 import torch
 
 from . import _lib
-from .layer import MoeLayer
+from .layer import MoeLayer, _on
 
 _F8 = torch.float8_e4m3fn
-
-
-@contextlib.contextmanager
-def _on(stream, device):
-    """Work and allocate on `stream` of `device` (None: its current one); yields a function that hands tensors on to
-    the caller's stream."""
-    if stream is None:
-        yield lambda t: t
-        return
-    caller = torch.cuda.current_stream(device)
-    if not hasattr(stream, "cuda_stream"):
-        stream = torch.cuda.ExternalStream(int(stream), device=device)
-    elif stream.device_index != device.index:
-        raise ValueError("the stream belongs to another GPU than the tensors")
-
-    def give(t):
-        t.record_stream(caller)
-        return t
-
-    with torch.cuda.stream(stream):
-        yield give
 
 
 class Router:

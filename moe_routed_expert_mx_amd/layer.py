@@ -5,9 +5,12 @@
 plan buffer, and runs one decode step, either as one moe_decode_run launch (B <= 8: the
 experts kernel quantizes and routes the batch itself) or as the three ABI calls the
 runtime page's PersistentExperts.run makes: plan (MXFP8 of x), units (moe_group),
-experts.  torch only allocates memory and supplies the stream.
+experts.  torch only allocates memory and supplies the stream; a call with a `stream`
+allocates on it and records what it returns on the caller's current one.
 """
 from __future__ import annotations
+
+import contextlib
 
 import numpy as np
 import torch
@@ -18,6 +21,27 @@ from . import _lib
 def _dev(a, device, dtype=None):
     t = torch.as_tensor(a) if isinstance(a, np.ndarray) else a
     return t.to(device=device, dtype=dtype) if dtype is not None else t.to(device)
+
+
+@contextlib.contextmanager
+def _on(stream, device):
+    """Work and allocate on `stream` of `device` (None: its current one); yields a function that hands tensors on to
+    the caller's stream."""
+    if stream is None:
+        yield lambda t: t
+        return
+    caller = torch.cuda.current_stream(device)
+    if not hasattr(stream, "cuda_stream"):
+        stream = torch.cuda.ExternalStream(int(stream), device=device)
+    elif stream.device_index != device.index:
+        raise ValueError("the stream belongs to another GPU than the tensors")
+
+    def give(t):
+        t.record_stream(caller)
+        return t
+
+    with torch.cuda.stream(stream):
+        yield give
 
 
 class MoeLayer:
@@ -38,6 +62,7 @@ class MoeLayer:
         if ws_bytes == 0:
             raise ValueError("unsupported shape for the workspace")
         self.ws = torch.empty(ws_bytes, dtype=torch.uint8, device=self.device)
+        self.device = self.ws.device  # with its index: "cuda" would mean another GPU where another is current
         _lib.moe_workspace_init(self.ws)
         self.plan = torch.empty(_lib.moe_plan_bytes(self.B_max, self.D), dtype=torch.uint8, device=self.device)
         self.units = torch.empty(_lib.moe_units_bytes(self.B_max, self.topk, self.E), dtype=torch.uint8,
@@ -73,7 +98,8 @@ class MoeLayer:
         if path not in ("auto", "decode", "grouped"):
             raise ValueError(f"unknown path {path!r}")
         if out is None:
-            out = self.out_buffer(B)
+            with _on(stream, self.device) as give:
+                out = give(self.out_buffer(B))
         if path == "decode" or (path == "auto" and self.AUTO_DECODE and B <= self.DECODE_MAX):
             _lib.moe_decode_run(self.structs[replica], x, ids, self.ws, out, stream=stream, **opts)
             return out
@@ -113,7 +139,8 @@ class MoeLayer:
         into BF16 y [B, D]."""
         B = weights.shape[0]
         if y is None:
-            y = torch.empty(B, self.D, dtype=torch.bfloat16, device=self.device)
+            with _on(stream, self.device) as give:
+                y = give(torch.empty(B, self.D, dtype=torch.bfloat16, device=self.device))
         _lib.moe_combine(rows, weights, y, stream=stream)
         return y
 

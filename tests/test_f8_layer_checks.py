@@ -8,6 +8,7 @@ import torch
 
 import moe_routed_expert_mx_amd as m
 from moe_routed_expert_mx_amd import block
+from moe_routed_expert_mx_amd.layer import MoeLayer
 
 L, EINVAL = m._lib.lib, m._lib.MOE_EINVAL
 FAKE = ctypes.c_void_p(0x1000)
@@ -123,3 +124,23 @@ def test_combine_allocates_and_runs_on_its_stream(monkeypatch, stream):
     mine = _z(3, 64, dtype=BF)
     assert ex.combine(_z(6, 64, dtype=BF), _z(3, 2), mine, stream=named) is mine
     assert s.allocated == [] and s.calls == [(ex.device, ran)]
+
+
+@pytest.mark.parametrize("stream", [None, "side", 7])
+def test_fp4_layer_allocates_on_the_stream_it_runs_on(monkeypatch, stream):
+    layer = object.__new__(MoeLayer)
+    layer.E, layer.D, layer.I, layer.B_max, layer.topk, layer.device = 4, 64, 48, 8, 2, torch.device("cpu")
+    layer.structs, layer.ws, layer.plan, layer.units = [None], None, None, None
+    s = _Streams(monkeypatch)
+    for name in ("moe_decode_run", "moe_plan_group", "moe_experts_run", "moe_combine"):
+        monkeypatch.setattr(m._lib, name, s.called)
+    named = s.side if stream == "side" else stream
+    ran = s.here if stream is None else s.side
+    for path, calls in (("decode", 1), ("grouped", 2)):
+        rows = layer.forward(_z(3, 64, dtype=BF), _z(3, 2, dtype=I32), path=path, stream=named)
+        assert rows.shape == (6, 64) and s.allocated == [ran] and [c[1] for c in s.calls] == [ran] * calls
+        assert s.recorded == ([] if stream is None else [s.here]) and s.current is s.here
+        s.clear()
+    y = layer.combine(rows, _z(3, 2), stream=named)
+    assert y.shape == (3, 64) and s.allocated == [ran] and [c[1] for c in s.calls] == [ran]
+    assert s.recorded == ([] if stream is None else [s.here])
