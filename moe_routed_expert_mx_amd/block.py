@@ -158,8 +158,13 @@ class _CodesF8:
         self.scales = torch.empty(rows, (cols + 127) // 128, device=device)
 
     def of(self, x):
-        codes, scales = self.codes[:x.shape[0]], self.scales[:x.shape[0]]
-        _lib.moe_quant_f8(x, codes, scales)
+        n, most = x.shape[0], 1 << 22  # rows that moe_quant_f8 takes; the experts' routes may be more
+        codes, scales = self.codes[:n], self.scales[:n]
+        if n <= most:
+            _lib.moe_quant_f8(x, codes, scales)
+        else:
+            for i in range(0, n, most):
+                _lib.moe_quant_f8(x[i:i + most], codes[i:i + most], scales[i:i + most])
         return codes, scales
 
 
@@ -178,11 +183,14 @@ class ExpertsF8:
         self.B_max, self.topk, self.exact = int(B_max), int(topk), bool(exact)
         if self.D % 16 or self.I % 16 or not 1 <= self.E <= 1024 or self.topk < 1 or self.B_max < 1:
             raise ValueError("experts: D and I must be multiples of 16, E at most 1024")
+        R = self.B_max * self.topk
+        if max(self.D, self.I) > 65536 or R > 1 << 26 or R * max(2 * self.I, self.D) > 1 << 40 or self.B_max * self.D >= 1 << 31:
+            raise ValueError("experts: D and I up to 65536 and batches up to topk * B_max = 2^26 routes, 2^40 values of a product "
+                             "and B_max * D < 2^31 are taken")
         E, D, I, b = self.E, self.D, self.I, lambda n: (n + 127) // 128
         self.w13, self.s13 = _f8_weight(w13, s13, device, ((E, 2 * I, D), (E, 2 * b(I), b(D))), "experts: w13")
         self.w2, self.s2 = _f8_weight(w2, s2, device, ((E, D, I), (E, b(D), b(I))), "experts: w2")
         self.device = self.w2.device  # with its index: "cuda" would mean another GPU where another is current
-        R = self.B_max * self.topk
         self.x = _CodesF8(self.B_max, D, self.device)
         self.hidden = torch.empty(R, I, dtype=torch.bfloat16, device=self.device)
         self.h = _CodesF8(R, I, self.device)
@@ -238,6 +246,9 @@ class SharedExpertF8:
         self.B_max, self.exact = int(B_max), bool(exact)
         if self.D % 16 or self.I % 16 or self.B_max < 1:
             raise ValueError("shared expert: D and I must be multiples of 16")
+        if max(self.D, self.I) > 65536 or self.B_max > 1 << 22 or self.B_max * max(2 * self.I, self.D) > 1 << 34:
+            raise ValueError("shared expert: D and I up to 65536 and batches up to 2^22 tokens and 2^34 values of a product are "
+                             "taken")
         D, I, b = self.D, self.I, lambda n: (n + 127) // 128
         self.w13, self.s13 = _f8_weight(w13, s13, device, ((2 * I, D), (2 * b(I), b(D))), "shared expert: w13")
         self.w2, self.s2 = _f8_weight(w2, s2, device, ((D, I), (b(D), b(I))), "shared expert: w2")

@@ -144,3 +144,41 @@ def test_fp4_layer_allocates_on_the_stream_it_runs_on(monkeypatch, stream):
     y = layer.combine(rows, _z(3, 2), stream=named)
     assert y.shape == (3, 64) and s.allocated == [ran] and [c[1] for c in s.calls] == [ran]
     assert s.recorded == ([] if stream is None else [s.here])
+
+
+# --------------------------------------------------------------- sizes
+def test_experts_refuse_batches_that_a_step_would_refuse():
+    """When they are made, not between two launches: B_max * topk and B_max * D beyond what each step takes."""
+    meta = dict(device="meta", topk=2)
+    for I, D, k in ((48, 64, dict(topk=64, B_max=(1 << 20) + 1)),      # more routes than the lists take
+                    (48, 64, dict(B_max=(1 << 25) + 1)),               # (both: B_max * D = 2^31 too)
+                    (48, 8192, dict(B_max=1 << 18)),                   # rows gathered beyond 2^31
+                    (32768, 64, dict(B_max=1 << 24)),                  # the first product beyond 2^40
+                    (65552, 64, {}), (48, 65552, {})):
+        w13, w2 = torch.empty(1, 2 * I, D, dtype=F8, device="meta"), torch.empty(1, D, I, dtype=F8, device="meta")
+        b = lambda n: (n + 127) // 128
+        s13, s2 = torch.empty(1, 2 * b(I), b(D), device="meta"), torch.empty(1, b(D), b(I), device="meta")
+        with pytest.raises(ValueError, match="batch|65536"):
+            block.ExpertsF8(w13, s13, w2, s2, **{**meta, "B_max": 4, **k})
+    for I, D, B in ((48, 64, (1 << 22) + 1), (8192, 64, (1 << 20) + 1), (65552, 64, 4), (48, 65552, 4)):
+        w13, w2 = torch.empty(2 * I, D, dtype=F8, device="meta"), torch.empty(D, I, dtype=F8, device="meta")
+        with pytest.raises(ValueError, match="batch|65536"):
+            block.SharedExpertF8(w13, torch.empty(2 * b(I), b(D), device="meta"), w2, torch.empty(b(D), b(I), device="meta"),
+                                 B_max=B, device="meta")
+
+
+def test_rows_are_quantized_in_parts_that_the_library_takes(monkeypatch):
+    """A hidden of more than 2^22 rows (routes): in order, whole, no part longer."""
+    parts = []
+    monkeypatch.setattr(m._lib, "moe_quant_f8", lambda x, q, s: parts.append((x.storage_offset() // 16, len(x), q.storage_offset() // 16,
+                                                                              len(q), s.storage_offset(), len(s))))
+    buffers = block._CodesF8((1 << 23) + 5, 16, "meta")
+    for n in (1, 1 << 22, (1 << 22) + 1, (1 << 23) + 5):
+        parts.clear()
+        q, s = buffers.of(torch.empty(n, 16, dtype=BF, device="meta"))
+        assert len(q) == len(s) == n
+        at = 0
+        for p in parts:
+            assert p == (at, p[1]) * 3 and 1 <= p[1] <= 1 << 22
+            at += p[1]
+        assert at == n

@@ -59,3 +59,32 @@ def test_combine_on_a_side_stream(m, raw):
     got = y.clone()
     torch.cuda.synchronize()
     assert torch.equal(got, want) and not any(j.any() for j in junk)
+
+
+def _rows_from_end_to_end(ex, weights, x, ids, routes):
+    """The formula in 64 bits for some routes (float64)."""
+    w13, s13, w2, s2 = weights
+    want = np.empty((len(routes), ex.D))
+    for i, r in enumerate(routes):
+        e = int(ids.flatten()[r])
+        q, s = ref.quant(_np(x[r // ex.topk:r // ex.topk + 1]))
+        h, _ = ref.linear(q, s, _np(w13[e].float()), _np(s13[e]), act="swiglu")
+        hq, hs = ref.quant(torch.from_numpy(h).to(BF).double().numpy())
+        want[i] = ref.linear(hq, hs, _np(w2[e].float()), _np(s2[e]))[0]
+    return want
+
+
+def test_more_routes_than_one_quantization_takes(m):
+    """2^22 and some routes: the hidden is quantized in parts.  Bound: test_gpu_f8_sums.py, from end to end."""
+    from moe_routed_expert_mx_amd.block import ExpertsF8, f8_weight_blocks
+    B, D, I, E, topk = (1 << 21) + 37, 16, 32, 3, 2
+    log(f"{B * topk} routes")
+    g = _gen(5)
+    weights = (*f8_weight_blocks(torch.randn(E, 2 * I, D, generator=g) / 4, halves=True), *f8_weight_blocks(torch.randn(E, D, I, generator=g) / 5))
+    ex = ExpertsF8(*weights, topk=topk, B_max=B)
+    x, ids = torch.randn(B, D, generator=g).to(BF), torch.randint(0, E, (B, topk), generator=g, dtype=I32)
+    got = ex.forward(x.to(DEV), ids.to(DEV))
+    torch.cuda.synchronize()
+    routes = np.r_[0:20, (1 << 22) - 20:(1 << 22) + 20, B * topk - 20:B * topk, torch.randint(0, B * topk, (40,), generator=g).numpy()]
+    got, want = _np(got[torch.from_numpy(routes).to(DEV)]), _rows_from_end_to_end(ex, weights, x, ids, routes)
+    assert np.linalg.norm(got - want) <= (2.0 ** -8 / 3 ** 0.5 + 2 * 2.0 ** -7.5) * np.linalg.norm(want)
