@@ -88,3 +88,53 @@ def test_more_routes_than_one_quantization_takes(m):
     routes = np.r_[0:20, (1 << 22) - 20:(1 << 22) + 20, B * topk - 20:B * topk, torch.randint(0, B * topk, (40,), generator=g).numpy()]
     got, want = _np(got[torch.from_numpy(routes).to(DEV)]), _rows_from_end_to_end(ex, weights, x, ids, routes)
     assert np.linalg.norm(got - want) <= (2.0 ** -8 / 3 ** 0.5 + 2 * 2.0 ** -7.5) * np.linalg.norm(want)
+
+
+@pytest.mark.parametrize("B,K,E", [(200003, 16, 256), ((1 << 21) + 129, 1, 1000), (300001, 8, 1)])
+@pytest.mark.parametrize("kind", ["skewed", "foreign"])
+def test_lists_longer_than_a_waves_registers(m, B, K, E, kind):
+    """Beyond 2^21 routes a wave's share does not stay in registers: shares of 832, 576 and 640 routes."""
+    log(f"lists {B}x{K} of {E} {kind}")
+    g = _gen(B)
+    R = B * K
+    ids = torch.randint(0, E, (B, K), generator=g, dtype=I32) if kind == "skewed" else \
+        torch.randint(-E, 2 * E, (B, K), generator=g, dtype=I32)
+    if kind == "skewed":
+        ids = torch.where(torch.rand(B, K, generator=g) < 0.9, torch.full_like(ids, E // 2), ids)
+    offsets, pairs = torch.full((E + 2,), -9, dtype=I32, device=DEV), torch.full((R + 1,), -9, dtype=I32, device=DEV)
+    ws = torch.full((m.moe_lists_ws_bytes(R, E),), 0x5a, dtype=torch.uint8, device=DEV)
+    m.moe_lists(ids.to(DEV), offsets[:E + 1], pairs[:R], ws=ws)
+    torch.cuda.synchronize()
+    flat = ids.flatten().numpy().astype(np.int64)
+    flat = np.where((flat >= 0) & (flat < E), flat, E)
+    order, counts = np.argsort(flat, kind="stable"), np.bincount(flat, minlength=E + 1)
+    want = np.where(np.arange(R) < R - counts[E], order, -1)
+    assert offsets[E + 1] == -9 and pairs[R] == -9
+    assert np.array_equal(offsets[:E + 1].cpu().numpy(), np.r_[0, np.cumsum(counts[:E])])
+    assert np.array_equal(pairs[:R].cpu().numpy(), want)
+
+
+@pytest.mark.parametrize("B", [1, 13, 70, 520])
+@pytest.mark.parametrize("how", ["rows", "codes", "add", "add in place"])
+def test_shared_expert_against_the_plain_form(m, B, how):
+    """SharedExpertF8 stage by stage on the values that the GPU handed on."""
+    from moe_routed_expert_mx_amd.block import SharedExpertF8, f8_weight_blocks
+    log(f"shared expert B={B} {how}")
+    g = _gen(B)
+    D, I = 400, 272
+    w13, s13 = f8_weight_blocks(torch.randn(2 * I, D, generator=g) / 20, halves=True)
+    w2, s2 = f8_weight_blocks(torch.randn(D, I, generator=g) / 16)
+    shared = SharedExpertF8(w13, s13, w2, s2, B_max=600)
+    x, add = torch.randn(B, D, generator=g).to(BF), torch.randn(B, D, generator=g).to(BF)
+    q, s = ref.quant(_np(x))
+    given = (torch.from_numpy(q).float().to(F8).to(DEV), torch.from_numpy(s).float().to(DEV)) if how == "codes" else x.to(DEV)
+    d = add.to(DEV)
+    out = shared.forward(given, add=d if "add" in how else None, out=d if how == "add in place" else None)
+    torch.cuda.synchronize()
+    assert how != "add in place" or out is d
+    y, e = ref.linear(q, s, _np(w13.float()), _np(s13), act="swiglu", cut=False)
+    hidden = _np(shared.hidden[:B])
+    assert np.all(np.abs(hidden - y) <= e + 2.0 ** -8 * (np.abs(y) + e) * 1.001 + 2.0 ** -134)
+    hq, hs = ref.quant(hidden)
+    y, e = ref.linear(hq, hs, _np(w2.float()), _np(s2), add=_np(add) if "add" in how else None)
+    assert np.all(np.abs(_np(out) - y) <= e + 2.0 ** -8 * (np.abs(y) + e) * 1.001 + 2.0 ** -134)
