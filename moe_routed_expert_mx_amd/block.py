@@ -136,7 +136,10 @@ def f8_weight_blocks(w, *, halves: bool = False):
     *lead, N, K = w.shape
     nb, kb = (N + 127) // 128, (K + 127) // 128
     v = torch.nn.functional.pad(w.float(), (0, kb * 128 - K, 0, nb * 128 - N)).view(*lead, nb, 128, kb, 128)
-    scales = v.abs().amax((-3, -1)) / 448
+    amax = v.abs().amax((-3, -1))
+    scales = amax / 448
+    # among subnormals the quotient's rounding is coarse: up, or v / scale could pass 448
+    scales = torch.where((amax > 0) & (scales < 2.0 ** -126), torch.nextafter(scales, torch.full_like(scales, 1.0)), scales)
     v = v / torch.where(scales > 0, scales, 1.0)[..., :, None, :, None]
     return v.view(*lead, nb * 128, kb * 128)[..., :N, :K].to(_F8).contiguous(), scales.contiguous()
 

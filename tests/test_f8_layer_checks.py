@@ -182,3 +182,21 @@ def test_rows_are_quantized_in_parts_that_the_library_takes(monkeypatch):
             assert p == (at, p[1]) * 3 and 1 <= p[1] <= 1 << 22
             at += p[1]
         assert at == n
+
+
+# --------------------------------------------------------------- weights
+def test_weight_blocks_of_tiny_values():
+    """Scales that FP32 holds as subnormals: codes stay finite, values within half a code's step and half a scale's."""
+    unit = 2.0 ** -149
+    for top in (1, 2, 300, 448, 449, 628, 629, 700, 1000, 2000, 5000, 448 * 3 + 200, 448 * 1000):
+        w = torch.full((130, 144), float(top), dtype=torch.float64) * unit
+        w[:, ::3] *= -0.5
+        c, s = block.f8_weight_blocks(w.float())
+        assert torch.isfinite(c.float()).all() and torch.isfinite(s).all()
+        v = c.double() * s.double().repeat_interleave(128, 0)[:130].repeat_interleave(128, 1)[:, :144]
+        # half a step of e4m3 (of its smallest at least), and of the scale's own rounding up nothing: codes are of v / scale
+        assert ((v - w.float().double()).abs() <= 2.0 ** -4 * w.abs() + 2.0 ** -10 * s.double().max()).all(), top
+    w = torch.full((128, 128), 8.8e-43)
+    assert torch.isfinite(block.f8_weight_blocks(w)[0].float()).all()
+    w[0, 0], w[1, 1] = float("inf"), float("nan")
+    assert not torch.isfinite(block.f8_weight_blocks(w)[1]).any()
