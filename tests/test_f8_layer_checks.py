@@ -200,3 +200,25 @@ def test_weight_blocks_of_tiny_values():
     assert torch.isfinite(block.f8_weight_blocks(w)[0].float()).all()
     w[0, 0], w[1, 1] = float("inf"), float("nan")
     assert not torch.isfinite(block.f8_weight_blocks(w)[1]).any()
+
+
+# --------------------------------------------------------------- ids of another rank
+def test_rows_of_another_ranks_experts_are_zeros_in_a_new_buffer(monkeypatch):
+    """What no product writes is not left undefined: 0 times a NaN there would reach the combined output.  Buffers of the
+    caller are left as they were, and MoeBlock, whose router names experts of this layer only, does not pay for zeros."""
+    empty, zeros, filled = torch.empty, torch.zeros, []
+    monkeypatch.setattr(torch, "empty", lambda *a, **k: empty(*a, **k).fill_(float("nan")) if k.get("dtype") == BF else empty(*a, **k))
+    monkeypatch.setattr(torch, "zeros", lambda *a, **k: filled.append(a) or zeros(*a, **k))
+    for name in ("moe_quant_f8", "moe_lists", "moe_grouped_f8", "moe_combine"):
+        monkeypatch.setattr(m._lib, name, lambda *a, **k: None)
+    ex, ids = _experts(), torch.full((3, 2), -1, dtype=I32)
+    filled.clear()
+    x = empty(3, 64, dtype=BF)
+    out = ex.forward(x, ids)
+    assert out.shape == (6, 64) and out.dtype == BF and (out == 0).all() and len(filled) == 1
+    mine = torch.full((6, 64), 7.0, dtype=BF)
+    assert ex.forward(x, ids, mine) is mine and (mine == 7).all() and len(filled) == 1
+    router = types.SimpleNamespace(E=4, D=64, topk=2, forward=lambda x: (ids, empty(3, 2)))
+    monkeypatch.setattr(torch.cuda, "device", lambda d: contextlib.nullcontext())
+    block.MoeBlock(router, ex).forward(x)
+    assert len(filled) == 1

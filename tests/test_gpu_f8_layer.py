@@ -138,3 +138,28 @@ def test_shared_expert_against_the_plain_form(m, B, how):
     hq, hs = ref.quant(hidden)
     y, e = ref.linear(hq, hs, _np(w2.float()), _np(s2), add=_np(add) if "add" in how else None)
     assert np.all(np.abs(_np(out) - y) <= e + 2.0 ** -8 * (np.abs(y) + e) * 1.001 + 2.0 ** -134)
+
+
+def test_a_ranks_part_of_the_layer(m):
+    """Ids of another rank from experts to the combined output, on memory that held NaN: the parts of two ranks add up."""
+    log("two ranks' parts")
+    from moe_routed_expert_mx_amd.block import ExpertsF8
+    g = _gen(41)
+    B, E, topk, D, I = 70, 12, 3, 320, 144
+    whole = _experts(g, E, topk, D, I)
+    halves = [ExpertsF8(*(t[h * 6:h * 6 + 6] for t in (whole.w13, whole.s13, whole.w2, whole.s2)), topk=topk, B_max=300) for h in range(2)]
+    x, ids, w = torch.randn(B, D, generator=g).to(BF).to(DEV), _ids(B, topk, E, g).to(DEV), torch.rand(B, topk, generator=g).to(DEV)
+    rows = whole.forward(x, ids)
+    parts = []
+    for h, ex in enumerate(halves):
+        junk = torch.full((B * topk, D), float("nan"), dtype=BF, device=DEV)
+        torch.cuda.synchronize()
+        del junk                                        # the next buffer of its size
+        part = ex.forward(x, ids - 6 * h)
+        here = ((ids // 6) == h).flatten()
+        assert torch.equal(part[here], rows[here]) and (part[~here] == 0).all()
+        parts.append(ex.combine(part, w))
+    got, want = _np(parts[0]) + _np(parts[1]), np.einsum("bkd,bk->bd", _np(rows).reshape(B, topk, D), _np(w))
+    assert np.isfinite(got).all()
+    # each part is rounded to BF16 once; a bound by magnitudes for both
+    assert np.all(np.abs(got - want) <= 2.0 ** -8 * 1.01 * np.einsum("bkd,bk->bd", np.abs(_np(rows)).reshape(B, topk, D), _np(w)))
