@@ -219,6 +219,8 @@ class ExpertsF8:
         if path != "auto":
             raise ValueError(f"unknown path {path!r}")
         R = B * self.topk
+        if out is not None and (out.dim() != 2 or out.shape[0] < R or out.shape[1] != self.D):
+            raise ValueError(f"out: expected [{R}, {self.D}], got {list(out.shape)}")
         with _on(stream, self.device) as give:
             if out is None:
                 out = give(torch.zeros(R, self.D, dtype=torch.bfloat16, device=self.device))

@@ -222,3 +222,17 @@ def test_rows_of_another_ranks_experts_are_zeros_in_a_new_buffer(monkeypatch):
     monkeypatch.setattr(torch.cuda, "device", lambda d: contextlib.nullcontext())
     block.MoeBlock(router, ex).forward(x)
     assert len(filled) == 1
+
+
+def test_experts_refuse_an_output_of_too_few_rows(monkeypatch):
+    """Routes behind its last row would be dropped without a word."""
+    made = []
+    for name in ("moe_quant_f8", "moe_lists", "moe_grouped_f8"):
+        monkeypatch.setattr(m._lib, name, lambda *a, **k: made.append(a))
+    ex, x, ids = _experts(), _z(3, 64, dtype=BF), _z(3, 2, dtype=I32)
+    for bad in (_z(5, 64, dtype=BF), _z(6, 63, dtype=BF), _z(3, 2, 64, dtype=BF)):
+        with pytest.raises(ValueError, match="out"):
+            ex.forward(x, ids, bad)
+    assert made == []
+    for fine in (_z(6, 64, dtype=BF), _z(9, 64)):
+        assert ex.forward(x, ids, fine) is fine
