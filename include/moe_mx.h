@@ -459,7 +459,7 @@ int moe_linear_i8(const int8_t* a_dev, int64_t lda, const float* a_scales_dev, c
  * 2^-e <= 448 (as the MXFP8 plan's); code = e4m3 of x * 2^-e, which is exact, half to even.  A
  * block of zeros has scale 0; one with an infinity or NaN scale NaN and codes 0, so that
  * what is computed from it is NaN.  Bytes of codes_dev between K and ldc are left as they were.
- * 1 <= K <= 131072. */
+ * 1 <= M <= 2^22, 1 <= K <= 131072, M * ceil(K / 512) < 2^27; MOE_EINVAL otherwise. */
 int moe_quant_f8(const void* x_dev, int32_t type, int64_t ldx, int32_t M, int32_t K, uint8_t* codes_dev,
                  int64_t ldc, float* scales_dev, int64_t lds, void* stream);
 
@@ -491,7 +491,7 @@ typedef struct {
  *   y = (h * r) * weight, in FP32;   out = y rounded to x's type;
  *   codes and scales of y: as moe_quant_i8 makes them of an FP32 row, or as moe_quant_f8 does.
  * x_dev [M, K] (moe_dtype, ldx >= K); weight_dev [K] of wtype, MOE_F32 or x's type.  One of out
- * and codes at least.  1 <= K <= 16384, eps >= 0 and finite; MOE_EINVAL otherwise. */
+ * and codes at least.  1 <= M <= 2^22, 1 <= K <= 16384, eps >= 0 and finite; MOE_EINVAL otherwise. */
 int moe_rms_norm(const void* x_dev, int32_t type, int64_t ldx, int32_t M, int32_t K, const void* weight_dev,
                  int32_t wtype, const moe_norm_opts_t* opts, void* stream);
 
@@ -507,7 +507,7 @@ int moe_rms_norm(const void* x_dev, int32_t type, int64_t ldx, int32_t M, int32_
  * [NB, KB], contiguous: NB = ceil(N / 128), with act 1 NB = 2 ceil(N/2 / 128), as the gate rows (0 ..
  * N/2 - 1) and the up rows have blocks of their own.  out_dev [M, N or N/2] of out_type (ldo).
  * opts as moe_linear_i8's.  16-byte alignment of a_dev, w_dev, lda and ldw, K % 16 == 0.
- * 1 <= N <= 2^20, M * N <= 2^34, 16 <= K <= 65536, lda and ldw < 2^22, ldsa < 2^20;
+ * 1 <= M <= 2^22, 1 <= N <= 2^20, M * N <= 2^34, 16 <= K <= 65536, lda and ldw < 2^22, ldsa < 2^20;
  * MOE_EINVAL otherwise. */
 int moe_linear_f8(const uint8_t* a_dev, int64_t lda, const float* a_scales_dev, int64_t ldsa, const uint8_t* w_dev,
                   int64_t ldw, const float* w_scales_dev, int32_t M, int32_t N, int32_t K,

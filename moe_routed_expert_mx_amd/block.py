@@ -161,7 +161,8 @@ class _CodesF8:
         self.scales = torch.empty(rows, (cols + 127) // 128, device=device)
 
     def of(self, x):
-        n, most = x.shape[0], 1 << 22  # rows that moe_quant_f8 takes; the experts' routes may be more
+        # rows that moe_quant_f8 takes; the experts' routes may be more
+        n, most = x.shape[0], min(1 << 22, ((1 << 27) - 1) // ((self.codes.shape[1] + 511) // 512))
         codes, scales = self.codes[:n], self.scales[:n]
         if n <= most:
             _lib.moe_quant_f8(x, codes, scales)

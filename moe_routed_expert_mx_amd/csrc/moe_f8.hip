@@ -747,7 +747,7 @@ int launch_stream(const F8Args& a, hipStream_t st) {
   constexpr int BM = 16 * TT;
   // grouped: the experts' last runs may be short
   const int64_t units = GROUPED ? (a.M + static_cast<int64_t>(std::min(a.E, a.M)) * (BM - 1)) / BM : (a.M + BM - 1) / BM;
-  if (nx * units > 0x7fffffff) return MOE_EINVAL;
+  if (nx * units * (64 * WV) >> 32) return MOE_EINVAL;  // (threads of a launch)
   return launch(f8_stream_kernel<OUT, SWIGLU, GROUPED, EXACT, RT, TT, WV, WK>, static_cast<uint32_t>(nx * units), 64 * WV, lds, st, a,
                 static_cast<uint32_t>(nx));
 }
@@ -762,8 +762,9 @@ int launch_tile(const F8Args& a, hipStream_t st) {
   const size_t lds = fixed + NB * static_cast<size_t>((a.K + 8191) / 8192 * 64) * 4;
   const int64_t bn = SWIGLU ? BN / 2 : BN, nn = ((SWIGLU ? a.N / 2 : a.N) + bn - 1) / bn;
   const int64_t nm = GROUPED ? (a.M + static_cast<int64_t>(std::min(a.E, a.M)) * (BM - 1)) / BM : (a.M + BM - 1) / BM;
-  if (nm * nn > 0x7ffffff0) return MOE_EINVAL;
-  const uint32_t per = static_cast<uint32_t>((nm * nn + 7) / 8);
+  const int64_t groups = (nm * nn + 7) / 8 * 8;
+  if (groups * (64 * WM * WN) >> 32) return MOE_EINVAL;  // (threads of a launch)
+  const uint32_t per = static_cast<uint32_t>(groups / 8);
   return launch(f8_tile_kernel<BM, BN, WM, WN, NS, OUT, SWIGLU, GROUPED, EXACT>, per * 8, 64 * WM * WN, lds, st, a, static_cast<uint32_t>(nm),
                 static_cast<uint32_t>(nn), per);
 }

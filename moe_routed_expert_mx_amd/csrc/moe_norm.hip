@@ -347,7 +347,7 @@ extern "C" {
 int moe_quant_f8(const void* x, int32_t type, int64_t ldx, int32_t M, int32_t K, uint8_t* codes, int64_t ldc,
                  float* scales, int64_t lds, void* stream) {
   if (!x || !codes || !scales || !type_ok(type) || M < 1 || M > kMaxRows || K < 1 || K > 131072 || ldx < K || ldc < K ||
-      lds < (K + 127) / 128)
+      lds < (K + 127) / 128 || static_cast<int64_t>(M) * ((K + 511) / 512) >= 1 << 27)  // (2^32 threads)
     return MOE_EINVAL;
   hipStream_t st = as_stream(stream);
   if (type == MOE_F32) return launch_quant_f8<MOE_F32>(x, ldx, M, K, codes, ldc, scales, lds, st);

@@ -236,3 +236,9 @@ def test_experts_refuse_an_output_of_too_few_rows(monkeypatch):
     assert made == []
     for fine in (_z(6, 64, dtype=BF), _z(9, 64)):
         assert ex.forward(x, ids, fine) is fine
+
+
+def test_grids_beyond_the_launch_limit_are_refused():
+    """2^32 threads: an error of the arguments, not of the launch."""
+    for M, K in ((1 << 22, 16384), (1 << 22, 131072), (1 << 19, 131072)):
+        assert L.moe_quant_f8(FAKE, 0, K, M, K, FAKE, K, FAKE, K // 128, None) == EINVAL
