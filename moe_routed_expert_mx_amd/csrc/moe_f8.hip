@@ -786,8 +786,10 @@ int launch_product(const F8Args& a, hipStream_t st) {
   // 27, 41 and 29; of 50 tokens 115 and 49, 79 and 47.
   if (shallow && rows <= 4 && met * (a.N / 32) >= 1024) return launch_stream<OUT, SWIGLU, GROUPED, EXACT, 2, 1, 4, 1>(a, st);
   if (rows <= 64 && n0 < 256) {
-    if (rows <= 16) return GROUPED ? launch_stream<OUT, SWIGLU, GROUPED, EXACT, 2, 1, 8, 4>(a, st)
-                                   : launch_stream<OUT, SWIGLU, GROUPED, EXACT, R1, 1, SWIGLU && EXACT ? 8 : 16>(a, st);
+    if (rows <= 16) {
+      if constexpr (GROUPED) return launch_stream<OUT, SWIGLU, true, EXACT, 2, 1, 8, 4>(a, st);
+      else return launch_stream<OUT, SWIGLU, false, EXACT, R1, 1, SWIGLU && EXACT ? 8 : 16>(a, st);
+    }
     if constexpr (!EXACT)  // (four row tiles of BF16 operands do not fit the registers)
       if (rows > 32) return launch_stream<OUT, SWIGLU, GROUPED, false, 2, 4, 8>(a, st);
     return launch_stream<OUT, SWIGLU, GROUPED, EXACT, R1, 2, 8>(a, st);
