@@ -179,7 +179,7 @@ class ExpertsF8:
         """w13 float8_e4m3fn [E, 2I, D] (gate rows, then up rows) with FP32 scales [E, 2 ceil(I / 128), ceil(D / 128)],
         w2 [E, D, I] with [E, ceil(D / 128), ceil(I / 128)]; D and I multiples of 16.  f8_weight_blocks makes them of
         other weights.  exact: the first product's sums, as moe_linear_f8's; its result is quantized again, so that
-        without it the rows' error grows by a fifth, while a prompt takes a quarter less time."""
+        without it the rows' error grows by a fifth, while a prompt takes a fifth less time."""
         w2 = torch.as_tensor(w2)
         if w2.dim() != 3:
             raise ValueError("experts: w2: expected [E, D, I]")

@@ -313,7 +313,7 @@ struct Operand<true> {
 // through LDS of its own; a block's sum is scaled and added in FP32.
 // Lane l's operand holds parts l / 16 and 4 + l / 16 of its row's eight: any order of k within the block
 // will do that both sides have, and this one meets all banks of LDS.  The 16 experts of one token (gate and up rows of 384
-// x 3584, 44 MB) take 13 us, 3.4 TB/s, their second product 6 us (22 MB).
+// x 3584, 44 MB) take 14 us, 3.1 TB/s, exact sums or not, their second product 8 us (22 MB).
 template <int OUT, bool SWIGLU, bool GROUPED, bool EXACT, int RT, int TT, int WV, int WK>
 __global__ __launch_bounds__(64 * WV) void f8_stream_kernel(F8Args a, uint32_t nx) {
   extern __shared__ __attribute__((aligned(16))) unsigned char smem[];
@@ -795,7 +795,8 @@ int launch_product(const F8Args& a, hipStream_t st) {
     return launch_stream<OUT, SWIGLU, GROUPED, EXACT, R1, 2, 8>(a, st);
   }
   // Rounds of tiles over 256 CUs, weighed with a round's time at K = 4096 (us): large tiles move fewer bytes for each
-  // product, small ones fill the CUs.  Two or three of the smallest fit a CU.  Exact sums take some 1.56 times as long with
+  // product, small ones fill the CUs.  The order holds for short K too (experts' second product, K = 384, 16 a token, with
+  // 64 x 128, 128 x 128, 128 x 256, 256 x 256, us: 512 tokens 74, 114, 88, 99; 2048 232, 236, 182, 159; 8192 745, 748, 629, 555).  Two or three of the smallest fit a CU.  Exact sums take some 1.56 times as long with
   // each of the first three (8192 x 7168 x 3584, SwiGLU: 365 to 376 us, against 217 with tiles of 256 x 256, whose BF16
   // operands do not fit the registers; 128 x 128 454).
   const int64_t c0 = n0 <= 256 ? 20 : (n0 + 511) / 512 * 25, c1 = (tiles(128, 128) + 255) / 256 * 24,

@@ -63,7 +63,8 @@ __device__ __forceinline__ float codes_e4m3(const float (&v)[VE], uint32_t (&c)[
 
 // ------------------------------------------------------------- blocks of e4m3
 // 16 lanes a block, four blocks a wave at once; a wave takes P runs of four blocks, all loaded before
-// the first is used.  Bytes bound it: 16384 x 4096 BF16, 203 MB, 41.6 us, 4.9 TB/s (a copy 5.15).
+// the first is used.  Bytes bound it: 16384 x 4096 BF16, 203 MB, 41.6 us, 4.9 TB/s (a copy 5.15).  Rows of less than 512
+// leave lanes idle: 65536 x 128 13.1 us, 1.9 TB/s, 65536 x 384 18.8, 4.1.
 template <int TYPE, int P>
 __global__ __launch_bounds__(256) void quant_f8_kernel(const void* x, int64_t ldx, int32_t M, int32_t K, uint8_t* codes,
                                                        int64_t ldc, float* scales, int64_t lds, uint32_t runs) {
@@ -163,7 +164,7 @@ struct Piece {
 
 // W waves a row, which they hold in registers, in its own type: NV pieces of 8 elements a lane.  One pass over
 // the data; bytes bound it: 16384 x 3584 BF16 with residual, total, out and e4m3 codes, 530 MB, 98 us, 5.4 TB/s (a copy
-// 5.15; held as FP32 instead it took 177 us).  The sum of squares is FP64 (two instructions an element, hidden behind the
+// 5.15; half of the input came from the memory-side cache; held as FP32 instead it took 177 us).  The sum of squares is FP64 (two instructions an element, hidden behind the
 // loads), so that r, and with it every code, is the same however the sum is cut.
 template <int TYPE, int WTYPE, int W, int NV>
 __global__ __launch_bounds__(256) void norm_kernel(NormArgs a) {
