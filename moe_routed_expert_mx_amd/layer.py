@@ -32,7 +32,8 @@ def _on(stream, device):
         return
     caller = torch.cuda.current_stream(device)
     if not hasattr(stream, "cuda_stream"):
-        stream = torch.cuda.ExternalStream(int(stream), device=device)
+        handle = int(stream)  # (0, the default stream, would be no external one to torch, which hands out another)
+        stream = torch.cuda.ExternalStream(handle, device=device) if handle else torch.cuda.default_stream(device)
     elif stream.device_index != device.index:
         raise ValueError("the stream belongs to another GPU than the tensors")
 

@@ -242,3 +242,21 @@ def test_grids_beyond_the_launch_limit_are_refused():
     """2^32 threads: an error of the arguments, not of the launch."""
     for M, K in ((1 << 22, 16384), (1 << 22, 131072), (1 << 19, 131072)):
         assert L.moe_quant_f8(FAKE, 0, K, M, K, FAKE, K, FAKE, K // 128, None) == EINVAL
+
+
+@pytest.mark.parametrize("handle", [0, 7])
+def test_raw_handle_of_the_default_stream(monkeypatch, handle):
+    """0 names the default stream of the tensors' GPU (what the default stream's cuda_stream is); torch takes an external
+    handle of 0 for none and hands out a stream of its own."""
+    ex, layer = _experts(), object.__new__(MoeLayer)
+    layer.E, layer.D, layer.B_max, layer.topk, layer.device = 4, 64, 8, 2, torch.device("cpu")
+    s = _Streams(monkeypatch)
+    default = types.SimpleNamespace(name="default")
+    monkeypatch.setattr(torch.cuda, "default_stream", lambda device=None: default)
+    monkeypatch.setattr(m._lib, "moe_combine", lambda *a, stream=None: s.calls.append(s.current if stream is None else stream))
+    ran = s.side if handle else default
+    ex.combine(_z(6, 64, dtype=BF), _z(3, 2), stream=handle)
+    assert s.allocated == [ran] and s.calls == [ran] and s.recorded == [s.here]
+    s.clear()
+    layer.combine(_z(6, 64, dtype=BF), _z(3, 2), stream=handle)
+    assert s.allocated == [ran] and s.recorded == [s.here]

@@ -166,3 +166,36 @@ def test_a_ranks_part_of_the_layer(m):
     got, want = _np(parts[0]) + _np(parts[1]), np.einsum("bkd,bk->bd", sums.reshape(B, topk, D), _np(w))
     # each part is rounded to BF16 once; a bound by magnitudes for both
     assert np.all(np.abs(got - want) <= 2.0 ** -8 * 1.01 * np.einsum("bkd,bk->bd", np.abs(sums).reshape(B, topk, D), _np(w)))
+
+
+def test_objects_on_the_default_stream_by_its_handle(m):
+    """stream=0 from another current stream: behind what the default stream, which lags, still has to do."""
+    log("objects on stream 0")
+    from moe_routed_expert_mx_amd.block import MoeBlock, Norm, Router, SharedExpertI8
+    g = _gen(51)
+    B, D, E, topk = 40, 512, 12, 3
+    ex, router = _experts(g, E, topk, D), Router(torch.randn(E, D, generator=g) / 22, topk=topk, B_max=B)
+    shared = SharedExpertI8.quantize(torch.randn(128, D, generator=g), torch.randn(D, 64, generator=g), B_max=B)
+    block = MoeBlock(router, ex, shared, Norm(torch.ones(D)))
+    x = torch.randn(B, D, generator=g).to(BF).to(DEV)
+    ids, w = router.forward(x)
+    rows = ex.forward(x, ids)
+    calls = [lambda x, **k: router.forward(x, **k)[1], shared.forward, block.norm.forward, lambda x, **k: ex.forward(x, ids, **k), block.forward,
+             lambda x, **k: ex.combine(ex.forward(x, ids, **k), w, **k)]
+    want = [c(x).clone() for c in calls]
+    default, side, big = torch.cuda.default_stream(), torch.cuda.Stream(), torch.randn(4096, 4096, device=DEV)
+    assert default.cuda_stream == 0
+    late = [torch.zeros_like(x) for _ in calls]
+    torch.cuda.synchronize()
+    for call, v, t in zip(calls, want, late):
+        with torch.cuda.stream(default):
+            for _ in range(8):
+                torch.mm(big, big)
+            t.copy_(x)
+        with torch.cuda.stream(side):
+            y = call(t, stream=0)
+            side.wait_stream(default)
+            got = y.clone()
+        torch.cuda.synchronize()
+        assert torch.equal(got, v)
+    assert rows.shape == (B * topk, D)
